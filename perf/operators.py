@@ -1,0 +1,502 @@
+"""The attention operators' work cases: inputs, plain forms, exact values and costs.
+
+Five kinds of call: "rotate" (multi-axis rotary positions on queries and keys),
+"norm_rotate" (RMS norm of each query and key head with the rotation in the
+same pass), both with their backward pass where "train" is set, "attention"
+(packed sequences, causal or full, grouped heads, with its backward pass where
+"train" is set) and "decode" (a few new tokens of every sequence against a
+partly used key/value cache).
+
+`own` false: elementary torch operations; `own` true: the framework's calls.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+SIZE = {"f32": 4, "f16": 2, "bf16": 2}
+EPS = 1e-6
+
+
+def _ints(text):
+    return [int(v) for v in text.split(",")]
+
+
+# ------------------------------------------------------------------ the cases
+
+def _rot(name, op, dtype, tokens, hq, hk, dim, axes, far=0, train=False, adjacent=False,
+         round_robin=False, per_axis=False, base=10000.0):
+    c = dict(op=op, dtype=dtype, tokens=tokens, q_heads=hq, k_heads=hk, dim=dim, axes=axes, far=far,
+             train=train, adjacent=adjacent, round_robin=round_robin, per_axis=per_axis, base=base)
+    return dict(c, name=name) if name else c
+
+
+def _att(name, dtype, q_lens, k_lens, hq, hk, dim, causal, train):
+    c = dict(op="attention", dtype=dtype, q_lens=q_lens, k_lens=k_lens, q_heads=hq, k_heads=hk,
+             dim=dim, causal=causal, train=train)
+    return dict(c, name=name) if name else c
+
+
+def _dec(name, dtype, lens, size, new, hq, hk, dim):
+    c = dict(op="decode", dtype=dtype, lens=lens, size=size, new=new, q_heads=hq, k_heads=hk, dim=dim)
+    return dict(c, name=name) if name else c
+
+
+def listed():
+    return [
+        # one step of 16 streams, far into a long recording: latency
+        _rot("rotate step bf16", "rotate", "bf16", 16, 16, 4, 128, "16,24,24", far=1000000),
+        # the maps of four images of different sizes (40x40, 24x24, 7x5, 1x1), rows and columns with a
+        # spectrum each, in training at full precision
+        _rot("rotate maps f32", "rotate", "f32", 2212, 8, 8, 64, "16,16", train=True, adjacent=True,
+             per_axis=True, base=100.0),
+        # two frames of a 160x160 map and a closing token, axes dealt in turn
+        _rot("rotate video bf16", "rotate", "bf16", 51201, 16, 4, 128, "16,24,24", round_robin=True),
+        # one step of a serving batch of 48
+        _rot("norm rotate step f16", "norm_rotate", "f16", 48, 32, 8, 128, "64", far=30000),
+        # a long prompt behind the projection of queries, keys and values
+        _rot("norm rotate prompt bf16", "norm_rotate", "bf16", 16000, 32, 8, 128, "16,24,24",
+             base=1000000.0),
+        # a training step over an odd number of tokens, a quarter of each head left unturned
+        _rot("norm rotate train bf16", "norm_rotate", "bf16", 8193, 16, 4, 96, "12,12,12", train=True),
+        # feature maps of different sizes attended in full, with an empty and a one-token sequence
+        _att("attend maps f16", "f16", "1600,400,1024,100,1,0,77", "", 8, 8, 64, False, False),
+        # a batch of prompts of very different lengths
+        _att("attend prompt bf16", "bf16", "4096,1,1337,2048,700,9", "", 32, 8, 128, True, False),
+        # a training step over packed sequences
+        _att("attend train bf16", "bf16", "2048,1023,1,512,600", "", 16, 4, 128, True, True),
+        # a training step at full precision with a head size between the usual ones; queries of
+        # another length than their keys
+        _att("attend train f32", "f32", "400,257,64", "300,257,200", 8, 8, 80, False, True),
+        # one new token after a prompt of one user: latency
+        _dec("decode step bf16", "bf16", "4097", 8192, 1, 32, 8, 128),
+        # a serving batch of 48 with between 1 and 16384 tokens in its caches
+        _dec("decode batch bf16", "bf16",
+             ",".join(str(1 + (i * 6151 + 11) % 16384) for i in range(48)), 16384, 1, 32, 8, 128),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _heads(rng, most):
+    hk = rng.choice([1, 2, 4, 8])
+    g = rng.choice([1, 2, 3, 4, 7, 8])
+    while hk * g > most:
+        g = max(1, g // 2)
+        hk = hk if g > 1 else min(hk, most)
+    return hk * g, hk
+
+
+def _lens(rng, total, parts):
+    cuts = sorted(rng.randint(0, total) for _ in range(parts - 1))
+    return [b - a for a, b in zip([0] + cuts, cuts + [total])]
+
+
+def draw(rng):
+    op = rng.choice(["rotate", "norm_rotate", "attention", "attention", "decode"])
+    dtype = rng.choice(["f32", "f16", "bf16", "bf16"])
+    if op in ("rotate", "norm_rotate"):
+        dim = rng.choice([32, 64, 80, 96, 128, 256])
+        hq, hk = _heads(rng, 32)
+        train = rng.random() < 0.5
+        most = 60000000 // ((hq + hk) * dim * (2 if train else 1))
+        tokens = _log_int(rng, 1, max(1, most))
+        n = rng.choice([1, 2, 3])
+        pairs = rng.choice([dim // 2, dim // 2, dim // 4])
+        cuts = [pairs // n] * (n - 1)
+        axes = ",".join(str(v) for v in [pairs - sum(cuts)] + cuts)
+        return _rot(None, op, dtype, tokens, hq, hk, dim, axes, far=rng.choice([0, 0, 5000, 1000000]),
+                    train=train, adjacent=rng.random() < 0.5, round_robin=rng.random() < 0.5,
+                    per_axis=rng.random() < 0.5, base=rng.choice([100.0, 10000.0, 1000000.0]))
+    if op == "attention":
+        dim = rng.choice([32, 64, 64, 80, 96, 128, 128])
+        train = rng.random() < 0.5
+        hq, hk = _heads(rng, 16 if train else 32)
+        total = _log_int(rng, 1, (1500 if train else 3000) if dtype == "f32" else (4000 if train else 7000))
+        q = _lens(rng, total, rng.randint(1, 8))
+        k = ""
+        if rng.random() < 0.4:                        # queries that follow on earlier tokens, or fewer keys
+            k = ",".join(str(max(0, v + rng.randint(-20, 300))) for v in q)
+        return _att(None, dtype, ",".join(map(str, q)), k, hq, hk, dim, rng.random() < 0.6, train)
+    dim = rng.choice([64, 96, 128, 128])
+    hq, hk = _heads(rng, 32)
+    count = _log_int(rng, 1, 64)
+    size = _log_int(rng, 16, max(16, min(32768, 500000000 // (count * hk * dim * SIZE[dtype]))))
+    new = rng.choice([1, 1, 1, 2, 5])
+    lens = ",".join(str(rng.randint(min(new, size), size)) for _ in range(count))
+    return _dec(None, dtype, lens, size, min(new, size), hq, hk, dim)
+
+
+# ------------------------------------------------------------------ inputs
+
+def _normal(gen, shape, dtype, scale=1.0):
+    return (torch.randn(shape, generator=gen, device="cuda", dtype=torch.float32) * scale).to(dtype)
+
+
+def _cu(lens):
+    c = [0]
+    for v in lens:
+        c.append(c[-1] + v)
+    return torch.tensor(c, dtype=torch.int32).cuda()
+
+
+def _handles(case):
+    from modulated_deformable_convolution_amd import attention
+    if case["op"] in ("rotate", "norm_rotate"):
+        return attention.mdcn_rotary_create(
+            case["dim"], _ints(case["axes"]), base=case["base"], adjacent=case["adjacent"],
+            round_robin=case["round_robin"], per_axis=case["per_axis"])
+    causal = True if case["op"] == "decode" else case["causal"]
+    return attention.mdcn_attention_create(case["q_heads"], case["k_heads"], case["dim"], causal)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = DTYPES[case["dtype"]]
+    hq, hk, d = case["q_heads"], case["k_heads"], case["dim"]
+    s = dict(case=case)
+    if case["op"] in ("rotate", "norm_rotate"):
+        t = case["tokens"]
+        # queries and keys lie in the output of one projection, as slices of its rows
+        qkv = _normal(gen, (t, hq + 2 * hk, d), dt)
+        s["q"], s["k"] = qkv[:, :hq], qkv[:, hq:hq + hk]
+        n = len(_ints(case["axes"]))
+        step = torch.arange(t, device="cuda", dtype=torch.int64)
+        rows = [step + case["far"], step // 40 % 40, step % 40][:n]
+        shift = torch.randint(0, 64, (n, 1), generator=gen, device="cuda")
+        s["positions"] = (torch.stack(rows) + shift).to(torch.int32)
+        if case["op"] == "norm_rotate":
+            s["q_gain"] = _normal(gen, (d,), torch.float32, 0.2).add_(1).to(dt)
+            s["k_gain"] = _normal(gen, (d,), torch.float32, 0.2).add_(1).to(dt)
+        if case["train"]:
+            s["gq"], s["gk"] = _normal(gen, (t, hq, d), dt), _normal(gen, (t, hk, d), dt)
+    elif case["op"] == "attention":
+        ql = _ints(case["q_lens"])
+        kl = _ints(case["k_lens"]) if case["k_lens"] else ql
+        s["q"] = _normal(gen, (sum(ql), hq, d), dt)
+        kv = _normal(gen, (sum(kl), 2 * hk, d), dt)
+        s["k"], s["v"] = kv[:, :hk], kv[:, hk:]
+        s["cu_q"], s["cu_k"] = _cu(ql), _cu(kl)
+        if case["train"]:
+            s["go"] = _normal(gen, (sum(ql), hq, d), dt)
+    else:
+        lens, size, new = _ints(case["lens"]), case["size"], case["new"]
+        b = len(lens)
+        s["q"] = _normal(gen, (b * new, hq, d), dt)
+        used = torch.tensor(lens, dtype=torch.int32).cuda()
+        free = torch.arange(size, device="cuda") >= used[:, None]
+        caches = []
+        for _ in range(2):
+            c = torch.empty((b, size, hk, d), device="cuda", dtype=dt)
+            c.normal_(generator=gen)
+            c[free] = float("nan")                    # what nobody has written yet holds anything
+            caches.append(c.view(b * size, hk, d))
+        s["k"], s["v"] = caches
+        s["cu_q"], s["cu_k"] = _cu([new] * b), _cu([size] * b)
+        s["used"] = used
+    if own:
+        s["handle"] = _handles(case)
+    return s
+
+
+# ------------------------------------------------------------------ the framework's calls
+
+def _run_own(s):
+    from modulated_deformable_convolution_amd import attention as A
+    c, h = s["case"], s["handle"]
+    if c["op"] == "rotate":
+        q, k = A.rotate(h, s["q"], s["k"], s["positions"])
+        if not c["train"]:
+            return {"q": q, "k": k}
+        dq, dk = A.rotate_backward(h, s["gq"], s["gk"], s["positions"])
+        return {"q": q, "k": k, "dq": dq, "dk": dk}
+    if c["op"] == "norm_rotate":
+        q, k = A.norm_rotate(h, s["q"], s["k"], s["positions"], s["q_gain"], s["k_gain"], EPS)
+        if not c["train"]:
+            return {"q": q, "k": k}
+        g = A.norm_rotate_backward(h, s["q"], s["k"], s["positions"], s["q_gain"], s["k_gain"],
+                                   s["gq"], s["gk"], EPS)
+        return {"q": q, "k": k, "dq": g["q"], "dk": g["k"], "dq_gain": g["q_gain"],
+                "dk_gain": g["k_gain"]}
+    if c["op"] == "attention":
+        out, lse = A.attend(h, s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"])
+        if not c["train"]:
+            return {"out": out, "lse": lse}
+        g = A.attend_backward(h, s["q"], s["k"], s["v"], out, lse, s["go"], s["cu_q"], s["cu_k"])
+        return {"out": out, "lse": lse, "dq": g["q"], "dk": g["k"], "dv": g["v"]}
+    out, lse = A.attend(h, s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], used_k=s["used"])
+    return {"out": out, "lse": lse}
+
+
+# ------------------------------------------------------------------ the plain forms
+
+def _axis_of_pairs(axes, round_robin):
+    """(axis, place within the axis) of every pair of channels."""
+    if not round_robin:
+        return [(a, j) for a, n in enumerate(axes) for j in range(n)]
+    return [(a, j) for j in range(max(axes)) for a, n in enumerate(axes) if j < n]
+
+
+def _frequencies(case):
+    axes = _ints(case["axes"])
+    order = _axis_of_pairs(axes, case["round_robin"])
+    total = sum(axes)
+    return [a for a, _ in order], [case["base"] ** (-(j / axes[a] if case["per_axis"] else i / total))
+                                   for i, (a, j) in enumerate(order)]
+
+
+def _turn(x, cos, sin, case):
+    p = cos.shape[-1]
+    body, rest = x[..., :2 * p], x[..., 2 * p:]
+    if case["adjacent"]:
+        a, b = body[..., 0::2], body[..., 1::2]
+        y = torch.stack((a * cos - b * sin, a * sin + b * cos), -1).flatten(-2)
+    else:
+        a, b = body[..., :p], body[..., p:]
+        y = torch.cat((a * cos - b * sin, a * sin + b * cos), -1)
+    return torch.cat((y, rest), -1)
+
+
+def _angles(s):
+    axis, freq = _frequencies(s["case"])
+    place = s["positions"].double()[torch.tensor(axis, device="cuda")].t()
+    theta = place * torch.tensor(freq, device="cuda", dtype=torch.float64)
+    return theta.cos().float()[:, None], theta.sin().float()[:, None]
+
+
+def _plain_rotate(s):
+    c, dt = s["case"], s["q"].dtype
+    cos, sin = _angles(s)
+    r = {"q": _turn(s["q"].float(), cos, sin, c).to(dt), "k": _turn(s["k"].float(), cos, sin, c).to(dt)}
+    if c["train"]:
+        r["dq"] = _turn(s["gq"].float(), cos, -sin, c).to(dt)
+        r["dk"] = _turn(s["gk"].float(), cos, -sin, c).to(dt)
+    return r
+
+
+def _plain_norm(x, gain):
+    inv = (x.square().mean(-1, keepdim=True) + EPS).rsqrt()
+    return x * inv, inv
+
+
+def _plain_norm_backward(x, gain, gy, cos, sin, c):
+    n, inv = _plain_norm(x, gain)
+    g = _turn(gy, cos, -sin, c)
+    h = g * gain
+    return inv * (h - n * (h * n).mean(-1, keepdim=True)), (g * n).sum((0, 1), dtype=torch.float64)
+
+
+def _plain_norm_rotate(s):
+    c, dt = s["case"], s["q"].dtype
+    cos, sin = _angles(s)
+    q, k, gq, gk = s["q"].float(), s["k"].float(), s["q_gain"].float(), s["k_gain"].float()
+    r = {"q": _turn(_plain_norm(q, gq)[0] * gq, cos, sin, c).to(dt),
+         "k": _turn(_plain_norm(k, gk)[0] * gk, cos, sin, c).to(dt)}
+    if c["train"]:
+        dq, dgq = _plain_norm_backward(q, gq, s["gq"].float(), cos, sin, c)
+        dk, dgk = _plain_norm_backward(k, gk, s["gk"].float(), cos, sin, c)
+        r.update(dq=dq.to(dt), dk=dk.to(dt), dq_gain=dgq.to(dt), dk_gain=dgk.to(dt))
+    return r
+
+
+def _visible(s):
+    """[q rows][k rows]: whether a row sees a key."""
+    cq, ck = s["cu_q"].long(), s["cu_k"].long()
+    i = torch.arange(s["q"].shape[0], device="cuda")
+    j = torch.arange(s["k"].shape[0], device="cuda")
+    bi, bj = (torch.searchsorted(c, x, right=True) - 1 for c, x in ((cq, i), (ck, j)))
+    see = bi[:, None] == bj[None]
+    if s["case"]["causal"]:
+        last = i - cq[bi] + (ck[bi + 1] - ck[bi]) - (cq[bi + 1] - cq[bi])
+        see = see & ((j - ck[bj])[None] <= last[:, None])
+    return see
+
+
+def _softmax(scores):
+    top = scores.amax(-1, keepdim=True) if scores.shape[-1] else scores.new_zeros(scores.shape[:-1] + (1,))
+    top = top.masked_fill(top == -math.inf, 0.0)
+    e = (scores - top).exp()
+    total = e.sum(-1, keepdim=True)
+    lse = (top + total.log()).squeeze(-1) if scores.shape[-1] else top.squeeze(-1) - math.inf
+    return e / total.masked_fill(total == 0, 1.0), lse
+
+
+def _plain_attention(s):
+    c, dt = s["case"], s["q"].dtype
+    g, scale = c["q_heads"] // c["k_heads"], c["dim"] ** -0.5
+    heads = lambda x, n: x.float().transpose(0, 1).repeat_interleave(n, 0).contiguous()  # noqa: E731
+    q, k, v = heads(s["q"], 1), heads(s["k"], g), heads(s["v"], g)
+    scores = (q @ k.transpose(1, 2).contiguous() * scale).masked_fill_(~_visible(s), -math.inf)
+    p, lse = _softmax(scores)
+    del scores
+    o = p @ v
+    back = lambda x: x.transpose(0, 1).contiguous().to(dt)  # noqa: E731
+    r = {"out": back(o), "lse": lse}
+    if c["train"]:
+        go = heads(s["go"], 1)
+        shared = lambda x: back(x.unflatten(0, (c["k_heads"], g)).sum(1))  # noqa: E731
+        r["dv"] = shared(p.transpose(1, 2).contiguous() @ go)
+        ds = p * (go @ v.transpose(1, 2).contiguous() - (go * o).sum(-1, keepdim=True)) * scale
+        r["dq"] = back(ds @ k)
+        r["dk"] = shared(ds.transpose(1, 2).contiguous() @ q)
+    return r
+
+
+def _plain_decode(s):
+    c, dt = s["case"], s["q"].dtype
+    b, n, hk, d, size = s["used"].shape[0], c["new"], c["k_heads"], c["dim"], c["size"]
+    g = c["q_heads"] // hk
+    q = s["q"].float().view(b, n, hk, g, d).permute(0, 2, 1, 3, 4).reshape(b, hk, n * g, d)
+    j = torch.arange(size, device="cuda")
+    held = (j < s["used"][:, None])[:, :, None, None]
+    k, v = (torch.where(held, x.view(b, size, hk, d), 0).float().transpose(1, 2).contiguous()
+            for x in (s["k"], s["v"]))
+    last = s["used"].long()[:, None] - n + torch.arange(n, device="cuda")
+    see = (j <= last[:, :, None])[:, None, :, None].expand(b, 1, n, g, size).reshape(b, 1, n * g, size)
+    scores = (q @ k.transpose(2, 3).contiguous() * d ** -0.5).masked_fill(~see, -math.inf)
+    p, lse = _softmax(scores)
+    o = (p @ v).view(b, hk, n, g, d).permute(0, 2, 1, 3, 4).reshape(b * n, hk * g, d)
+    return {"out": o.to(dt), "lse": lse.view(b, hk, n, g).permute(1, 3, 0, 2).reshape(hk * g, b * n)}
+
+
+def run(state):
+    if own:
+        return _run_own(state)
+    return {"rotate": _plain_rotate, "norm_rotate": _plain_norm_rotate, "attention": _plain_attention,
+            "decode": _plain_decode}[state["case"]["op"]](state)
+
+
+# ------------------------------------------------------------------ the cost
+
+def _pairs(case):
+    """Visible (row, key) pairs of one head."""
+    if case["op"] == "decode":
+        lens, n = _ints(case["lens"]), case["new"]
+        return sum(max(0, v - n + 1 + i) for v in lens for i in range(n))
+    ql = _ints(case["q_lens"])
+    kl = _ints(case["k_lens"]) if case["k_lens"] else ql
+    if not case["causal"]:
+        return sum(a * b for a, b in zip(ql, kl))
+    return sum(sum(max(0, b - a + 1 + i) for i in range(a)) for a, b in zip(ql, kl))
+
+
+def work(case):
+    e, d, hq, hk = SIZE[case["dtype"]], case["dim"], case["q_heads"], case["k_heads"]
+    if case["op"] in ("rotate", "norm_rotate"):
+        t, norm = case["tokens"], case["op"] == "norm_rotate"
+        rows = t * (hq + hk)
+        # forward: in and out; backward: the gradient in and out, and the input again for the norm's
+        moved = rows * d * e * (2 + (2 if case["train"] else 0))
+        moved += 4 * t * len(_ints(case["axes"])) + (2 * d * e if norm else 0)
+        flops = rows * d * ((3 + (4 if norm else 0)) + ((3 + (9 if norm else 0)) if case["train"] else 0))
+        return {"bytes": moved, "flops": flops}
+    flops = 4 * d * hq * _pairs(case)
+    if case["op"] == "decode":
+        lens, n = _ints(case["lens"]), case["new"]
+        rows = len(lens) * n
+        return {"bytes": 2 * sum(lens) * hk * d * e + rows * hq * (2 * d * e + 4), "flops": flops}
+    tq = sum(_ints(case["q_lens"]))
+    tk = sum(_ints(case["k_lens"])) if case["k_lens"] else tq
+    moved = (2 * tq * hq + 2 * tk * hk) * d * e + 4 * tq * hq
+    if case["train"]:                       # and the output's gradient in, those of q, k and v out
+        moved += (2 * tq * hq + 2 * tk * hk) * d * e
+        flops += 10 * d * hq * _pairs(case)
+    return {"bytes": max(1, moved), "flops": flops}
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+
+def _exact_rotation(case, pos):
+    """[tokens][pairs] complex numbers exp(i theta)."""
+    axes = _ints(case["axes"])
+    left, turn, owner = list(axes), 0, []
+    while any(left):
+        a = turn % len(axes) if case["round_robin"] else next(i for i, n in enumerate(left) if n)
+        if left[a]:
+            owner.append((a, axes[a] - left[a]))
+            left[a] -= 1
+        turn += 1
+    cols = []
+    for i, (a, j) in enumerate(owner):
+        e = j / axes[a] if case["per_axis"] else i / len(owner)
+        cols.append(pos[a].double() * math.exp(-e * math.log(case["base"])))
+    th = torch.stack(cols, 1)
+    return torch.polar(torch.ones_like(th), th)
+
+
+def _exact_turn(x, z, adjacent):
+    p = z.shape[1]
+    lo, hi = (slice(0, 2 * p, 2), slice(1, 2 * p, 2)) if adjacent else (slice(0, p), slice(p, 2 * p))
+    w = torch.complex(x[..., lo].contiguous(), x[..., hi].contiguous()) * z[:, None]
+    y = x.clone()
+    y[..., lo], y[..., hi] = w.real, w.imag
+    return y
+
+
+def _exact_norm_rotate(s, case):
+    z = _exact_rotation(case, s["positions"])
+    r = {}
+    for n in ("q", "k"):
+        x = s[n].double()
+        if case["op"] == "rotate":
+            r[n] = _exact_turn(x, z, case["adjacent"])
+            if case["train"]:
+                r["d" + n] = _exact_turn(s["g" + n].double(), z.conj(), case["adjacent"])
+            continue
+        gain = s[n + "_gain"].double()
+        var = (x * x).sum(-1, keepdim=True) / x.shape[-1] + EPS
+        r[n] = _exact_turn(x / var.sqrt() * gain, z, case["adjacent"])
+        if case["train"]:
+            g = _exact_turn(s["g" + n].double(), z.conj(), case["adjacent"])
+            r["d%s_gain" % n] = (g * x / var.sqrt()).sum((0, 1))
+            w = g * gain
+            r["d" + n] = w / var.sqrt() - x * (w * x).sum(-1, keepdim=True) / (x.shape[-1] * var ** 1.5)
+    return r
+
+
+def _exact_attention(s, case):
+    d, hq = case["dim"], case["q_heads"]
+    g = hq // case["k_heads"]
+    cq, ck = s["cu_q"].tolist(), s["cu_k"].tolist()
+    used = s["used"].tolist() if "used" in s else None
+    zeros = lambda x: torch.zeros(x.shape, device="cuda", dtype=torch.float64)  # noqa: E731
+    r = {"out": zeros(s["q"]), "lse": torch.full((hq, s["q"].shape[0]), -math.inf, device="cuda",
+                                                 dtype=torch.float64)}
+    if case.get("train"):
+        r.update(dq=zeros(s["q"]), dk=zeros(s["k"]), dv=zeros(s["v"]))
+    for b in range(len(cq) - 1):
+        lq, lk = cq[b + 1] - cq[b], used[b] if used else ck[b + 1] - ck[b]
+        if not lq or not lk:
+            continue
+        qs, ks = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b] + lk)
+        hide = None
+        if case.get("causal", True):
+            i, j = torch.arange(lq, device="cuda"), torch.arange(lk, device="cuda")
+            hide = j[None] - (lk - lq) > i[:, None]
+        for h in range(hq):
+            q, k, v = s["q"][qs, h].double(), s["k"][ks, h // g].double(), s["v"][ks, h // g].double()
+            t = (q @ k.T) / math.sqrt(d)
+            if hide is not None:
+                t[hide] = -math.inf
+            lse = torch.logsumexp(t, 1)
+            p = torch.nan_to_num((t - lse[:, None]).exp(), nan=0.0)
+            r["out"][qs, h], r["lse"][h, qs] = p @ v, lse
+            if case.get("train"):
+                go = s["go"][qs, h].double()
+                r["dv"][ks, h // g] += p.T @ go
+                dp = go @ v.T
+                ds = p * (dp - (p * dp).sum(1, keepdim=True)) / math.sqrt(d)
+                r["dq"][qs, h] = ds @ k
+                r["dk"][ks, h // g] += ds.T @ q
+    return r
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] in ("rotate", "norm_rotate"):
+        return _exact_norm_rotate(s, case)
+    return _exact_attention(s, case)
