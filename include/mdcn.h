@@ -61,7 +61,8 @@ extern "C" {
 typedef enum mdcn_status {
     MDCN_OK = 0,
     MDCN_E_NULL = 1,        /* a required pointer is NULL                            */
-    MDCN_E_ATTR = 2,        /* stride/dilation <= 0, padding < 0, group or dg <= 0   */
+    MDCN_E_ATTR = 2,        /* stride/dilation <= 0, padding < 0, group or dg <= 0, or
+                               a limit stated at another create call breached        */
     MDCN_E_SHAPE = 3,       /* the dims break a binding listed at mdcn_forward       */
     MDCN_E_DTYPE = 4,       /* dtype is not one of mdcn_dtype                        */
     MDCN_E_WORKSPACE = 5,   /* workspace NULL or smaller than mdcn_workspace_min_bytes */
@@ -278,6 +279,120 @@ mdcn_status mdcn_backward(const mdcn_op *op, mdcn_dtype dtype, const int64_t dim
                           void *grad_offset, void *grad_mask, void *grad_weight, void *grad_bias,
                           int64_t bias_len, void *workspace, size_t workspace_bytes,
                           void *stream);
+
+/* ---- attention ----------------------------------------------------------- */
+
+/* Operators for attention over the tokens of feature maps and sequences:
+ * rotary positions, norms of queries and keys, attention over packed
+ * sequences and against a key/value cache.  The conventions above hold
+ * (device pointers, the caller's stream and buffers, status codes, fp32
+ * arithmetic, one rounding per output; fp32, fp16 or bf16, one dtype per
+ * call), except that tensors are views [tokens][heads][dim]: dim values lie
+ * together, tokens and heads at strides given in elements, so queries, keys
+ * and values may be slices of one projection's output.  Strides are not
+ * negative, a token stride is at most 2^22.  An output's rows must not overlap
+ * (MDCN_E_ALIAS).  Handles hold no device memory. */
+
+typedef struct mdcn_rotary mdcn_rotary;
+
+/* Rotary positions of a head of `dim` channels (even, at most 256) with
+ * 1 to 8 axes: axis a turns pairs[a] pairs of channels, at most dim/2 in all;
+ * channels past 2 * sum(pairs) stay as they are.  Pair i of n is channels
+ * (i, i + n), or (2i, 2i + 1) if `adjacent`.  Pairs belong to the axes in
+ * blocks, or dealt in turn if `round_robin` (an axis that has run out is
+ * passed over).  The angle of pair i at position p is p * base^-e, e = i / n,
+ * or (if per_axis) e = j / pairs[a] for the j-th pair of axis a.
+ * Errors: MDCN_E_NULL, MDCN_E_ATTR. */
+mdcn_status mdcn_rotary_create(int32_t dim, int32_t axes, const int32_t *pairs, double base,
+                               int32_t adjacent, int32_t round_robin, int32_t per_axis,
+                               mdcn_rotary **out);
+void mdcn_rotary_destroy(mdcn_rotary *op);
+
+/* Turns every pair (a, b) of every head of q and k to
+ * (a cos t - b sin t, a sin t + b cos t); by -t if `inverse` (the backward
+ * pass: the gradient of the inputs from that of the outputs).
+ *   dims[0] tokens, dims[1] q heads, dims[2] k heads (one of the two may be 0,
+ *   its pointers are then ignored), dims[3] stride of positions between axes;
+ *   dims[4..11] token and head stride of q, k, q_out, k_out.
+ *   positions: int32 [axes][tokens].
+ * q_out may be q and k_out k (same view).  Angles are reduced in double, so
+ * that any int32 position is exact to fp32.
+ * Errors: MDCN_E_NULL, MDCN_E_SHAPE, MDCN_E_DTYPE, MDCN_E_ALIAS,
+ * MDCN_E_DEVICE, MDCN_E_LAUNCH. */
+mdcn_status mdcn_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const int64_t dims[12],
+                        const void *q, const void *k, const int32_t *positions, int32_t inverse,
+                        void *q_out, void *k_out, void *stream);
+
+/* The same on n * gain, with n = x / sqrt(mean(x^2) + eps) over the dim
+ * channels of each head; q_gain and k_gain: dim values.  eps >= 0 (MDCN_E_ATTR). */
+mdcn_status mdcn_norm_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const int64_t dims[12],
+                             const void *q, const void *k, const int32_t *positions,
+                             const void *q_gain, const void *k_gain, float eps, void *q_out,
+                             void *k_out, void *stream);
+
+/* Gradients of mdcn_norm_rotate from those of its outputs: grad_q, grad_k and
+ * the gains' (sums over all tokens and heads, in fp32, in a fixed order).
+ * dims[0..7] as above, dims[8..15] token and head stride of grad_q_out,
+ * grad_k_out, grad_q, grad_k.  No tokens: the gains' gradients are zero. */
+mdcn_status mdcn_norm_rotate_backward_workspace_bytes(const mdcn_rotary *op, int64_t tokens,
+                                                      size_t *bytes);
+mdcn_status mdcn_norm_rotate_backward(const mdcn_rotary *op, mdcn_dtype dtype,
+                                      const int64_t dims[16], const void *q, const void *k,
+                                      const int32_t *positions, const void *q_gain,
+                                      const void *k_gain, float eps, const void *grad_q_out,
+                                      const void *grad_k_out, void *grad_q, void *grad_k,
+                                      void *grad_q_gain, void *grad_k_gain, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+typedef struct mdcn_attention mdcn_attention;
+
+/* Attention with q_heads query heads sharing k_heads key and value heads
+ * (q_heads a multiple of k_heads; query head h uses key head
+ * h / (q_heads / k_heads)), dim channels each (a multiple of 8, at most 128),
+ * scores scaled by `scale` (> 0).  Errors: MDCN_E_NULL, MDCN_E_ATTR. */
+mdcn_status mdcn_attention_create(int32_t q_heads, int32_t k_heads, int32_t dim, int32_t causal,
+                                  float scale, mdcn_attention **out);
+void mdcn_attention_destroy(mdcn_attention *op);
+
+/* out = softmax(scale * q k^T) v within each of `batch` packed sequences, and
+ * lse[q_heads][q_tokens], the logarithm of each row's sum of exponentials.
+ *   dims[0] batch, dims[1] query tokens, dims[2] key tokens;
+ *   dims[3..10] token and head stride of q, k, v, out (multiples of 16 bytes,
+ *   as are the pointers; a token stride of dim at least).
+ *   cu_q, cu_k: int32 [batch + 1], sequence b's queries are tokens
+ *   cu_q[b] .. cu_q[b + 1] - 1, its keys cu_k[b] .. cu_k[b + 1] - 1.
+ *   used_k: int32 [batch] or NULL: only the first used_k[b] keys of sequence
+ *   b exist (a cache with room); the others are never used, whatever they hold.
+ * Sequence b has lq queries and lk (used) keys; causal: row i sees the keys
+ * j <= i + lk - lq.  Values in hidden rows of v never reach a row that does
+ * not see them, be they infinite or NaN.  A row that sees no key gets zeros
+ * and lse -infinity.  The lengths are read on the GPU only; offsets outside
+ * the tensors are clamped to them.  Tokens that belong to no sequence are left
+ * as they are in out and lse.  Scores, statistics and sums in fp32;
+ * probabilities are rounded to the inputs' type for the product with v.
+ * Workspace: mdcn_attend_workspace_bytes, 0 unless there are few query rows.
+ * Errors: MDCN_E_NULL, MDCN_E_SHAPE, MDCN_E_DTYPE, MDCN_E_WORKSPACE,
+ * MDCN_E_ALIAS, MDCN_E_DEVICE, MDCN_E_LAUNCH. */
+mdcn_status mdcn_attend_workspace_bytes(const mdcn_attention *op, mdcn_dtype dtype,
+                                        const int64_t dims[11], size_t *bytes);
+mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[11],
+                        const void *q, const void *k, const void *v, const int32_t *cu_q,
+                        const int32_t *cu_k, const int32_t *used_k, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of mdcn_attend's out with respect to q, k and v, from grad_out and
+ * the forward's out and lse.  dims[0..10] as there, dims[11..18] token and
+ * head stride of grad_out, grad_q, grad_k, grad_v.  The gradients of shared
+ * key heads are the sums over their query heads; keys that are not used get
+ * zeros.  No atomics: repeated calls give the same bits. */
+mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_dtype dtype,
+                                                 const int64_t dims[19], size_t *bytes);
+mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
+                                 const int64_t dims[19], const void *q, const void *k,
+                                 const void *v, const void *out, const float *lse,
+                                 const void *grad_out, const int32_t *cu_q, const int32_t *cu_k,
+                                 const int32_t *used_k, void *grad_q, void *grad_k, void *grad_v,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---- tracing: per-kernel device time, for profiling --------------------- */
 

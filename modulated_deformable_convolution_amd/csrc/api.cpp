@@ -504,6 +504,8 @@ mdcn_status forward_with_workspace(const mdcn_op *op, mdcn_dtype dtype, const in
                         workspace_bytes, stream, nullptr);
 }
 
+mdcn_status check_device() { return device_ok(); }
+
 }  // namespace mdcn
 
 
@@ -807,7 +809,7 @@ const char *mdcn_status_string(mdcn_status status)
     case MDCN_OK: return "ok";
     case MDCN_E_NULL: return "a required pointer is NULL";
     case MDCN_E_ATTR: return "invalid attribute (stride/dilation must be > 0, padding >= 0, "
-                             "group and deformable_group > 0)";
+                             "group and deformable_group > 0; see the create call's limits)";
     case MDCN_E_SHAPE: return "tensor dims violate the operator's shape bindings or limits";
     case MDCN_E_DTYPE: return "unsupported dtype";
     case MDCN_E_WORKSPACE: return "workspace missing or too small";

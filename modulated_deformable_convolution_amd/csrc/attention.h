@@ -1,0 +1,76 @@
+// attention.h -- arguments and launchers of the attention operators: rotary
+// positions, norms of queries and keys, attention over packed sequences.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "mdcn.h"
+
+namespace mdcn {
+
+constexpr int kMaxRotaryDim = 256;
+constexpr int kMaxRotaryAxes = 8;
+constexpr int kMaxAttendDim = 128;
+
+// [tokens][heads][dim] in device memory, dim contiguous; strides in elements.
+struct Heads {
+    const void *data;
+    int64_t token_stride, head_stride;
+};
+
+// The angle of pair i at position p is 2 pi * turns[i] * p.  Passed to the
+// kernels by value (1.2 KB of kernel arguments), so a handle holds no device
+// memory.
+struct RotaryTable {
+    double turns[kMaxRotaryDim / 2];
+    uint8_t axis[kMaxRotaryDim / 2];
+};
+
+struct RotaryArgs {
+    Heads q, k;            // rotate, norm_rotate: inputs; backward: the forward's inputs
+    Heads gq, gk;          // norm_rotate's backward: gradients of its outputs
+    Heads oq, ok;          // outputs (backward: gradients of the inputs)
+    const void *q_gain, *k_gain;
+    float *partial;        // backward: [blocks][2][dim] sums of the gains' gradients
+    const int32_t *positions;
+    int64_t axis_stride, tokens;
+    int32_t q_heads, k_heads, dim, pairs;
+    int32_t adjacent, inverse;
+    float eps;
+    RotaryTable table;
+};
+
+enum class RotaryKind { Rotate, NormRotate, NormRotateBackward };
+
+// Blocks of the backward, one row of `partial` each.
+int rotary_backward_blocks(int64_t tokens);
+hipError_t launch_rotary(RotaryKind kind, mdcn_dtype dtype, const RotaryArgs &a, hipStream_t s);
+// Sums partial's rows into the two gain gradients.
+hipError_t launch_gain_sum(mdcn_dtype dtype, const RotaryArgs &a, void *dq_gain, void *dk_gain,
+                           hipStream_t s);
+
+struct AttendArgs {
+    Heads q, k, v, out;    // out: output of the forward, input of the backward
+    Heads go, dq, dk, dv;  // backward
+    float *lse;            // [q_heads][q_tokens]
+    float *delta;          // backward: [q_heads][q_tokens], sum over dim of go * out
+    const int32_t *cu_q, *cu_k, *used_k;
+    int32_t batch, q_tokens, k_tokens;
+    int32_t q_heads, k_heads, dim, causal;
+    float scale;
+    // split kernel
+    int32_t workers;
+    float *partial;
+};
+
+hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
+// Workgroups of the split kernel and the bytes of `partial` they need.
+int attend_split_workers(mdcn_dtype dtype, int dim);
+size_t attend_split_bytes(mdcn_dtype dtype, int dim);
+hipError_t launch_attend_split(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
+hipError_t launch_attend_backward(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
+
+}  // namespace mdcn

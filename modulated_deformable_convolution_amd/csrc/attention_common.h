@@ -1,0 +1,450 @@
+// attention_common.h -- pieces shared by the attention kernels (gfx950).
+//
+// Everything is built from two products on 32x32 MFMA tiles, with rows
+// staged in LDS on one side and operands in registers on the other:
+//   mm_rows: S[i][c] = sum_d tile[i][d] * frag[c][d]   (c = lane % 32)
+//   mm_cols: acc[d][c] += sum_i tile[i][d] * p[i][c]
+// An accumulator of a 32x32 tile holds column lane % 32 in every register and
+// row 8*(r/4) + 4*(lane/32) + r%4 in register r.  So the result of mm_rows
+// has one query (or key) per lane: a softmax row needs one exchange with lane
+// ^ 32, and its registers, rounded, are the operand p of mm_cols without any
+// exchange, because the order of an instruction's k index is free as long as
+// both operands share it: half h of the wave takes rows 8*j + 4*h + (0..3).
+// mm_cols needs the staged rows transposed: 16-bit types read them with the
+// transposing LDS read (4 rows x 16 columns per 16 lanes), fp32 reads single
+// values, which needs no transposition.
+//
+// LDS tiles: a row of DP values padded to a power of two of bytes (64..512);
+// its 16-byte chunk c sits at c ^ swz(row), swz chosen so that both kinds of
+// read (one chunk of 16 rows; four chunks of 4 rows) touch every bank once.
+// Tiles are written by buffer loads straight to LDS; rows past the end
+// and channels past dim are out of the buffer's range and arrive as zeros.
+#pragma once
+
+#include "attention.h"
+#include "device_common.h"
+#include "mfma_common.h"
+
+namespace mdcn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) short4v lds_short4;
+
+// Layout of one staged tile row.
+template <typename T, int DP> struct Row {
+    static constexpr int BYTES = DP * int(sizeof(T));
+    static constexpr int PITCH = BYTES <= 64 ? 64 : BYTES <= 128 ? 128 : BYTES <= 256 ? 256 : 512;
+    static constexpr int CHUNKS = PITCH / 16;
+    static constexpr int STEPS = BYTES / 32;     // mm_rows steps: two chunks each
+    static constexpr int BLOCKS = DP / 32;       // mm_cols: 32-channel blocks
+    // mm_cols steps: rows per Mma::step (16-bit: 16, fp32: 8)
+    static constexpr int KROWS = sizeof(T) == 2 ? 16 : 8;
+
+    static __device__ __forceinline__ int swz(int row)
+    {
+        if (CHUNKS == 4)
+            return (row >> 2) & 3;
+        if (CHUNKS == 8)
+            return ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+        if (sizeof(T) == 2)
+            return (row & 3) << 2 | ((row >> 2) & 3);
+        return ((row >> 2) & 1) << 3 | ((row >> 3) & 1) << 2 | (row & 3);
+    }
+};
+
+// A row as mm_rows' register operand; the accumulators of mm_cols.
+template <typename T, int DP> using Frag = uint4[Row<T, DP>::STEPS];
+template <typename T, int DP> using Acc = float16v[Row<T, DP>::BLOCKS];
+
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    return uint32_t(reinterpret_cast<uintptr_t>((const lds_void *)p));
+}
+
+// 16 bytes per lane from rsrc + voff into LDS at lds + 16 * lane.  The
+// compiler does not see the write; callers wait (dma_wait) and pass a barrier
+// before any wave reads the data.
+__device__ __forceinline__ void dma_row16(uint32_t lds, v4i rsrc, uint32_t voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory");
+}
+
+// The same with 4 bytes per lane, to lds + 4 * lane.
+__device__ __forceinline__ void dma_row4(uint32_t lds, v4i rsrc, uint32_t voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory");
+}
+
+template <int N> __device__ __forceinline__ void dma_wait()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ v4i row_resource(const char *base, uint32_t bytes)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(base);
+    v4i r;
+    r.x = __builtin_amdgcn_readfirstlane(int(uint32_t(v)));
+    r.y = __builtin_amdgcn_readfirstlane(int(uint32_t(v >> 32)) & 0xffff);
+    r.z = __builtin_amdgcn_readfirstlane(int(bytes));
+    r.w = 0x00020000;
+    return r;
+}
+
+// Stages tiles of ROWS rows with WAVES waves: each wave's share of the copies.
+template <typename T, int DP, int ROWS, int WAVES> struct Stager {
+    using R = Row<T, DP>;
+    static constexpr int COPIES = ROWS * R::CHUNKS / 64 / WAVES;
+    static_assert(COPIES * 64 * WAVES == ROWS * R::CHUNKS, "copies fill the tile");
+    uint32_t voff[COPIES];
+    uint32_t stride, width;
+    uint32_t slot;
+
+    __device__ __forceinline__ void init(int64_t token_stride, int dim, int wave, int lane)
+    {
+        stride = uint32_t(token_stride) * uint32_t(sizeof(T));
+        width = uint32_t(dim) * uint32_t(sizeof(T));
+        slot = uint32_t(wave * COPIES * 1024);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            const int s = (wave * COPIES + i) * 64 + lane;
+            const int row = s / R::CHUNKS;
+            const uint32_t byte = uint32_t((s % R::CHUNKS) ^ R::swz(row)) * 16;
+            voff[i] = byte < width ? uint32_t(row) * stride + byte : 0x80000000u;
+        }
+    }
+
+    // Rows [0, left) of the tile at `base` (ROWS at most) to LDS at `lds`.
+    __device__ __forceinline__ void load(uint32_t lds, const char *base, int left) const
+    {
+        const int n = left < ROWS ? left : ROWS;
+        const v4i r = row_resource(base, n > 0 ? uint32_t(n - 1) * stride + width : 0);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i)
+            dma_row16(__builtin_amdgcn_readfirstlane(lds + slot + i * 1024), r, voff[i]);
+    }
+};
+
+// The register operand of mm_rows: row `src` (dim values, 16-byte aligned),
+// zeros past dim or when src is null.
+template <typename T, int DP>
+__device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *src, int dim,
+                                          int half)
+{
+#pragma unroll
+    for (int k = 0; k < Row<T, DP>::STEPS; ++k) {
+        const int d = (2 * k + half) * int(16 / sizeof(T));
+        f[k] = make_uint4(0, 0, 0, 0);
+        if (src && d < dim)
+            f[k] = *reinterpret_cast<const uint4 *>(src + d);
+    }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ float16v mm_rows(const char *tile, const Frag<T, DP> &f,
+                                            int lane)
+{
+    using R = Row<T, DP>;
+    const int row = lane & 31, half = lane >> 5, sw = R::swz(row);
+    const char *p = tile + row * R::PITCH;
+    float16v s = {};
+#pragma unroll
+    for (int k = 0; k < R::STEPS; ++k) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(p + ((2 * k + half) ^ sw) * 16);
+        s = Mma<T>::step(a, f[k], s);
+    }
+    return s;
+}
+
+// Registers r0.. of a 32x32 accumulator rounded to T (to nearest even) as the
+// operand of mm_cols.  Probabilities and their gradients enter the second
+// product in the inputs' type, as the matrix instructions need it; sums stay in fp32.
+template <typename T>
+__device__ __forceinline__ uint4 pack_p(const float16v &p, int r0)
+{
+    uint4 o;
+    if constexpr (sizeof(T) == 4) {
+        o = make_uint4(__float_as_uint(p[r0]), __float_as_uint(p[r0 + 1]),
+                       __float_as_uint(p[r0 + 2]), __float_as_uint(p[r0 + 3]));
+    } else {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        typedef T t2 __attribute__((ext_vector_type(2)));
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const t2 v = __builtin_convertvector((f2){p[r0 + 2 * i], p[r0 + 2 * i + 1]}, t2);
+            __builtin_memcpy(&w[i], &v, 4);
+        }
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return o;
+}
+
+// Transposed operand of mm_cols step `step`, channel block `blk`.
+template <typename T, int DP>
+__device__ __forceinline__ uint4 col_frag(const char *tile, int step, int blk, int lane)
+{
+    using R = Row<T, DP>;
+    const int half = lane >> 5;
+    uint4 o;
+    if constexpr (sizeof(T) == 2) {
+        const int l = lane & 15;
+        const int chunk = blk * 4 + ((lane >> 4) & 1) * 2 + ((l & 3) >> 1);
+        uint2 w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = step * 16 + j * 8 + half * 4 + (l >> 2);
+            const char *p = tile + row * R::PITCH + (chunk ^ R::swz(row)) * 16 + (l & 1) * 8;
+            const short4v v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)p);
+            __builtin_memcpy(&w[j], &v, 8);
+        }
+        o = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+    } else {
+        const int d = blk * 32 + (lane & 31);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = step * 8 + half * 4 + j;
+            w[j] = *reinterpret_cast<const uint32_t *>(
+                tile + row * R::PITCH + ((d >> 2) ^ R::swz(row)) * 16 + (d & 3) * 4);
+        }
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return o;
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void mm_cols(Acc<T, DP> &acc, const char *tile,
+                                        const float16v &p, int lane)
+{
+    using R = Row<T, DP>;
+#pragma unroll
+    for (int s = 0; s < 32 / R::KROWS; ++s) {
+        const uint4 b = pack_p<T>(p, s * R::KROWS / 2);
+#pragma unroll
+        for (int d = 0; d < R::BLOCKS; ++d)
+            acc[d] = Mma<T>::step(col_frag<T, DP>(tile, s, d, lane), b, acc[d]);
+    }
+}
+
+// Row of register r of an accumulator.
+__device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
+
+__device__ __forceinline__ float swap_halves(float v) { return __shfl_xor(v, 32, 64); }
+
+// acc[d][c] * factor to row `dst` of lane c (null: nothing is stored).
+template <typename T, int DP>
+__device__ __forceinline__ void store_cols(T *dst, const Acc<T, DP> &acc,
+                                           float factor, int dim, int half)
+{
+    if (!dst)
+        return;
+#pragma unroll
+    for (int b = 0; b < Row<T, DP>::BLOCKS; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int d = b * 32 + 8 * g + 4 * half;
+            if (d < dim) {
+                struct alignas(4 * sizeof(T)) {
+                    T e[4];
+                } v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v.e[j] = from_f32<T>(acc[b][4 * g + j] * factor);
+                __builtin_memcpy(__builtin_assume_aligned(dst + d, 4 * sizeof(T)), &v, sizeof(v));
+            }
+        }
+}
+
+// ---- softmax ---------------------------------------------------------------
+
+// The running maximum is raised only when a score exceeds it by more than
+// this many powers of two: e^s stays below 2^8 relative to the maximum, which
+// costs no accuracy in fp32 sums and saves most rescalings.
+constexpr float kRaise = 8.0f;
+
+// Softmax state of one query row (both halves of the wave hold the same
+// maximum; the sums are those of the half's own keys).
+template <typename T, int DP> struct Softmax {
+    Acc<T, DP> o;
+    float m, l;
+
+    __device__ __forceinline__ void init()
+    {
+#pragma unroll
+        for (int b = 0; b < Row<T, DP>::BLOCKS; ++b)
+            o[b] = (float16v){};
+        m = -INFINITY;
+        l = 0.0f;
+    }
+
+    // Takes NS blocks of 32 scores (raw, -infinity where masked) and turns them into e^(c (s - m)).
+    template <int NS> __device__ __forceinline__ void step(float16v (&s)[NS], float c)
+    {
+        float top = s[0][0];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                top = fmaxf(top, s[n][r]);
+        top = fmaxf(top, swap_halves(top));
+        if (__any(top > m + kRaise / c || (m == -INFINITY && top > m))) {
+            const float up = fmaxf(top, m);
+            const float f = up == -INFINITY ? 1.0f : exp2f((m - up) * c);
+#pragma unroll
+            for (int b = 0; b < Row<T, DP>::BLOCKS; ++b)
+                o[b] *= f;
+            l *= f;
+            m = up;
+        }
+        const float mc = m == -INFINITY ? 0.0f : m * c;
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[n][r] = __builtin_amdgcn_exp2f(fmaf(s[n][r], c, -mc));
+                sum += s[n][r];
+            }
+        l += sum;
+    }
+};
+
+// Recomputes the accumulators of keys [begin, last] one key at a time, each
+// lane for its own row: hidden keys are never touched, whatever they hold.
+template <typename T, int DP>
+__device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *qf, const char *k,
+                                                    const char *v, uint32_t k_stride,
+                                                    uint32_t v_stride, int begin, int end,
+                                                    int last, float m, float c, int dim, int half)
+{
+    using R = Row<T, DP>;
+    constexpr int E = 16 / sizeof(T);
+    for (int b = 0; b < R::BLOCKS; ++b)
+        o[b] = (float16v){};
+    for (int j = begin; j < end; ++j) {
+        const T *kr = reinterpret_cast<const T *>(k + uint64_t(j) * k_stride);
+        const T *vr = reinterpret_cast<const T *>(v + uint64_t(j) * v_stride);
+        float s = 0.0f;
+        for (int i = 0; i < R::STEPS; ++i) {
+            const int d = (2 * i + half) * E;
+            if (d >= dim)
+                break;
+            Vec16<T> qv;
+            qv.raw = qf[i];
+            const Vec16<T> kv = load16(kr + d);
+            for (int e = 0; e < E; ++e)
+                s = fmaf(to_f32(qv.e[e]), to_f32(kv.e[e]), s);
+        }
+        s += swap_halves(s);
+        if (j > last)
+            continue;
+        const float p = exp2f(fmaf(s, c, -m * c));
+        for (int b = 0; b < R::BLOCKS; ++b)
+            for (int r = 0; r < 16; ++r) {
+                const int d = b * 32 + acc_row(r, half);
+                if (d < dim)
+                    o[b][r] = fmaf(p, to_f32(vr[d]), o[b][r]);
+            }
+    }
+}
+
+// After the tiles [begin, end) that a causal mask cuts, while the accumulators
+// hold nothing else: where they are not finite, recomputes them without the hidden keys.
+template <typename T, int DP>
+__device__ __forceinline__ void repair_hidden(Acc<T, DP> &acc, const Frag<T, DP> &qf,
+                                              const char *k, const char *v, uint32_t k_stride,
+                                              uint32_t v_stride, int begin, int end, int last,
+                                              float m, float c, int dim, int half)
+{
+    using R = Row<T, DP>;
+    float bad = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R::BLOCKS; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            bad += acc[i][r] * 0.0f;
+    if (__any(bad != 0.0f)) {
+        Acc<T, DP> o;                                    // copies: only they are
+        Frag<T, DP> f;                                   // addressed in memory
+#pragma unroll
+        for (int i = 0; i < R::STEPS; ++i)
+            f[i] = qf[i];
+        recompute<T, DP>(o, f, k, v, k_stride, v_stride, begin, end, last, m, c, dim, half);
+#pragma unroll
+        for (int i = 0; i < R::BLOCKS; ++i)
+            acc[i] = o[i];
+    }
+}
+
+// ---- packed sequences ------------------------------------------------------
+
+struct Span {
+    int q0, lq, k0, lk;       // first query and key row, their numbers
+    int k_all;                // keys of the sequence, used or not
+};
+
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi)
+{
+    return v < lo ? lo : v > hi ? hi : v;
+}
+
+// Rows of sequence b.  Offsets are clamped to the tensors, so that no offsets
+// whatever lead to an access outside them.
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int b)
+{
+    Span s;
+    s.q0 = clamp_int(a.cu_q[b], 0, a.q_tokens);
+    s.lq = clamp_int(a.cu_q[b + 1], s.q0, a.q_tokens) - s.q0;
+    s.k0 = clamp_int(a.cu_k[b], 0, a.k_tokens);
+    s.k_all = clamp_int(a.cu_k[b + 1], s.k0, a.k_tokens) - s.k0;
+    s.lk = a.used_k ? clamp_int(a.used_k[b], 0, s.k_all) : s.k_all;
+    return s;
+}
+
+// The sequence and its tile that hold tile t of the batch, where `count(b)`
+// is the number of tiles of sequence b; false past the last tile.  Every
+// lane of the wave must call it.
+template <class F>
+__device__ __forceinline__ bool find_tile(int batch, int t, int lane, F &&count, int &b, int &tile)
+{
+    int base = 0;
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        const int mine = b0 + lane < batch ? count(b0 + lane) : 0;
+        int upto = mine;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int v = __shfl_up(upto, m, 64);
+            upto += lane >= m ? v : 0;
+        }
+        const uint64_t past = __ballot(base + upto > t);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            b = __builtin_amdgcn_readfirstlane(b0 + l);
+            tile = __builtin_amdgcn_readfirstlane(
+                t - base - (__shfl(upto, l, 64) - __shfl(mine, l, 64)));
+            return true;
+        }
+        base += __shfl(upto, 63, 64);
+    }
+    return false;
+}
+
+template <typename T>
+__device__ __forceinline__ const char *row_ptr(const Heads &h, int64_t token, int head)
+{
+    return reinterpret_cast<const char *>(static_cast<const T *>(h.data) + token * h.token_stride +
+                                          head * h.head_stride);
+}
+
+}  // namespace mdcn

@@ -1,5 +1,5 @@
-// entry.h -- the forward pass behind the extern "C" entry points, for the
-// entry points defined outside api.cpp.
+// entry.h -- the forward pass behind the extern "C" entry points and the device
+// check, for the entry points defined outside api.cpp.
 #pragma once
 
 #include "mdcn.h"
@@ -13,5 +13,8 @@ mdcn_status forward_with_workspace(const mdcn_op *op, mdcn_dtype dtype, const in
                                    const void *weight, const void *bias, int64_t bias_len,
                                    void *out, void *workspace, size_t workspace_bytes,
                                    void *stream);
+
+// MDCN_OK if the current device is a gfx950 GPU, else MDCN_E_DEVICE.
+mdcn_status check_device();
 
 }  // namespace mdcn

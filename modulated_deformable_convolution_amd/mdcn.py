@@ -51,6 +51,10 @@ EXPORTED = [
     "mdcn_kernel_name", "mdcn_status_string", "mdcn_abi_version", "mdcn_describe_plan",
     "mdcn_backward_workspace_bytes", "mdcn_backward", "mdcn_backward_traced",
     "mdcn_forward_check", "mdcn_forward_noalloc",
+    "mdcn_rotary_create", "mdcn_rotary_destroy", "mdcn_rotate", "mdcn_norm_rotate",
+    "mdcn_norm_rotate_backward_workspace_bytes", "mdcn_norm_rotate_backward",
+    "mdcn_attention_create", "mdcn_attention_destroy", "mdcn_attend_workspace_bytes",
+    "mdcn_attend", "mdcn_attend_backward_workspace_bytes", "mdcn_attend_backward",
 ]
 
 # bytes of the device array mdcn_forward_noalloc works in (include/mdcn.h)
@@ -107,6 +111,27 @@ def _bind(lib):
         "mdcn_abi_version": ([], ctypes.c_int32),
         "mdcn_describe_plan": ([_vp, ctypes.c_int, _i64p, ctypes.c_size_t, ctypes.c_char_p,
                                 ctypes.c_size_t], ctypes.c_int),
+        "mdcn_rotary_create": ([ctypes.c_int32, ctypes.c_int32, _i32p, ctypes.c_double,
+                                ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                ctypes.POINTER(_vp)], ctypes.c_int),
+        "mdcn_rotary_destroy": ([_vp], None),
+        "mdcn_rotate": ([_vp, ctypes.c_int, _i64p, _vp, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp],
+                        ctypes.c_int),
+        "mdcn_norm_rotate": ([_vp, ctypes.c_int, _i64p, _vp, _vp, _vp, _vp, _vp, ctypes.c_float,
+                              _vp, _vp, _vp], ctypes.c_int),
+        "mdcn_norm_rotate_backward_workspace_bytes": ([_vp, ctypes.c_int64, _szp], ctypes.c_int),
+        "mdcn_norm_rotate_backward": ([_vp, ctypes.c_int, _i64p, _vp, _vp, _vp, _vp, _vp,
+                                       ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       ctypes.c_size_t, _vp], ctypes.c_int),
+        "mdcn_attention_create": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_float, ctypes.POINTER(_vp)], ctypes.c_int),
+        "mdcn_attention_destroy": ([_vp], None),
+        "mdcn_attend_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
+        "mdcn_attend": ([_vp, ctypes.c_int, _i64p] + [_vp] * 9 + [ctypes.c_size_t, _vp],
+                        ctypes.c_int),
+        "mdcn_attend_backward_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
+        "mdcn_attend_backward": ([_vp, ctypes.c_int, _i64p] + [_vp] * 13 + [ctypes.c_size_t, _vp],
+                                 ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
