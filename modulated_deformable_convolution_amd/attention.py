@@ -11,13 +11,28 @@ kernels.  Calls enqueue work and return; they raise MdcnError on bad arguments.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+
+import torch
 
 from . import mdcn as _m
 from .mdcn import MDCN_E_ATTR, MDCN_E_NULL, MDCN_E_SHAPE, MdcnError
 
 _i64 = ctypes.c_int64
 _CACHED_CALLS = 64
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _raw_stream(index):
+    """Handle of torch's current stream on a device (0, the default stream, as None)."""
+    return torch.cuda.current_stream(index).cuda_stream or None
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    # the same handle without building a Stream object (a microsecond a call)
+    def _raw_stream(index, _get=torch._C._cuda_getCurrentRawStream):  # noqa: F811
+        return _get(index) or None
 
 
 class Rotary:
@@ -99,7 +114,6 @@ def _device_tensors(where, *tensors):
 
 
 def _check_ints(where, name, t, like, shape):
-    import torch
     if t.dtype != torch.int32 or t.device != like.device or tuple(t.shape) != shape:
         _fail(where, "%s must be int32 of shape %s on the tensors' device" % (name, shape))
     if shape[-1] > 1 and t.stride(-1) != 1:
@@ -120,27 +134,32 @@ def _remember(calls, key, value):
     return value
 
 
-def _rotary_dims(op, where, q, k, positions, more):
-    """ctypes dims of a call on q, k and further views, checked once per
-    combination of shapes and strides."""
-    key = (q.dtype, q.shape, q.stride(), k.shape, k.stride(), positions.dtype, positions.shape,
-           positions.stride(), q.device, k.device, k.dtype, positions.device,
-           tuple((t.dtype, t.device, t.shape, t.stride()) for _, t, _ in more))
-    dims = op.calls.get(key)
-    if dims is None:
-        if q.dim() != 3 or k.dim() != 3:
-            _fail(where, "q and k must be [tokens, heads, dim]")
-        t = q.shape[0]
-        _check_view(where, "q", q, q, (t, q.shape[1], op.dim))
-        _check_view(where, "k", k, q, (t, k.shape[1], op.dim))
-        _check_ints(where, "positions", positions, q, (len(op.axes), t))
-        vals = [t, q.shape[1], k.shape[1], positions.stride(0) if len(op.axes) > 1 else t]
-        vals += _strides(q) + _strides(k)
-        for name, view, like in more:
-            _check_view(where, name, view, q, tuple(like.shape))
-            vals += _strides(view)
-        dims = _remember(op.calls, key, (_i64 * len(vals))(*vals))
-    return dims
+def _sig(t):
+    """What a call's checks and dims depend on."""
+    return (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _rotary_call(op, where, q, k, positions, more):
+    """(dtype code, ctypes dims) of a call on q, k and further views."""
+    if q.dim() != 3 or k.dim() != 3:
+        _fail(where, "q and k must be [tokens, heads, dim]")
+    t = q.shape[0]
+    _check_view(where, "q", q, q, (t, q.shape[1], op.dim))
+    _check_view(where, "k", k, q, (t, k.shape[1], op.dim))
+    _check_ints(where, "positions", positions, q, (len(op.axes), t))
+    vals = [t, q.shape[1], k.shape[1], positions.stride(0) if len(op.axes) > 1 else t]
+    vals += _strides(q) + _strides(k)
+    for name, view, like in more:
+        _check_view(where, name, view, q, tuple(like.shape))
+        vals += _strides(view)
+    return _m.dtype_code(q.dtype), (_i64 * len(vals))(*vals)
+
+
+def _stream_of(stream, t):
+    """(handle, context or None) to allocate and launch with; see mdcn._alloc_stream."""
+    if stream is None:
+        return _raw_stream(t.get_device()), None
+    return _m._alloc_stream(stream, t.device, True)
 
 
 def _check_gain(where, op, q, *gains):
@@ -152,19 +171,29 @@ def _check_gain(where, op, q, *gains):
 
 # ---------------------------------------------------------------- rotary positions
 
+def _outputs(stream, q, k, q_out, k_out):
+    """(stream handle, q_out, k_out), allocated where not given."""
+    stream, ctx = _stream_of(stream, q)
+    if q_out is None or k_out is None:
+        with ctx or _NO_CONTEXT:
+            q_out = torch.empty_like(q) if q_out is None else q_out
+            k_out = torch.empty_like(k) if k_out is None else k_out
+    return stream, q_out, k_out
+
+
 def _rotate(op, q, k, positions, inverse, q_out, k_out, stream, where):
-    import torch
     _device_tensors(where, q, k, positions)
-    stream, ctx = _m._alloc_stream(stream, q.device, q_out is None or k_out is None)
-    with ctx:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        dims = _rotary_dims(op, where, q, k, positions, (("q_out", q_out, q), ("k_out", k_out, k)))
-        _m._check(_m._lib.mdcn_rotate(op.handle, _m.dtype_code(q.dtype), dims, q.data_ptr(),
-                                      k.data_ptr(), positions.data_ptr(), inverse,
-                                      q_out.data_ptr(), k_out.data_ptr(), stream or None), where)
+    stream, q_out, k_out = _outputs(stream, q, k, q_out, k_out)
+    key = (_sig(q), _sig(k), _sig(positions), _sig(q_out), _sig(k_out))
+    call = op.calls.get(key)
+    if call is None:
+        call = _remember(op.calls, key, _rotary_call(
+            op, where, q, k, positions, (("q_out", q_out, q), ("k_out", k_out, k))))
+    st = _m._lib.mdcn_rotate(op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(),
+                             positions.data_ptr(), inverse, q_out.data_ptr(), k_out.data_ptr(),
+                             stream)
+    if st:
+        _m._check(st, where)
     return q_out, k_out
 
 
@@ -183,90 +212,92 @@ def rotate_backward(op: Rotary, grad_q, grad_k, positions, q_out=None, k_out=Non
 def norm_rotate(op: Rotary, q, k, positions, q_gain, k_gain, eps: float = 1e-6, q_out=None,
                 k_out=None, stream=None):
     """rotate of the RMS norm of each head times a gain [dim]."""
-    import torch
     where = "norm_rotate"
     _device_tensors(where, q, k, positions, q_gain, k_gain)
-    stream, ctx = _m._alloc_stream(stream, q.device, q_out is None or k_out is None)
-    with ctx:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        dims = _rotary_dims(op, where, q, k, positions, (("q_out", q_out, q), ("k_out", k_out, k)))
+    stream, q_out, k_out = _outputs(stream, q, k, q_out, k_out)
+    key = (_sig(q), _sig(k), _sig(positions), _sig(q_out), _sig(k_out), _sig(q_gain), _sig(k_gain))
+    call = op.calls.get(key)
+    if call is None:
         _check_gain(where, op, q, q_gain, k_gain)
-        _m._check(_m._lib.mdcn_norm_rotate(
-            op.handle, _m.dtype_code(q.dtype), dims, q.data_ptr(), k.data_ptr(),
-            positions.data_ptr(), q_gain.data_ptr(), k_gain.data_ptr(), eps, q_out.data_ptr(),
-            k_out.data_ptr(), stream or None), where)
+        call = _remember(op.calls, key, _rotary_call(
+            op, where, q, k, positions, (("q_out", q_out, q), ("k_out", k_out, k))))
+    st = _m._lib.mdcn_norm_rotate(op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(),
+                                  positions.data_ptr(), q_gain.data_ptr(), k_gain.data_ptr(), eps,
+                                  q_out.data_ptr(), k_out.data_ptr(), stream)
+    if st:
+        _m._check(st, where)
     return q_out, k_out
 
 
 def norm_rotate_backward(op: Rotary, q, k, positions, q_gain, k_gain, grad_q_out, grad_k_out,
                          eps: float = 1e-6, workspace=None, stream=None):
     """Gradients of norm_rotate: a dict of q, k, q_gain, k_gain."""
-    import torch
     where = "norm_rotate_backward"
     _device_tensors(where, q, k, positions, q_gain, k_gain, grad_q_out, grad_k_out)
-    stream, ctx = _m._alloc_stream(stream, q.device, True)
-    with ctx:
-        g = {"q": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-             "k": torch.empty(k.shape, dtype=k.dtype, device=k.device),
-             "q_gain": torch.empty(op.dim, dtype=q.dtype, device=q.device),
-             "k_gain": torch.empty(op.dim, dtype=q.dtype, device=q.device)}
-        dims = _rotary_dims(op, where, q, k, positions,
-                            (("grad_q_out", grad_q_out, q), ("grad_k_out", grad_k_out, k),
-                             ("grad_q", g["q"], q), ("grad_k", g["k"], k)))
-        _check_gain(where, op, q, q_gain, k_gain)
-        lib = _m._lib
-        if workspace is None:
+    lib = _m._lib
+    stream, ctx = _stream_of(stream, q)
+    with ctx or _NO_CONTEXT:
+        dq, dk = torch.empty_like(q), torch.empty_like(k)
+        dq_gain, dk_gain = torch.empty_like(q_gain), torch.empty_like(k_gain)
+        key = (_sig(q), _sig(k), _sig(positions), _sig(q_gain), _sig(k_gain), _sig(grad_q_out),
+               _sig(grad_k_out), "backward")
+        call = op.calls.get(key)
+        if call is None:
+            _check_gain(where, op, q, q_gain, k_gain)
+            call = _rotary_call(op, where, q, k, positions,
+                                (("grad_q_out", grad_q_out, q), ("grad_k_out", grad_k_out, k),
+                                 ("grad_q", dq, q), ("grad_k", dk, k)))
             n = ctypes.c_size_t()
             _m._check(lib.mdcn_norm_rotate_backward_workspace_bytes(op.handle, q.shape[0],
                                                                     ctypes.byref(n)), where)
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-        _m._check(lib.mdcn_norm_rotate_backward(
-            op.handle, _m.dtype_code(q.dtype), dims, q.data_ptr(), k.data_ptr(),
-            positions.data_ptr(), q_gain.data_ptr(), k_gain.data_ptr(), eps,
-            grad_q_out.data_ptr(), grad_k_out.data_ptr(), g["q"].data_ptr(), g["k"].data_ptr(),
-            g["q_gain"].data_ptr(), g["k_gain"].data_ptr(), workspace.data_ptr(),
-            workspace.numel(), stream or None), where)
-    return g
+            call = _remember(op.calls, key, call + (n.value,))
+        if workspace is None:
+            workspace = torch.empty(call[2], dtype=torch.uint8, device=q.device)
+    st = lib.mdcn_norm_rotate_backward(
+        op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), positions.data_ptr(),
+        q_gain.data_ptr(), k_gain.data_ptr(), eps, grad_q_out.data_ptr(), grad_k_out.data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dq_gain.data_ptr(), dk_gain.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), stream)
+    if st:
+        _m._check(st, where)
+    return {"q": dq, "k": dk, "q_gain": dq_gain, "k_gain": dk_gain}
 
 
 # ---------------------------------------------------------------- attention
 
-def _attend_dims(op, where, q, k, v, out, cu_q, cu_k, used_k, grads):
-    """(ctypes dims, workspace bytes) of a call, checked once per combination
-    of shapes and strides."""
-    views = (q, k, v, out) + grads
-    ints = (cu_q, cu_k) + (() if used_k is None else (used_k,))
-    key = tuple((t.dtype, t.device, t.shape, t.stride()) for t in views + ints)
-    call = op.calls.get(key)
-    if call is None:
-        if q.dim() != 3 or k.dim() != 3:
-            _fail(where, "q and k must be [tokens, heads, dim]")
-        q_shape = (q.shape[0], op.q_heads, op.dim)
-        k_shape = (k.shape[0], op.k_heads, op.dim)
-        for name, t, shape in zip(("q", "k", "v", "out", "grad_out", "grad_q", "grad_k", "grad_v"),
-                                  views, (q_shape, k_shape, k_shape, q_shape, q_shape, q_shape,
-                                          k_shape, k_shape)):
-            _check_view(where, name, t, q, shape)
-        if cu_q.dim() != 1 or cu_q.shape[0] < 1:
-            _fail(where, "cu_q must hold batch + 1 offsets")
-        batch = cu_q.shape[0] - 1
-        _check_ints(where, "cu_q", cu_q, q, (batch + 1,))
-        _check_ints(where, "cu_k", cu_k, q, (batch + 1,))
-        if used_k is not None:
-            _check_ints(where, "used_k", used_k, q, (batch,))
-        vals = [batch, q.shape[0], k.shape[0]]
-        for t in views:
-            vals += _strides(t)
-        dims = (_i64 * len(vals))(*vals)
-        n = ctypes.c_size_t()
-        lib = _m.library()
-        fn = lib.mdcn_attend_backward_workspace_bytes if grads else lib.mdcn_attend_workspace_bytes
-        _m._check(fn(op.handle, _m.dtype_code(q.dtype), dims, ctypes.byref(n)), where)
-        call = _remember(op.calls, key, (dims, n.value))
-    return call
+def _attend_call(op, where, views, cu_q, cu_k, used_k, grads):
+    """(dtype code, ctypes dims, workspace bytes) of a call."""
+    q, k = views[:2]
+    if q.dim() != 3 or k.dim() != 3:
+        _fail(where, "q and k must be [tokens, heads, dim]")
+    q_shape = (q.shape[0], op.q_heads, op.dim)
+    k_shape = (k.shape[0], op.k_heads, op.dim)
+    for name, t, shape in zip(("q", "k", "v", "out", "grad_out", "grad_q", "grad_k", "grad_v"),
+                              views, (q_shape, k_shape, k_shape, q_shape, q_shape, q_shape,
+                                      k_shape, k_shape)):
+        _check_view(where, name, t, q, shape)
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        _fail(where, "cu_q must hold batch + 1 offsets")
+    batch = cu_q.shape[0] - 1
+    _check_ints(where, "cu_q", cu_q, q, (batch + 1,))
+    _check_ints(where, "cu_k", cu_k, q, (batch + 1,))
+    if used_k is not None:
+        _check_ints(where, "used_k", used_k, q, (batch,))
+    vals = [batch, q.shape[0], k.shape[0]]
+    for t in views:
+        vals += _strides(t)
+    code, dims = _m.dtype_code(q.dtype), (_i64 * len(vals))(*vals)
+    n = ctypes.c_size_t()
+    lib = _m.library()
+    fn = lib.mdcn_attend_backward_workspace_bytes if grads else lib.mdcn_attend_workspace_bytes
+    _m._check(fn(op.handle, code, dims, ctypes.byref(n)), where)
+    return code, dims, n.value
+
+
+def _check_lse(where, op, q, lse):
+    if lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous() or \
+            tuple(lse.shape) != (op.q_heads, q.shape[0]):
+        _fail(where, "lse must be contiguous fp32 [q_heads, q_tokens]")
 
 
 def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, workspace=None,
@@ -276,49 +307,55 @@ def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, 
     sequences.  used_k (int32 [batch]): the keys that sequence b's part of k and
     v holds so far, for a cache with room.  Returns (out, lse) with lse fp32
     [q_heads, q_tokens]."""
-    import torch
     _device_tensors("attend", q, k, v, cu_q, cu_k)
-    stream, ctx = _m._alloc_stream(stream, q.device, True)
-    with ctx:
+    stream, ctx = _stream_of(stream, q)
+    with ctx or _NO_CONTEXT:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q)
         if lse is None:
             lse = torch.empty((op.q_heads, q.shape[0]), dtype=torch.float32, device=q.device)
-        elif lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous() or \
-                tuple(lse.shape) != (op.q_heads, q.shape[0]):
-            _fail("attend", "lse must be contiguous fp32 [q_heads, q_tokens]")
-        dims, need = _attend_dims(op, "attend", q, k, v, out, cu_q, cu_k, used_k, ())
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _m._check(_m._lib.mdcn_attend(
-            op.handle, _m.dtype_code(q.dtype), dims, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            cu_q.data_ptr(), cu_k.data_ptr(), None if used_k is None else used_k.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), stream or None), "attend")
+        else:
+            _check_lse("attend", op, q, lse)
+        key = (_sig(q), _sig(k), _sig(v), _sig(out), _sig(cu_q), _sig(cu_k),
+               None if used_k is None else _sig(used_k))
+        call = op.calls.get(key)
+        if call is None:
+            call = _remember(op.calls, key, _attend_call(op, "attend", (q, k, v, out), cu_q, cu_k,
+                                                         used_k, False))
+        if workspace is None and call[2]:
+            workspace = torch.empty(call[2], dtype=torch.uint8, device=q.device)
+    st = _m._lib.mdcn_attend(
+        op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+        cu_k.data_ptr(), None if used_k is None else used_k.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), stream)
+    if st:
+        _m._check(st, "attend")
     return out, lse
 
 
 def attend_backward(op: Attention, q, k, v, out, lse, grad_out, cu_q, cu_k, used_k=None,
                     workspace=None, stream=None):
     """Gradients of attend: a dict of q, k, v.  out and lse are the forward's."""
-    import torch
     where = "attend_backward"
     _device_tensors(where, q, k, v, out, lse, grad_out, cu_q, cu_k)
-    if lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous() or \
-            tuple(lse.shape) != (op.q_heads, q.shape[0]):
-        _fail(where, "lse must be contiguous fp32 [q_heads, q_tokens]")
-    stream, ctx = _m._alloc_stream(stream, q.device, True)
-    with ctx:
-        g = {"q": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-             "k": torch.empty(k.shape, dtype=k.dtype, device=k.device),
-             "v": torch.empty(v.shape, dtype=v.dtype, device=v.device)}
-        dims, need = _attend_dims(op, where, q, k, v, out, cu_q, cu_k, used_k,
-                                  (grad_out, g["q"], g["k"], g["v"]))
+    _check_lse(where, op, q, lse)
+    stream, ctx = _stream_of(stream, q)
+    with ctx or _NO_CONTEXT:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        key = (_sig(q), _sig(k), _sig(v), _sig(out), _sig(grad_out), _sig(cu_q), _sig(cu_k),
+               None if used_k is None else _sig(used_k), "backward")
+        call = op.calls.get(key)
+        if call is None:
+            call = _remember(op.calls, key, _attend_call(
+                op, where, (q, k, v, out, grad_out, dq, dk, dv), cu_q, cu_k, used_k, True))
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _m._check(_m._lib.mdcn_attend_backward(
-            op.handle, _m.dtype_code(q.dtype), dims, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
-            None if used_k is None else used_k.data_ptr(), g["q"].data_ptr(), g["k"].data_ptr(),
-            g["v"].data_ptr(), workspace.data_ptr(), workspace.numel(), stream or None), where)
-    return g
+            workspace = torch.empty(call[2], dtype=torch.uint8, device=q.device)
+    st = _m._lib.mdcn_attend_backward(
+        op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), grad_out.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+        None if used_k is None else used_k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+        dv.data_ptr(), workspace.data_ptr(), workspace.numel(), stream)
+    if st:
+        _m._check(st, where)
+    return {"q": dq, "k": dk, "v": dv}

@@ -63,12 +63,45 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane)
     return v;
 }
 
-__device__ __forceinline__ int64_t total_units(const AttendArgs &a, int lane)
+// The units of 64 sequences, one per lane: its own and those up to it.
+struct Chunk {
+    Span span;
+    int64_t mine, upto;
+
+    __device__ __forceinline__ void load(const AttendArgs &a, int b0, int lane)
+    {
+        span = {};
+        mine = 0;
+        if (b0 + lane < a.batch) {
+            span = span_of(a, b0 + lane);
+            mine = units_of(a, span).all;
+        }
+        upto = scan64(mine, lane);
+    }
+};
+
+// All units of the batch; `first` is the chunk of its first 64 sequences.
+__device__ __forceinline__ int64_t total_units(const AttendArgs &a, const Chunk &first, int lane)
 {
-    int64_t sum = 0;
-    for (int b = lane; b < a.batch; b += 64)
-        sum += units_of(a, span_of(a, b)).all;
-    return shfl64(scan64(sum, lane), 63);
+    int64_t sum = shfl64(first.upto, 63);
+    if (a.batch > 64) {
+        int64_t more = 0;
+        for (int b = 64 + lane; b < a.batch; b += 64)
+            more += units_of(a, span_of(a, b)).all;
+        sum += shfl64(scan64(more, lane), 63);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ Span span_in(const Chunk &c, int l)
+{
+    Span s;
+    s.q0 = __builtin_amdgcn_readlane(c.span.q0, l);
+    s.lq = __builtin_amdgcn_readlane(c.span.lq, l);
+    s.k0 = __builtin_amdgcn_readlane(c.span.k0, l);
+    s.lk = __builtin_amdgcn_readlane(c.span.lk, l);
+    s.k_all = __builtin_amdgcn_readlane(c.span.k_all, l);
+    return s;
 }
 
 // Workgroups that share the units: enough units for all waves of each.
@@ -97,7 +130,9 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
     const int group = a.q_heads / a.k_heads;
     const float c = a.scale * kLog2e;
 
-    const int64_t units = total_units(a, lane);
+    Chunk chunk;
+    chunk.load(a, 0, lane);
+    const int64_t units = total_units(a, chunk, lane);
     const int64_t share = sharers(units, a.workers, NW);
     if (int64_t(blockIdx.x) >= share)
         return;
@@ -112,15 +147,14 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
 
     int64_t base = 0;
     for (int b0 = 0; b0 < a.batch && base < u_end; b0 += 64) {
-        const int64_t mine = b0 + lane < a.batch ? units_of(a, span_of(a, b0 + lane)).all : 0;
-        const int64_t upto = scan64(mine, lane);
-        for (int i = 0; i < 64 && b0 + i < a.batch; ++i) {
-            const int64_t s_end = base + shfl64(upto, i);
-            const int64_t s_begin = s_end - shfl64(mine, i);
-            if (s_end <= u_begin || s_begin >= u_end)
-                continue;
-            const int b = b0 + i;
-            const Span sp = span_of(a, b);
+        if (b0 > 0)
+            chunk.load(a, b0, lane);
+        const int64_t s_end_l = base + chunk.upto, s_begin_l = s_end_l - chunk.mine;
+        uint64_t mine = __ballot(chunk.mine > 0 && s_end_l > u_begin && s_begin_l < u_end);
+        for (; mine; mine &= mine - 1) {
+            const int i = __builtin_ctzll(mine);
+            const int64_t s_end = shfl64(s_end_l, i), s_begin = shfl64(s_begin_l, i);
+            const Span sp = span_in(chunk, i);
             const Units un = units_of(a, sp);
             const int shift = sp.lk - sp.lq;
             const int64_t from = u_begin > s_begin ? u_begin : s_begin;
@@ -258,73 +292,111 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                 __syncthreads();
             }
         }
-        base += shfl64(upto, 63);
+        base += shfl64(chunk.upto, 63);
     }
 }
 
-// One wave per (query token, head): joins the parts that several workgroups
-// left of its item, if there are several.
+// One workgroup per (query token, head): joins the parts that several
+// workgroups left of its item, if there are several.  Each wave takes every
+// fourth part, four at a time so that their reads overlap.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
 {
     constexpr int NW = split_waves<T, DP>();
     constexpr int PART = DP + 2;
-    const int lane = threadIdx.x & 63;
-    const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (w >= int64_t(a.q_tokens) * a.q_heads)
-        return;
-    const int token = int(w / a.q_heads), head = int(w % a.q_heads);
+    constexpr int AT_ONCE = 4;
+    __shared__ float stat[4][2];
+    __shared__ float outs[4][DP];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int token = int(blockIdx.x / a.q_heads), head = int(blockIdx.x % a.q_heads);
     const int group = a.q_heads / a.k_heads;
+    const float c = a.scale * kLog2e;
 
-    const int64_t units = total_units(a, lane);
+    Chunk chunk;
+    chunk.load(a, 0, lane);
+    const int64_t units = total_units(a, chunk, lane);
     const int64_t share = sharers(units, a.workers, NW);
     int64_t base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
-        Span mine = {};
-        int64_t n = 0;
-        if (b0 + lane < a.batch) {
-            mine = span_of(a, b0 + lane);
-            n = units_of(a, mine).all;
+        if (b0 > 0)
+            chunk.load(a, b0, lane);
+        const uint64_t here =
+            __ballot(token >= chunk.span.q0 && token < chunk.span.q0 + chunk.span.lq);
+        if (!here) {
+            base += shfl64(chunk.upto, 63);
+            continue;
         }
-        const int64_t upto = scan64(n, lane);
-        const uint64_t here = __ballot(token >= mine.q0 && token < mine.q0 + mine.lq);
-        if (here) {
-            const int l = __builtin_ctzll(here);
-            const Span sp = span_of(a, b0 + l);
-            const Units un = units_of(a, sp);
-            const int64_t packed = int64_t(token - sp.q0) * group + head % group;
-            const int tile = int(packed / kTileRows), r = int(packed % kTileRows);
-            const int64_t first = base + shfl64(upto, l) - shfl64(n, l) +
-                                  (int64_t(head / group) * un.tiles + tile) * un.keys;
-            const int64_t i0 = ((first + 1) * share - 1) / units;
-            const int64_t i1 = ((first + un.keys) * share - 1) / units;
-            if (i0 == i1)
-                return;
-            const float c = a.scale * kLog2e;
-            float m = -INFINITY, sum = 0.0f, o[2] = {0.0f, 0.0f};
-            for (int64_t i = i0; i <= i1; ++i) {
-                const float *p = a.partial + (2 * i + (i == i0 ? 1 : 0)) * (kTileRows * PART) +
-                                 r * PART;
-                const float pm = p[0], up = fmaxf(m, pm);
-                const float f = m == up ? 1.0f : exp2f((m - up) * c);
-                const float g = pm == up ? 1.0f : exp2f((pm - up) * c);
-                sum = sum * f + p[1] * g;
-                o[0] = o[0] * f + (lane < DP ? p[2 + lane] * g : 0.0f);
-                if (DP > 64)
-                    o[1] = o[1] * f + (lane + 64 < DP ? p[2 + 64 + lane] * g : 0.0f);
-                m = up;
-            }
-            T *dst = reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.out, token, head)));
+        const int l = __builtin_ctzll(here);
+        const Span sp = span_in(chunk, l);
+        const Units un = units_of(a, sp);
+        const int64_t packed = int64_t(token - sp.q0) * group + head % group;
+        const int tile = int(packed / kTileRows), r = int(packed % kTileRows);
+        const int64_t first = base + shfl64(chunk.upto, l) - shfl64(chunk.mine, l) +
+                              (int64_t(head / group) * un.tiles + tile) * un.keys;
+        const int64_t i0 = ((first + 1) * share - 1) / units;
+        const int64_t i1 = ((first + un.keys) * share - 1) / units;
+        if (i0 == i1)
+            return;                              // finished where it was computed
+        float m = -INFINITY, sum = 0.0f, o[2] = {0.0f, 0.0f};
+        for (int64_t i = i0 + wave; i <= i1; i += 4 * AT_ONCE) {
+            float pm[AT_ONCE], ps[AT_ONCE], po[AT_ONCE][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (lane + 64 * k < a.dim)
-                    dst[lane + 64 * k] = from_f32<T>(sum == 0.0f ? 0.0f : o[k] / sum);
-            if (lane == 0)
-                a.lse[int64_t(head) * a.q_tokens + token] =
-                    sum == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(sum));
-            return;
+            for (int n = 0; n < AT_ONCE; ++n) {
+                const int64_t j = i + 4 * n;
+                const bool ok = j <= i1;
+                const float *p = a.partial +
+                                 (2 * (ok ? j : i0) + (!ok || j == i0 ? 1 : 0)) *
+                                     (kTileRows * PART) + r * PART;
+                pm[n] = ok ? p[0] : -INFINITY;
+                ps[n] = ok ? p[1] : 0.0f;
+                po[n][0] = ok && lane < DP ? p[2 + lane] : 0.0f;
+                po[n][1] = ok && lane + 64 < DP ? p[66 + lane] : 0.0f;
+            }
+            float up = m;
+#pragma unroll
+            for (int n = 0; n < AT_ONCE; ++n)
+                up = fmaxf(up, pm[n]);
+            const float f = m == up ? 1.0f : exp2f((m - up) * c);
+            sum *= f;
+            o[0] *= f;
+            o[1] *= f;
+#pragma unroll
+            for (int n = 0; n < AT_ONCE; ++n) {
+                const float g = pm[n] == up ? 1.0f : exp2f((pm[n] - up) * c);
+                sum = fmaf(ps[n], g, sum);
+                o[0] = fmaf(po[n][0], g, o[0]);
+                o[1] = fmaf(po[n][1], g, o[1]);
+            }
+            m = up;
         }
-        base += shfl64(upto, 63);
+        if (lane == 0) {
+            stat[wave][0] = m;
+            stat[wave][1] = sum;
+        }
+        if (lane < DP)
+            outs[wave][lane] = o[0];
+        if (lane + 64 < DP)
+            outs[wave][lane + 64] = o[1];
+        __syncthreads();
+        if (int(threadIdx.x) < a.dim) {
+            float top = stat[0][0];
+#pragma unroll
+            for (int w = 1; w < 4; ++w)
+                top = fmaxf(top, stat[w][0]);
+            float total = 0.0f, out = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = stat[w][0] == top ? 1.0f : exp2f((stat[w][0] - top) * c);
+                total = fmaf(stat[w][1], f, total);
+                out = fmaf(outs[w][threadIdx.x], f, out);
+            }
+            reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.out, token, head)))[threadIdx.x] =
+                from_f32<T>(total == 0.0f ? 0.0f : out / total);
+            if (threadIdx.x == 0)
+                a.lse[int64_t(head) * a.q_tokens + token] =
+                    total == 0.0f ? -INFINITY : fmaf(top, a.scale, logf(total));
+        }
+        return;
     }
 }
 
@@ -335,10 +407,10 @@ hipError_t launch(AttendArgs a, hipStream_t s)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int64_t waves = int64_t(a.q_tokens) * a.q_heads;
-    if ((waves + 3) / 4 > INT32_MAX)
+    const int64_t rows = int64_t(a.q_tokens) * a.q_heads;
+    if (rows > INT32_MAX)
         return hipErrorInvalidValue;
-    attend_join_kernel<T, DP><<<uint32_t((waves + 3) / 4), 256, 0, s>>>(a);
+    attend_join_kernel<T, DP><<<uint32_t(rows), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

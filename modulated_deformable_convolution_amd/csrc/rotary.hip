@@ -11,9 +11,8 @@
 //
 // Angles: position * frequency in turns is taken in double and reduced to
 // [-1/2, 1/2] there, so far positions (10^6 and more) lose nothing; sine and
-// cosine of the rest in fp32.  They are computed once per token and lane and
-// used for all heads of the token: at 40 heads the ~320 instructions of a lane's
-// 8 pairs are a tenth of the work on the heads.
+// cosine of the rest in fp32.  A wave computes the pairs of a token once, one
+// or two per lane, and shares them through LDS for all heads of the token.
 //
 // A head is spread over G lanes (a power of two), each holding units of V
 // values from the first channels of its pairs and the V second channels, so
@@ -30,37 +29,61 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kMaxBackwardBlocks = 1024;
 
-template <typename T, int V> struct alignas(V * sizeof(T)) Pack {
+template <typename T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Pack {
     T e[V];
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void load_pack(float (&o)[V], const T *p)
-{
-    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V> *>(p);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        o[j] = to_f32(v.e[j]);
-}
+// A unit as it lies in memory.
+template <typename T, int V> struct Unit {
+    Pack<T, V> lo, hi;
 
-template <typename T, int V>
-__device__ __forceinline__ void store_pack(T *p, const float (&o)[V])
-{
-    Pack<T, V> v;
+    __device__ __forceinline__ void load(const T *p, int lo_at, int hi_at)
+    {
+        lo = *reinterpret_cast<const Pack<T, V> *>(p + lo_at);
+        hi = *reinterpret_cast<const Pack<T, V> *>(p + hi_at);
+    }
+
+    __device__ __forceinline__ void store(T *p, int lo_at, int hi_at) const
+    {
+        *reinterpret_cast<Pack<T, V> *>(p + lo_at) = lo;
+        *reinterpret_cast<Pack<T, V> *>(p + hi_at) = hi;
+    }
+
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        v.e[j] = from_f32<T>(o[j]);
-    *reinterpret_cast<Pack<T, V> *>(p) = v;
-}
+        for (int j = 0; j < V; ++j)
+            lo.e[j] = hi.e[j] = T(0.0f);
+    }
+
+    __device__ __forceinline__ void get(float (&x)[2 * V]) const
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            x[j] = to_f32(lo.e[j]);
+            x[V + j] = to_f32(hi.e[j]);
+        }
+    }
+
+    __device__ __forceinline__ void set(const float (&x)[2 * V])
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            lo.e[j] = from_f32<T>(x[j]);
+            hi.e[j] = from_f32<T>(x[V + j]);
+        }
+    }
+};
 
 // Unit u of a head: V pairs, as the channel offsets of its two vectors.  For
 // adjacent pairs the two vectors are the halves of 2V consecutive channels.
-template <int V>
-__device__ __forceinline__ void unit_offsets(int u, int pairs, bool adjacent, int &lo, int &hi)
+template <int V, bool ADJ>
+__device__ __forceinline__ void unit_offsets(int u, int pairs, int &lo, int &hi)
 {
     const int turned = pairs / V;
-    if (adjacent) {
+    if (ADJ) {
         lo = u * 2 * V;
         hi = lo + V;
     } else if (u < turned) {
@@ -73,13 +96,13 @@ __device__ __forceinline__ void unit_offsets(int u, int pairs, bool adjacent, in
 }
 
 // x[0..V) and x[V..2V) are a unit's two vectors.
-template <int V>
+template <int V, bool ADJ>
 __device__ __forceinline__ void turn_unit(float (&x)[2 * V], const float (&c)[V],
-                                          const float (&s)[V], bool adjacent)
+                                          const float (&s)[V])
 {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        if (adjacent) {
+        if (ADJ) {
             const float a = x[2 * j], b = x[2 * j + 1];
             x[2 * j] = a * c[j] - b * s[j];
             x[2 * j + 1] = a * s[j] + b * c[j];
@@ -91,54 +114,41 @@ __device__ __forceinline__ void turn_unit(float (&x)[2 * V], const float (&c)[V]
     }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void load_unit(float (&x)[2 * V], const T *p, int lo, int hi)
-{
-    float a[V];
-    load_pack<T, V>(a, p + lo);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        x[j] = a[j];
-    load_pack<T, V>(a, p + hi);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        x[V + j] = a[j];
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_unit(T *p, const float (&x)[2 * V], int lo, int hi)
-{
-    float a[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        a[j] = x[j];
-    store_pack<T, V>(p + lo, a);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        a[j] = x[V + j];
-    store_pack<T, V>(p + hi, a);
-}
+// Cosines and sines of one token's pairs, in LDS: each lane computes every
+// 64th pair and all read what their units need, (1, 0) past the turned
+// pairs.  A wave writes and reads its own table only.
+struct Angles {
+    alignas(16) float c[kMaxRotaryDim / 2], s[kMaxRotaryDim / 2];
+};
 
 template <int U, int V>
-__device__ __forceinline__ void angles(float (&c)[U][V], float (&s)[U][V], const RotaryArgs &a,
-                                       int64_t t, int lane_in_head, int group)
+__device__ __forceinline__ void angles(float (&c)[U][V], float (&s)[U][V], Angles &table,
+                                       const RotaryArgs &a, int64_t t, int lane, const int (&at)[U])
 {
+    __builtin_amdgcn_wave_barrier();                 // the last token's reads come first
+    for (int i = lane; i < a.dim / 2; i += 64) {
+        float cv = 1.0f, sv = 0.0f;
+        if (i < a.pairs) {
+            const int p = a.positions[a.table.axis[i] * a.axis_stride + t];
+            double turns = double(p) * a.table.turns[i];
+            turns -= rint(turns);
+            sincospif(float(2.0 * turns), &sv, &cv);
+        }
+        table.c[i] = cv;
+        table.s[i] = a.inverse ? -sv : sv;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+        const Pack<float, V> cv = *reinterpret_cast<const Pack<float, V> *>(table.c + at[u]);
+        const Pack<float, V> sv = *reinterpret_cast<const Pack<float, V> *>(table.s + at[u]);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int i = (lane_in_head + u * group) * V + j;
-            c[u][j] = 1.0f;
-            s[u][j] = 0.0f;
-            if (i < a.pairs) {
-                const int p = a.positions[a.table.axis[i] * a.axis_stride + t];
-                double turns = double(p) * a.table.turns[i];
-                turns -= rint(turns);
-                sincospif(float(2.0 * turns), &s[u][j], &c[u][j]);
-                if (a.inverse)
-                    s[u][j] = -s[u][j];
-            }
+            c[u][j] = cv.e[j];
+            s[u][j] = sv.e[j];
         }
+    }
 }
 
 __device__ __forceinline__ float group_sum(float v, int group)
@@ -150,10 +160,11 @@ __device__ __forceinline__ float group_sum(float v, int group)
 
 // Forward (rotate, norm_rotate): one wave takes `per_wave` rounds of one
 // token's heads, 64 / G heads a round.
-template <typename T, int V, int U, bool NORM>
+template <typename T, int V, int U, bool ADJ, bool NORM>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int group, int units,
                                                           int per_wave, int waves_per_token)
 {
+    __shared__ Angles table[kWaves];
     const int lane = threadIdx.x & 63;
     const int64_t w = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
     const int64_t t = w / waves_per_token;
@@ -163,38 +174,60 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int grou
     const int li = lane & (group - 1);
     const int slots = 64 / group;
     const int rows = a.q_heads + a.k_heads;
-    const bool adjacent = a.adjacent != 0;
 
-    int lo[U], hi[U];
+    int lo[U], hi[U], at[U];                         // at: the unit's first pair
     bool ok[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int unit = li + u * group;
         ok[u] = unit < units;
-        unit_offsets<V>(ok[u] ? unit : 0, a.pairs, adjacent, lo[u], hi[u]);
+        at[u] = ok[u] ? unit * V : 0;
+        unit_offsets<V, ADJ>(ok[u] ? unit : 0, a.pairs, lo[u], hi[u]);
     }
-    float c[U][V], s[U][V];
-    angles<U, V>(c, s, a, t, li, group);
 
-    const float inv_dim = 1.0f / float(a.dim);
-    const int r_end = min(rows, (part + 1) * per_wave * slots);
-    for (int r0 = part * per_wave * slots; r0 < r_end; r0 += slots) {
-        const int r = r0 + lane / group;
-        const bool live = r < rows;
+    // The heads of a round are read one round ahead, the first before the
+    // angles are computed.
+    auto fetch = [&](Unit<T, V>(&x)[U], int r) {
         const bool is_q = r < a.q_heads;
         const Heads &in = is_q ? a.q : a.k;
-        const Heads &out = is_q ? a.oq : a.ok;
-        const int h = live ? (is_q ? r : r - a.q_heads) : 0;
-        const T *src = static_cast<const T *>(in.data) + t * in.token_stride + h * in.head_stride;
-        float x[U][2 * V];
+        const T *src = static_cast<const T *>(in.data) + t * in.token_stride +
+                       (is_q ? r : r - a.q_heads) * in.head_stride;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int j = 0; j < 2 * V; ++j)
-                x[u][j] = 0.0f;
-            if (live && ok[u])
-                load_unit<T, V>(x[u], src, lo[u], hi[u]);
+            x[u].clear();
+            if (r < rows && ok[u])
+                x[u].load(src, lo[u], hi[u]);
         }
+    };
+    const int r_begin = part * per_wave * slots + lane / group;
+    const int r_end = min(rows, (part + 1) * per_wave * slots);
+    Unit<T, V> next[U], gain_q[U], gain_k[U];
+    fetch(next, r_begin);
+    if (NORM) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            gain_q[u].clear();
+            gain_k[u].clear();
+            if (ok[u] && a.q_heads > 0)
+                gain_q[u].load(static_cast<const T *>(a.q_gain), lo[u], hi[u]);
+            if (ok[u] && a.k_heads > 0)
+                gain_k[u].load(static_cast<const T *>(a.k_gain), lo[u], hi[u]);
+        }
+    }
+    float c[U][V], s[U][V];
+    angles<U, V>(c, s, table[threadIdx.x >> 6], a, t, lane, at);
+
+    const float inv_dim = 1.0f / float(a.dim);
+    // (the group sums need all lanes, also those whose row is past the end)
+    for (int r = r_begin; r - lane / group < r_end; r += slots) {
+        const bool live = r < rows;
+        const bool is_q = r < a.q_heads;
+        float x[U][2 * V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            next[u].get(x[u]);
+        if (r + slots - lane / group < r_end)
+            fetch(next, r + slots);
         if (NORM) {
             float sum = 0.0f;
 #pragma unroll
@@ -204,24 +237,26 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int grou
                     sum += x[u][j] * x[u][j];
             sum = group_sum(sum, group);
             const float inv = 1.0f / sqrtf(sum * inv_dim + a.eps);
-            const T *gain = static_cast<const T *>(is_q ? a.q_gain : a.k_gain);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (live && ok[u]) {
-                    float g[2 * V];
-                    load_unit<T, V>(g, gain, lo[u], hi[u]);
+            for (int u = 0; u < U; ++u) {
+                const Unit<T, V> w = is_q ? gain_q[u] : gain_k[u];
+                float g[2 * V];
+                w.get(g);
 #pragma unroll
-                    for (int j = 0; j < 2 * V; ++j)
-                        x[u][j] *= inv * g[j];
-                }
+                for (int j = 0; j < 2 * V; ++j)
+                    x[u][j] *= inv * g[j];
+            }
         }
+        const Heads &out = is_q ? a.oq : a.ok;
         T *dst = static_cast<T *>(const_cast<void *>(out.data)) + t * out.token_stride +
-                 h * out.head_stride;
+                 (is_q ? r : r - a.q_heads) * out.head_stride;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (live && ok[u]) {
-                turn_unit<V>(x[u], c[u], s[u], adjacent);
-                store_unit<T, V>(dst, x[u], lo[u], hi[u]);
+                turn_unit<V, ADJ>(x[u], c[u], s[u]);
+                Unit<T, V> y;
+                y.set(x[u]);
+                y.store(dst, lo[u], hi[u]);
             }
     }
 }
@@ -230,61 +265,86 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int grou
 // gains' gradients stay in registers (fp32) until the end; they are joined
 // over the block in LDS and written as one row of a.partial.  No atomics: the
 // result does not depend on the order in which blocks run.
-template <typename T, int V, int U>
+template <typename T, int V, int U, bool ADJ>
 __global__ __launch_bounds__(kThreads) void norm_rotate_backward_kernel(RotaryArgs a, int group,
                                                                         int units)
 {
+    __shared__ Angles table[kWaves];
     __shared__ float sums[kWaves][2][kMaxRotaryDim];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & (group - 1);
     const int slots = 64 / group;
     const int rows = a.q_heads + a.k_heads;
-    const bool adjacent = a.adjacent != 0;
     const float inv_dim = 1.0f / float(a.dim);
 
-    int lo[U], hi[U];
+    int lo[U], hi[U], at[U];                         // at: the unit's first pair
     bool ok[U];
     float acc[2][U][2 * V];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int unit = li + u * group;
         ok[u] = unit < units;
-        unit_offsets<V>(ok[u] ? unit : 0, a.pairs, adjacent, lo[u], hi[u]);
+        at[u] = ok[u] ? unit * V : 0;
+        unit_offsets<V, ADJ>(ok[u] ? unit : 0, a.pairs, lo[u], hi[u]);
 #pragma unroll
         for (int j = 0; j < 2 * V; ++j)
             acc[0][u][j] = acc[1][u][j] = 0.0f;
     }
 
-    for (int64_t t = int64_t(blockIdx.x) * kWaves + wave; t < a.tokens;
-         t += int64_t(gridDim.x) * kWaves) {
+    Unit<T, V> gain_q[U], gain_k[U], next_x[U], next_g[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        gain_q[u].clear();
+        gain_k[u].clear();
+        if (ok[u] && a.q_heads > 0)
+            gain_q[u].load(static_cast<const T *>(a.q_gain), lo[u], hi[u]);
+        if (ok[u] && a.k_heads > 0)
+            gain_k[u].load(static_cast<const T *>(a.k_gain), lo[u], hi[u]);
+    }
+    // one round ahead, over the ends of tokens
+    auto fetch = [&](int64_t t, int r) {
+        const bool is_q = r < a.q_heads;
+        const int h = is_q ? r : r - a.q_heads;
+        const Heads &in = is_q ? a.q : a.k;
+        const Heads &gr = is_q ? a.gq : a.gk;
+        const T *src = static_cast<const T *>(in.data) + t * in.token_stride + h * in.head_stride;
+        const T *gsrc = static_cast<const T *>(gr.data) + t * gr.token_stride + h * gr.head_stride;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            next_x[u].clear();
+            next_g[u].clear();
+            if (t < a.tokens && r < rows && ok[u]) {
+                next_x[u].load(src, lo[u], hi[u]);
+                next_g[u].load(gsrc, lo[u], hi[u]);
+            }
+        }
+    };
+    const int64_t t_step = int64_t(gridDim.x) * kWaves;
+    const int64_t t_first = int64_t(blockIdx.x) * kWaves + wave;
+    fetch(t_first, lane / group);
+    for (int64_t t = t_first; t < a.tokens; t += t_step) {
         float c[U][V], s[U][V];
-        angles<U, V>(c, s, a, t, li, group);
+        angles<U, V>(c, s, table[threadIdx.x >> 6], a, t, lane, at);
         for (int r0 = 0; r0 < rows; r0 += slots) {
             const int r = r0 + lane / group;
             const bool live = r < rows;
             const bool is_q = r < a.q_heads;
-            const int h = live ? (is_q ? r : r - a.q_heads) : 0;
-            const Heads &in = is_q ? a.q : a.k;
-            const Heads &gr = is_q ? a.gq : a.gk;
-            const Heads &out = is_q ? a.oq : a.ok;
-            const T *src = static_cast<const T *>(in.data) + t * in.token_stride +
-                           h * in.head_stride;
-            const T *gsrc = static_cast<const T *>(gr.data) + t * gr.token_stride +
-                            h * gr.head_stride;
-            const T *gain = static_cast<const T *>(is_q ? a.q_gain : a.k_gain);
             float x[U][2 * V], g[U][2 * V], w[U][2 * V];
             float sum = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                next_x[u].get(x[u]);
+                next_g[u].get(g[u]);
+            }
+            if (r0 + slots < rows)
+                fetch(t, r + slots);
+            else
+                fetch(t + t_step, lane / group);
 #pragma unroll
-                for (int j = 0; j < 2 * V; ++j)
-                    x[u][j] = g[u][j] = w[u][j] = 0.0f;
-                if (live && ok[u]) {
-                    load_unit<T, V>(x[u], src, lo[u], hi[u]);
-                    load_unit<T, V>(g[u], gsrc, lo[u], hi[u]);
-                    load_unit<T, V>(w[u], gain, lo[u], hi[u]);
-                }
-                turn_unit<V>(g[u], c[u], s[u], adjacent);     // s is -sin here
+            for (int u = 0; u < U; ++u) {
+                const Unit<T, V> wu = is_q ? gain_q[u] : gain_k[u];
+                wu.get(w[u]);
+                turn_unit<V, ADJ>(g[u], c[u], s[u]);     // s is -sin here
 #pragma unroll
                 for (int j = 0; j < 2 * V; ++j) {
                     sum += x[u][j] * x[u][j];
@@ -295,8 +355,9 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_backward_kernel(RotaryAr
             dot = group_sum(dot, group);
             const float inv = 1.0f / sqrtf(sum * inv_dim + a.eps);
             const float corr = dot * inv * inv_dim;            // mean(h * n)
+            const Heads &out = is_q ? a.oq : a.ok;
             T *dst = static_cast<T *>(const_cast<void *>(out.data)) + t * out.token_stride +
-                     h * out.head_stride;
+                     (is_q ? r : r - a.q_heads) * out.head_stride;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float d[2 * V];
@@ -308,8 +369,11 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_backward_kernel(RotaryAr
                     acc[0][u][j] += is_q ? gn : 0.0f;
                     acc[1][u][j] += is_q ? 0.0f : gn;
                 }
-                if (live && ok[u])
-                    store_unit<T, V>(dst, d, lo[u], hi[u]);
+                if (live && ok[u]) {
+                    Unit<T, V> y;
+                    y.set(d);
+                    y.store(dst, lo[u], hi[u]);
+                }
             }
         }
     }
@@ -337,27 +401,43 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_backward_kernel(RotaryAr
     }
 }
 
-// Column sums of partial[blocks][2 * dim]: 32 columns a block, 8 rows at a
-// time (128-byte reads), joined in LDS.
+// Column sums of partial[blocks][2 * dim]: 16 columns a workgroup, 64 rows at a
+// time, joined in LDS; at most 16 independent reads a thread.
+constexpr int kSumCols = 16, kSumRows = 64;
+
 template <typename T>
-__global__ __launch_bounds__(256) void gain_sum_kernel(const float *partial, int blocks, int dim,
-                                                       int k_heads, T *dq_gain, T *dk_gain)
+__global__ __launch_bounds__(kSumCols * kSumRows) void gain_sum_kernel(const float *partial,
+                                                                       int blocks, int dim,
+                                                                       int k_heads, T *dq_gain,
+                                                                       T *dk_gain)
 {
-    __shared__ float part[8][32];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
-    float v = 0.0f;
-    if (col < 2 * dim)
-        for (int b = row; b < blocks; b += 8)
-            v += partial[int64_t(b) * 2 * dim + col];
-    part[row][threadIdx.x & 31] = v;
+    __shared__ float part[kSumRows][kSumCols + 1];
+    const int x = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;
+    const int col = blockIdx.x * kSumCols + x;
+    float v[kMaxBackwardBlocks / kSumRows];
+#pragma unroll
+    for (int i = 0; i < kMaxBackwardBlocks / kSumRows; ++i) {
+        const int b = row + i * kSumRows;
+        v[i] = b < blocks && col < 2 * dim ? partial[int64_t(b) * 2 * dim + col] : 0.0f;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxBackwardBlocks / kSumRows; ++i)
+        sum += v[i];
+    part[row][x] = sum;
     __syncthreads();
+    for (int n = kSumRows / 2; n > 0; n /= 2) {
+        if (row < n)
+            part[row][x] += part[row + n][x];
+        __syncthreads();
+    }
     if (row == 0 && col < 2 * dim) {
-        for (int r = 1; r < 8; ++r)
-            v += part[r][threadIdx.x];
-        if (col < dim)
-            dq_gain[col] = from_f32<T>(v);
-        else if (k_heads > 0)
-            dk_gain[col - dim] = from_f32<T>(v);
+        if (col < dim) {
+            if (dq_gain)
+                dq_gain[col] = from_f32<T>(part[0][x]);
+        } else if (k_heads > 0) {
+            dk_gain[col - dim] = from_f32<T>(part[0][x]);
+        }
     }
 }
 
@@ -386,11 +466,11 @@ int vector_width(const RotaryArgs &a, RotaryKind kind, size_t elem)
     return 1;
 }
 
-template <typename T, int V, int U>
+template <typename T, int V, int U, bool ADJ>
 hipError_t launch_units(RotaryKind kind, const RotaryArgs &a, int group, int units, hipStream_t s)
 {
     if (kind == RotaryKind::NormRotateBackward) {
-        norm_rotate_backward_kernel<T, V, U>
+        norm_rotate_backward_kernel<T, V, U, ADJ>
             <<<rotary_backward_blocks(a.tokens), kThreads, 0, s>>>(a, group, units);
         return hipGetLastError();
     }
@@ -408,10 +488,10 @@ hipError_t launch_units(RotaryKind kind, const RotaryArgs &a, int group, int uni
     if (blocks > INT32_MAX)
         return hipErrorInvalidValue;
     if (kind == RotaryKind::Rotate)
-        rotary_kernel<T, V, U, false>
+        rotary_kernel<T, V, U, ADJ, false>
             <<<uint32_t(blocks), kThreads, 0, s>>>(a, group, units, per_wave, waves);
     else
-        rotary_kernel<T, V, U, true>
+        rotary_kernel<T, V, U, ADJ, true>
             <<<uint32_t(blocks), kThreads, 0, s>>>(a, group, units, per_wave, waves);
     return hipGetLastError();
 }
@@ -424,9 +504,11 @@ hipError_t launch_width(RotaryKind kind, const RotaryArgs &a, hipStream_t s)
     while (group < units && group < 64)
         group *= 2;
     if (units <= 64)
-        return launch_units<T, V, 1>(kind, a, group, units, s);
+        return a.adjacent ? launch_units<T, V, 1, true>(kind, a, group, units, s)
+                          : launch_units<T, V, 1, false>(kind, a, group, units, s);
     if constexpr (V == 1)                           // up to 128 units of single pairs
-        return launch_units<T, V, 2>(kind, a, group, units, s);
+        return a.adjacent ? launch_units<T, V, 2, true>(kind, a, group, units, s)
+                          : launch_units<T, V, 2, false>(kind, a, group, units, s);
     return hipErrorInvalidValue;
 }
 
@@ -452,7 +534,7 @@ hipError_t launch_type(RotaryKind kind, const RotaryArgs &a, hipStream_t s)
 int rotary_backward_blocks(int64_t tokens)
 {
     const int64_t need = (tokens + kWaves - 1) / kWaves;
-    return int(need < 1024 ? (need > 0 ? need : 1) : 1024);
+    return int(need < kMaxBackwardBlocks ? (need > 0 ? need : 1) : kMaxBackwardBlocks);
 }
 
 hipError_t launch_rotary(RotaryKind kind, mdcn_dtype dtype, const RotaryArgs &a, hipStream_t s)
@@ -470,7 +552,7 @@ hipError_t launch_rotary(RotaryKind kind, mdcn_dtype dtype, const RotaryArgs &a,
 template <typename T>
 static hipError_t gain_sum(const RotaryArgs &a, void *dq, void *dk, hipStream_t s)
 {
-    gain_sum_kernel<T><<<(2 * a.dim + 31) / 32, 256, 0, s>>>(
+    gain_sum_kernel<T><<<(2 * a.dim + kSumCols - 1) / kSumCols, kSumCols * kSumRows, 0, s>>>(
         a.partial, rotary_backward_blocks(a.tokens), a.dim, a.k_heads, static_cast<T *>(dq),
         static_cast<T *>(dk));
     return hipGetLastError();
