@@ -4,10 +4,11 @@
 // Row i of a sequence of lq queries and lk keys sees every key, or (causal)
 // the keys j <= i + lk - lq.  A row that sees none gets zeros and -infinity.
 //
-// A workgroup takes 128 queries of one head, 32 per wave; K and V are staged
-// in LDS in tiles of 64 keys (fp32: 32), two stages, one barrier per tile:
-// the copies of the next tile run while this one is used.  One pass with the
-// running maximum and sum.  The last tile comes first: the tiles
+// A workgroup takes 32 * RW queries of one head, 32 per wave, with KW waves to
+// each 32 that share the keys; K and V are staged in LDS, 64 keys a wave (fp32:
+// 32), two stages, one barrier per tile: the copies of the next tile run
+// while this one is used.  One pass with the running maximum and sum.  The
+// last tile comes first: the tiles
 // that a causal mask cuts are then done before the accumulators hold
 // anything else, so that what hidden rows of V spoil (0 * infinity) can be
 // recomputed from these tiles alone.
@@ -17,22 +18,25 @@ namespace mdcn {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kRows = 32 * kWaves;
-
 template <typename T> constexpr int tile_keys() { return sizeof(T) == 2 ? 64 : 32; }
 
-template <typename T, int DP>
-__global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendArgs a)
+template <typename T, int DP, int RW, int KW>
+__global__ __launch_bounds__(64 * RW * KW, 2) void attend_kernel(AttendArgs a)
 {
     using R = Row<T, DP>;
-    constexpr int KB = tile_keys<T>();
+    constexpr int ROWS = 32 * RW;
+    constexpr int KB = tile_keys<T>();           // keys of a wave's part of a tile
     constexpr int NS = KB / 32;
-    constexpr int TILE = KB * R::PITCH;
+    constexpr int KT = KB * KW;                  // keys of a tile
+    constexpr int PART = KB * R::PITCH;
+    constexpr int TILE = KT * R::PITCH;
+    // reads of a tile ahead of their uses (fp32 rows would take twice the registers)
+    constexpr bool AHEAD = sizeof(T) == 2;
     __shared__ __align__(1024) char smem[4 * TILE];          // K, V, K, V
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int rg = wave % RW, kg = wave / RW;
     const int half = lane >> 5;
 
     // Key heads vary fastest over workgroups: neighbours on one XCD (every
@@ -42,84 +46,150 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendArgs a)
     const int head = kv_head * group + (blockIdx.x / a.k_heads) % group;
     int b, tile;
     if (!find_tile(a.batch, int(blockIdx.x / a.q_heads), lane,
-                   [&](int i) { return (span_of(a, i).lq + kRows - 1) / kRows; }, b, tile))
+                   [&](int i) { return (span_of(a, i).lq + ROWS - 1) / ROWS; }, b, tile))
         return;
-    Span sp = span_of(a, b);
-    tile = (sp.lq + kRows - 1) / kRows - 1 - tile;           // long rows first
+    const Span sp = span_of(a, b);
+    tile = (sp.lq + ROWS - 1) / ROWS - 1 - tile;             // long rows first
 
-    const int r0 = tile * kRows + wave * 32;                 // wave's first row
+    const int r0 = tile * ROWS + rg * 32;                    // wave's first row
     const int row = r0 + (lane & 31);
     const int shift = sp.lk - sp.lq;
     const bool live = row < sp.lq;
     const int last = a.causal ? row + shift : sp.lk - 1;     // last visible key
-    const int block_last =
-        a.causal ? min(tile * kRows + kRows, sp.lq) - 1 + shift : sp.lk - 1;
-    const int nt = block_last < 0 ? 0 : (block_last + KB) / KB;
+    const int block_last = a.causal ? min(tile * ROWS + ROWS, sp.lq) - 1 + shift : sp.lk - 1;
+    const int nt = block_last < 0 ? 0 : block_last / KT + 1;
     const int wave_last = a.causal ? min(r0 + 31, sp.lq - 1) + shift : sp.lk - 1;
     const int wave_first = a.causal ? r0 + shift : sp.lk - 1;
+
+    const char *kbase = row_ptr<T>(a.k, sp.k0, kv_head);
+    const char *vbase = row_ptr<T>(a.v, sp.k0, kv_head);
+    Stager<T, DP, KT, RW * KW> st;
+    st.init(a.k.token_stride, a.v.token_stride, a.dim, wave, lane);
+    const uint32_t lds = lds_address(smem);
+    // round i handles tile nt - 1 - i, in stage i & 1
+    auto stage = [&](int i) {
+        const int t = nt - 1 - i;
+        const uint32_t at = lds + (i & 1) * 2 * TILE;
+        st.template load<0>(at, kbase + uint64_t(t * KT) * st.stride[0], sp.lk - t * KT);
+        st.template load<1>(at + TILE, vbase + uint64_t(t * KT) * st.stride[1], sp.lk - t * KT);
+    };
+    if (nt > 0)
+        stage(0);
 
     Frag<T, DP> qf;
     load_frag<T, DP>(qf, live ? reinterpret_cast<const T *>(row_ptr<T>(a.q, sp.q0 + row, head))
                               : nullptr,
                      a.dim, half);
-    const char *kbase = row_ptr<T>(a.k, sp.k0, kv_head);
-    const char *vbase = row_ptr<T>(a.v, sp.k0, kv_head);
-    Stager<T, DP, KB, kWaves> ks, vs;
-    ks.init(a.k.token_stride, a.dim, wave, lane);
-    vs.init(a.v.token_stride, a.dim, wave, lane);
-
+    settle<T, DP>(qf);
     Softmax<T, DP> sm;
     sm.init();
-    const float c = a.scale * kLog2e;
-    const uint32_t lds = lds_address(smem);
+    const float c = a.scale * kLog2e, margin = kRaise / c;
     bool check = a.causal != 0;                              // hidden keys seen so far
-
-    auto stage = [&](int t, int buf) {
-        const int left = sp.lk - t * KB;
-        ks.load(lds + buf * 2 * TILE, kbase + uint64_t(t * KB) * ks.stride, left);
-        vs.load(lds + buf * 2 * TILE + TILE, vbase + uint64_t(t * KB) * vs.stride, left);
-    };
-    auto repair = [&](int begin) {
-        repair_hidden<T, DP>(sm.o, qf, kbase, vbase, ks.stride, vs.stride, begin,
-                             min(wave_last + 1, sp.lk), last, sm.m, c, a.dim, half);
+    auto repair = [&](int i) {
+        // this wave's keys of the rounds before i, one round at a time
+        repair_hidden<T, DP, KB, KT>(sm.o, qf, kbase, vbase, st.stride[0], st.stride[1],
+                                     (nt - i) * KT + kg * KB, min(wave_last + 1, sp.lk), last, sm.m,
+                                     c, a.dim, half);
     };
 
-    if (nt > 0)
-        stage(nt - 1, 0);
     for (int i = 0; i < nt; ++i) {
-        const int t = nt - 1 - i;
+        const int key0 = (nt - 1 - i) * KT + kg * KB;        // wave's first key of this round
         dma_wait<0>();
         lds_barrier();
-        if (t > 0)
-            stage(t - 1, (i + 1) & 1);
-        if (t * KB > wave_last)
-            continue;                                        // nothing visible to this wave
-        const char *kt = smem + (i & 1) * 2 * TILE;
-        const bool cut = t * KB + KB - 1 > wave_first;       // some key is hidden to some row
+        if (i + 1 < nt)
+            stage(i + 1);
+        if (key0 > wave_last)
+            continue;                                        // hidden from every row
+        const bool cut = key0 + KB - 1 > wave_first;         // some key is hidden to some row
         if (check && !cut) {
-            repair((t + 1) * KB);
+            repair(i);
             check = false;
         }
+        const char *kt = smem + (i & 1) * 2 * TILE + kg * PART;
+        const char *vt = kt + TILE;
         float16v s[NS];
+        Cols<T, DP> vf;
+        if constexpr (AHEAD) {
+            Frag<T, DP> kf[NS];
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-            s[n] = mm_rows<T, DP>(kt + n * 32 * R::PITCH, qf, lane);
+            for (int n = 0; n < NS; ++n)
+                load_rows<T, DP>(kf[n], kt + n * 32 * R::PITCH, lane);
+            reads_first();
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                s[n] = mm_rows<T, DP>(kf[n], qf);
+            vf.load(vt, lane);
+            reads_first();
+        } else {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                s[n] = mm_rows<T, DP>(kt + n * 32 * R::PITCH, qf, lane);
+        }
         if (cut) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    s[n][r] = t * KB + n * 32 + acc_row(r, half) <= last ? s[n][r] : -INFINITY;
+                    s[n][r] = key0 + n * 32 + acc_row(r, half) <= last ? s[n][r] : -INFINITY;
         }
-        sm.step(s, c);
+        sm.step(s, c, margin);
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-            mm_cols<T, DP>(sm.o, kt + TILE + n * 32 * R::PITCH, s[n], lane);
+        for (int n = 0; n < NS; ++n) {
+            if constexpr (AHEAD) {
+                Cols<T, DP> next;
+                if (n + 1 < NS) {
+                    next.load(vt + (n + 1) * 32 * R::PITCH, lane);
+                    reads_first();
+                }
+                mm_cols<T, DP>(sm.o, vf, s[n]);
+                if (n + 1 < NS)
+                    vf = next;
+            } else {
+                mm_cols<T, DP>(sm.o, vt + n * 32 * R::PITCH, s[n], lane);
+            }
+        }
     }
     if (check && nt > 0)
-        repair(0);
+        repair(nt);
 
-    const float l = sm.l + swap_halves(sm.l);
+    float l = sm.l + swap_halves(sm.l);
+    if constexpr (KW > 1) {
+        // join the waves that shared a row's keys: all but the first leave
+        // their sums in LDS
+        static_assert((KW - 1) * RW * (DP + 2) * 32 * 4 <= 4 * TILE, "the sums fit the stages");
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(smem);
+        auto at = [&](int g) { return sums + ((g - 1) * RW + rg) * (DP + 2) * 32 + (lane & 31); };
+        if (kg > 0) {
+            float *p = at(kg);
+#pragma unroll
+            for (int d = 0; d < R::BLOCKS; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    p[(d * 32 + acc_row(r, half)) * 32] = sm.o[d][r];
+            if (half == 0) {
+                p[DP * 32] = sm.m;
+                p[(DP + 1) * 32] = l;
+            }
+        }
+        __syncthreads();
+        if (kg > 0)
+            return;
+#pragma unroll 1
+        for (int g = 1; g < KW; ++g) {
+            const float *p = at(g);
+            const float m = p[DP * 32], up = fmaxf(sm.m, m);
+            const float f = sm.m == up ? 1.0f : exp2f((sm.m - up) * c);
+            const float h = m == up ? 1.0f : exp2f((m - up) * c);
+#pragma unroll
+            for (int d = 0; d < R::BLOCKS; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    sm.o[d][r] = sm.o[d][r] * f + p[(d * 32 + acc_row(r, half)) * 32] * h;
+            l = l * f + p[(DP + 1) * 32] * h;
+            sm.m = up;
+        }
+    }
     if (live) {
         store_cols<T, DP>(
             reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.out, sp.q0 + row, head))), sm.o,
@@ -130,17 +200,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendArgs a)
     }
 }
 
-template <typename T, int DP>
-hipError_t launch(const AttendArgs &a, hipStream_t s)
+template <typename T, int DP, int RW, int KW>
+hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 {
-    const int64_t tiles = int64_t(a.q_tokens / kRows) + (a.batch < a.q_tokens ? a.batch : a.q_tokens);
+    constexpr int ROWS = 32 * RW;
+    const int64_t tiles = int64_t(a.q_tokens / ROWS) + (a.batch < a.q_tokens ? a.batch : a.q_tokens);
     const int64_t blocks = tiles * a.q_heads;
     if (blocks > INT32_MAX)
         return hipErrorInvalidValue;
     if (blocks == 0)
         return hipSuccess;
-    attend_kernel<T, DP><<<uint32_t(blocks), 64 * kWaves, 0, s>>>(a);
+    attend_kernel<T, DP, RW, KW><<<uint32_t(blocks), 64 * RW * KW, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <typename T, int DP> hipError_t launch(const AttendArgs &a, hipStream_t s)
+{
+    // Two workgroups of four waves fit a compute unit.  Up to one each, eight
+    // waves that share the keys two ways use the second half of it.
+    const int64_t blocks = (int64_t(a.q_tokens) / 128 + 1) * a.q_heads;
+    return blocks <= 320 ? launch_shape<T, DP, 4, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
 }
 
 template <typename T>

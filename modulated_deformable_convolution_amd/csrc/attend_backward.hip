@@ -6,9 +6,9 @@
 //   dk_j = scale sum_i ds_ij q_i       (i over the rows of all heads that share j's head)
 // p is recomputed from lse, so nothing of size queries x keys is stored.
 //
-// Three kernels: delta; dk and dv, a workgroup per 128 keys walking
-// over the queries of its group's heads; dq, a workgroup per 128 queries
-// walking over the keys.  Scores and go.v are computed in both (7 products
+// Kernels: delta; dk and dv, a workgroup per 128 keys walking over the
+// queries of its group's heads, or several that share them, whose sums in the
+// workspace a fourth kernel adds up; dq, a workgroup per 128 queries walking over the keys.  Scores and go.v are computed in both (7 products
 // instead of 5), in exchange for which no gradient is accumulated through
 // memory: no atomics, the same bits every run, one rounding of each gradient.
 #include "attention_common.h"
@@ -85,13 +85,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_dq_kernel(AttendArgs a)
     load_frag<T, DP>(gf, live ? reinterpret_cast<const T *>(row_ptr<T>(a.go, token, head)) : nullptr,
                      a.dim, half);
     const int64_t stat = int64_t(head) * a.q_tokens + token;
-    const float lse2 = live ? a.lse[stat] * kLog2e : 0.0f;
-    const float delta = live ? a.delta[stat] : 0.0f;
+    float lse2 = live ? a.lse[stat] * kLog2e : 0.0f;
+    float delta = live ? a.delta[stat] : 0.0f;
+    settle<T, DP>(qf);
+    settle<T, DP>(gf);
+    settle(lse2);
+    settle(delta);
     const char *kbase = row_ptr<T>(a.k, sp.k0, kv_head);
     const char *vbase = row_ptr<T>(a.v, sp.k0, kv_head);
-    Stager<T, DP, KB, kWaves> ks, vs;
-    ks.init(a.k.token_stride, a.dim, wave, lane);
-    vs.init(a.v.token_stride, a.dim, wave, lane);
+    Stager<T, DP, KB, kWaves> st;
+    st.init(a.k.token_stride, a.v.token_stride, a.dim, wave, lane);
     const uint32_t lds = lds_address(smem);
     const float c = a.scale * kLog2e;
 
@@ -101,8 +104,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_dq_kernel(AttendArgs a)
         dq[i] = (float16v){};
     auto stage = [&](int t, int buf) {
         const int left = sp.lk - t * KB;
-        ks.load(lds + buf * 2 * TILE, kbase + uint64_t(t * KB) * ks.stride, left);
-        vs.load(lds + buf * 2 * TILE + TILE, vbase + uint64_t(t * KB) * vs.stride, left);
+        st.template load<0>(lds + buf * 2 * TILE, kbase + uint64_t(t * KB) * st.stride[0], left);
+        st.template load<1>(lds + buf * 2 * TILE + TILE, vbase + uint64_t(t * KB) * st.stride[1],
+                            left);
     };
     if (nt > 0)
         stage(0, 0);
@@ -150,8 +154,9 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     const int half = lane >> 5;
     const int kv_head = blockIdx.x % a.k_heads;
     const int group = a.q_heads / a.k_heads;
+    const int part = (blockIdx.x / a.k_heads) % a.splits;
     int b, tile;
-    if (!find_tile(a.batch, int(blockIdx.x / a.k_heads), lane,
+    if (!find_tile(a.batch, int(blockIdx.x / a.k_heads / a.splits), lane,
                    [&](int i) { return (span_of(a, i).k_all + kRows - 1) / kRows; }, b, tile))
         return;
     const Span sp = span_of(a, b);
@@ -171,9 +176,10 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     load_frag<T, DP>(
         vf, live ? reinterpret_cast<const T *>(row_ptr<T>(a.v, sp.k0 + key, kv_head)) : nullptr,
         a.dim, half);
-    Stager<T, DP, QB, kWaves> qs, gs;
-    qs.init(a.q.token_stride, a.dim, wave, lane);
-    gs.init(a.go.token_stride, a.dim, wave, lane);
+    Stager<T, DP, QB, kWaves> st;
+    st.init(a.q.token_stride, a.go.token_stride, a.dim, wave, lane);
+    settle<T, DP>(kf);
+    settle<T, DP>(vf);
     const uint32_t lds = lds_address(smem);
     const float c = a.scale * kLog2e;
 
@@ -186,8 +192,10 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
         const int head = kv_head * group + i / nt, t = t0 + i % nt;
         const int left = sp.lq - t * QB;
         const uint32_t at = lds + buf * STAGE;
-        qs.load(at, row_ptr<T>(a.q, sp.q0, head) + uint64_t(t * QB) * qs.stride, left);
-        gs.load(at + TILE, row_ptr<T>(a.go, sp.q0, head) + uint64_t(t * QB) * gs.stride, left);
+        st.template load<0>(at, row_ptr<T>(a.q, sp.q0, head) + uint64_t(t * QB) * st.stride[0],
+                            left);
+        st.template load<1>(at + TILE,
+                            row_ptr<T>(a.go, sp.q0, head) + uint64_t(t * QB) * st.stride[1], left);
         if (wave < 2) {
             const float *src = (wave == 0 ? a.lse : a.delta) + int64_t(head) * a.q_tokens + sp.q0 +
                                t * QB;
@@ -197,16 +205,18 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
                      uint32_t(lane) * 4);
         }
     };
-    const int total = nt * group;
-    if (total > 0)
-        stage(0, 0);
-    for (int i = 0; i < total; ++i) {
+    // this workgroup's part of the (head, tile) pairs
+    const int i_begin = int(int64_t(nt) * group * part / a.splits);
+    const int i_end = int(int64_t(nt) * group * (part + 1) / a.splits);
+    if (i_end > i_begin)
+        stage(i_begin, 0);
+    for (int i = i_begin; i < i_end; ++i) {
         dma_wait<0>();
         lds_barrier();
-        if (i + 1 < total)
-            stage(i + 1, (i + 1) & 1);
+        if (i + 1 < i_end)
+            stage(i + 1, (i + 1 - i_begin) & 1);
         const int q_tile = (t0 + i % nt) * QB;
-        const char *qt = smem + (i & 1) * STAGE;
+        const char *qt = smem + ((i - i_begin) & 1) * STAGE;
         const float *stat = reinterpret_cast<const float *>(qt + 2 * TILE);
 #pragma unroll
         for (int n = 0; n < QB / 32; ++n) {
@@ -247,6 +257,14 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
             for (int i = 0; i < R::BLOCKS; ++i)
                 dk[i] = dv[i] = (float16v){};
         }
+        if (a.splits > 1) {
+            const int64_t rows = int64_t(a.k_tokens) * a.k_heads;
+            float *sum = a.partial + (2 * part * rows + int64_t(kv_head) * a.k_tokens + sp.k0 +
+                                      key) * a.dim;
+            store_cols<float, DP>(sum, dk, 1.0f, a.dim, half);
+            store_cols<float, DP>(sum + rows * a.dim, dv, 1.0f, a.dim, half);
+            return;
+        }
         T *dst = reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.dk, sp.k0 + key, kv_head)));
         store_cols<T, DP>(dst, dk, a.scale, a.dim, half);
         dst = reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.dv, sp.k0 + key, kv_head)));
@@ -254,15 +272,59 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     }
 }
 
-int64_t tiles_of(int64_t tokens, int64_t batch) { return tokens / kRows + (batch < tokens ? batch : tokens); }
+constexpr int kSumRows = 16;
+
+// Adds the parts [part][dk, dv][key head][token][dim] of the keys of every
+// sequence, 16 keys a workgroup.
+template <typename T>
+__global__ __launch_bounds__(256) void attend_dkv_sum_kernel(AttendArgs a)
+{
+    const int kv_head = blockIdx.x % a.k_heads;
+    int b, tile;
+    if (!find_tile(a.batch, int(blockIdx.x / a.k_heads), threadIdx.x & 63,
+                   [&](int i) { return (span_of(a, i).k_all + kSumRows - 1) / kSumRows; }, b, tile))
+        return;
+    const Span sp = span_of(a, b);
+    const int vecs = a.dim / 4;
+    const int rows = min(kSumRows, sp.k_all - tile * kSumRows);
+    const int64_t all = int64_t(a.k_tokens) * a.k_heads * a.dim;
+    for (int e = threadIdx.x; e < 2 * rows * vecs; e += 256) {
+        const int which = e / (rows * vecs), rest = e % (rows * vecs);
+        const int row = rest / vecs, d = rest % vecs * 4;
+        const int64_t token = sp.k0 + tile * kSumRows + row;
+        const float *src = a.partial + which * all +
+                           (int64_t(kv_head) * a.k_tokens + token) * a.dim + d;
+        float4v sum = *reinterpret_cast<const float4v *>(src);
+        for (int n = 1; n < a.splits; ++n)
+            sum += *reinterpret_cast<const float4v *>(src + 2 * n * all);
+        const float f = which == 0 ? a.scale : 1.0f;
+        T *dst = reinterpret_cast<T *>(const_cast<char *>(
+                     row_ptr<T>(which == 0 ? a.dk : a.dv, token, kv_head))) + d;
+        struct alignas(4 * sizeof(T)) {
+            T e[4];
+        } v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v.e[j] = from_f32<T>(sum[j] * f);
+        __builtin_memcpy(__builtin_assume_aligned(dst, 4 * sizeof(T)), &v, sizeof(v));
+    }
+}
+
+// At least the tiles of `rows` rows of any `batch` sequences.
+int64_t tiles_of(int64_t tokens, int64_t batch, int rows)
+{
+    return tokens / rows + (batch < tokens ? batch : tokens);
+}
 
 template <typename T, int DP>
 hipError_t launch(const AttendArgs &a, hipStream_t s)
 {
     const int64_t rows = int64_t(a.q_tokens) * a.q_heads;
-    const int64_t q_blocks = tiles_of(a.q_tokens, a.batch) * a.q_heads;
-    const int64_t k_blocks = tiles_of(a.k_tokens, a.batch) * a.k_heads;
-    if ((rows + 15) / 16 > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
+    const int64_t q_blocks = tiles_of(a.q_tokens, a.batch, kRows) * a.q_heads;
+    const int64_t k_tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
+    const int64_t k_blocks = k_tiles * a.splits;
+    const int64_t sum_blocks = tiles_of(a.k_tokens, a.batch, kSumRows) * a.k_heads;
+    if (sum_blocks > INT32_MAX || (rows + 15) / 16 > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
         return hipErrorInvalidValue;
     if (rows > 0)
         attend_delta_kernel<T><<<uint32_t((rows + 15) / 16), 256, 0, s>>>(a);
@@ -270,6 +332,10 @@ hipError_t launch(const AttendArgs &a, hipStream_t s)
     if (e == hipSuccess && k_blocks > 0) {
         attend_dkv_kernel<T, DP><<<uint32_t(k_blocks), 64 * kWaves, 0, s>>>(a);
         e = hipGetLastError();
+        if (e == hipSuccess && a.splits > 1) {
+            attend_dkv_sum_kernel<T><<<uint32_t(sum_blocks), 256, 0, s>>>(a);
+            e = hipGetLastError();
+        }
     }
     if (e == hipSuccess && q_blocks > 0) {
         attend_dq_kernel<T, DP><<<uint32_t(q_blocks), 64 * kWaves, 0, s>>>(a);
@@ -291,6 +357,18 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
 }
 
 }  // namespace
+
+int attend_backward_splits(mdcn_dtype dtype, const AttendArgs &a)
+{
+    // Enough workgroups for two on each of the 256 compute units, with at
+    // least two tiles of queries to each (a part costs its sums' way through memory).
+    const int64_t tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
+    const int64_t queries = int64_t(a.q_heads / a.k_heads) * a.q_tokens /
+                            ((dtype == MDCN_F32 ? 32 : 64) * int64_t(a.batch > 0 ? a.batch : 1));
+    int64_t n = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
+    n = n < queries / 2 ? n : queries / 2;
+    return int(n < 1 ? 1 : n > 8 ? 8 : n);
+}
 
 hipError_t launch_attend_backward(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s)
 {

@@ -128,7 +128,7 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
     const int half = lane >> 5;
     const int col = lane & 31;
     const int group = a.q_heads / a.k_heads;
-    const float c = a.scale * kLog2e;
+    const float c = a.scale * kLog2e, margin = kRaise / c;
 
     Chunk chunk;
     chunk.load(a, 0, lane);
@@ -139,9 +139,8 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
     const int64_t u_end = units * (int64_t(blockIdx.x) + 1) / share;
     const int64_t u_begin = units * int64_t(blockIdx.x) / share;
 
-    Stager<T, DP, kUnit, 1> ks, vs;
-    ks.init(a.k.token_stride, a.dim, 0, lane);
-    vs.init(a.v.token_stride, a.dim, 0, lane);
+    Stager<T, DP, kUnit, 1> st;
+    st.init(a.k.token_stride, a.v.token_stride, a.dim, 0, lane);
     char *own = smem + wave * 4 * TILE;
     const uint32_t lds = lds_address(own);
 
@@ -197,15 +196,17 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                 const int w1 = min(n0 + int(int64_t(n1 - n0) * (wave + 1) / NW), visible);
                 auto stage = [&](int t, int buf) {
                     const int left = sp.lk - t * kUnit;
-                    ks.load(lds + buf * 2 * TILE, kbase + uint64_t(t) * kUnit * ks.stride, left);
-                    vs.load(lds + buf * 2 * TILE + TILE, vbase + uint64_t(t) * kUnit * vs.stride,
-                            left);
+                    st.template load<0>(lds + buf * 2 * TILE,
+                                        kbase + uint64_t(t) * kUnit * st.stride[0], left);
+                    st.template load<1>(lds + buf * 2 * TILE + TILE,
+                                        vbase + uint64_t(t) * kUnit * st.stride[1], left);
                 };
                 auto repair = [&](int begin) {
-                    repair_hidden<T, DP>(sm.o, qf, kbase, vbase, ks.stride, vs.stride,
+                    repair_hidden<T, DP, 1, 1>(sm.o, qf, kbase, vbase, st.stride[0], st.stride[1],
                                          begin * kUnit, min(w1 * kUnit, sp.lk), last, sm.m, c,
                                          a.dim, half);
                 };
+                settle<T, DP>(qf);
                 if (w1 > w0)
                     stage(w1 - 1, 0);
                 for (int j = 0; j < w1 - w0; ++j) {
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                         for (int r = 0; r < 16; ++r)
                             s[0][r] = t * kUnit + acc_row(r, half) <= last ? s[0][r] : -INFINITY;
                     }
-                    sm.step(s, c);
+                    sm.step(s, c, margin);
                     mm_cols<T, DP>(sm.o, kt + TILE, s[0], lane);
                 }
                 if (check && w1 > w0)

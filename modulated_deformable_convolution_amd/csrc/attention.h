@@ -61,9 +61,9 @@ struct AttendArgs {
     int32_t batch, q_tokens, k_tokens;
     int32_t q_heads, k_heads, dim, causal;
     float scale;
-    // split kernel
-    int32_t workers;
-    float *partial;
+    int32_t workers;       // split kernel
+    int32_t splits;        // backward: workgroups that share a tile of keys
+    float *partial;        // sums that several workgroups leave for one result
 };
 
 hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
@@ -71,6 +71,9 @@ hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
 int attend_split_workers(mdcn_dtype dtype, int dim);
 size_t attend_split_bytes(mdcn_dtype dtype, int dim);
 hipError_t launch_attend_split(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
+// Workgroups that share the queries of a tile of keys; more than one need
+// splits * 2 * k_tokens * k_heads * dim floats of `partial`.
+int attend_backward_splits(mdcn_dtype dtype, const AttendArgs &a);
 hipError_t launch_attend_backward(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
 
 }  // namespace mdcn

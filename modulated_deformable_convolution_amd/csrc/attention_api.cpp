@@ -225,6 +225,12 @@ mdcn_status check_attend_view(View &v)
     return MDCN_OK;
 }
 
+// The backward's delta, up to the next 256 bytes.
+size_t delta_bytes(const AttendArgs &a)
+{
+    return (size_t(a.q_heads) * a.q_tokens * sizeof(float) + 255) / 256 * 256;
+}
+
 // The kernel for few query rows per sequence.
 bool attend_uses_split(const AttendArgs &a)
 {
@@ -561,7 +567,10 @@ mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_
     const mdcn_status st = attend_dims(op, dtype, dims, &a);
     if (st != MDCN_OK)
         return st;
-    *bytes = size_t(a.q_heads) * a.q_tokens * sizeof(float) + 256;
+    const int splits = mdcn::attend_backward_splits(dtype, a);
+    *bytes = delta_bytes(a) + 256;
+    if (splits > 1)
+        *bytes += size_t(splits) * 2 * a.k_tokens * a.k_heads * a.dim * sizeof(float);
     return MDCN_OK;
 }
 
@@ -633,6 +642,8 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
         a.dv = g[2].h;
         a.lse = const_cast<float *>(lse);
         a.delta = static_cast<float *>(align_up(workspace));
+        a.partial = reinterpret_cast<float *>(reinterpret_cast<char *>(a.delta) + delta_bytes(a));
+        a.splits = mdcn::attend_backward_splits(dtype, a);
         a.cu_q = cu_q;
         a.cu_k = cu_k;
         a.used_k = used_k;

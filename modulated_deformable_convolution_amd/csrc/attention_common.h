@@ -101,38 +101,56 @@ __device__ __forceinline__ v4i row_resource(const char *base, uint32_t bytes)
     return r;
 }
 
-// Stages tiles of ROWS rows with WAVES waves: each wave's share of the copies.
+// Stages tiles of ROWS rows of two tensors (keys and values; queries and
+// gradients) with WAVES waves: each wave's share of the copies, consecutive
+// kilobytes of a tile.  The offsets of the first tensor's copies are kept;
+// those of the second, whose tokens may lie at another stride, follow by one
+// addition (rows past the end and channels past dim keep offsets out of range).
 template <typename T, int DP, int ROWS, int WAVES> struct Stager {
     using R = Row<T, DP>;
     static constexpr int COPIES = ROWS * R::CHUNKS / 64 / WAVES;
+    static constexpr int STEP = 64 / R::CHUNKS;      // rows of one copy
     static_assert(COPIES * 64 * WAVES == ROWS * R::CHUNKS, "copies fill the tile");
     uint32_t voff[COPIES];
-    uint32_t stride, width;
+    uint32_t shift0;                                 // of the second tensor's first row
+    uint32_t stride[2], width;
     uint32_t slot;
 
-    __device__ __forceinline__ void init(int64_t token_stride, int dim, int wave, int lane)
+    __device__ __forceinline__ void init(int64_t stride_a, int64_t stride_b, int dim, int wave,
+                                         int lane)
     {
-        stride = uint32_t(token_stride) * uint32_t(sizeof(T));
+        stride[0] = uint32_t(stride_a) * uint32_t(sizeof(T));
+        stride[1] = uint32_t(stride_b) * uint32_t(sizeof(T));
         width = uint32_t(dim) * uint32_t(sizeof(T));
         slot = uint32_t(wave * COPIES * 1024);
+        const int row0 = wave * COPIES * STEP + lane / R::CHUNKS;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            const int s = (wave * COPIES + i) * 64 + lane;
-            const int row = s / R::CHUNKS;
-            const uint32_t byte = uint32_t((s % R::CHUNKS) ^ R::swz(row)) * 16;
-            voff[i] = byte < width ? uint32_t(row) * stride + byte : 0x80000000u;
+            const int row = row0 + i * STEP;
+            const uint32_t byte = uint32_t((lane % R::CHUNKS) ^ R::swz(row)) * 16;
+            voff[i] = byte < width ? uint32_t(row) * stride[0] + byte : kOutside;
         }
+        shift0 = uint32_t(row0) * (stride[1] - stride[0]);
     }
 
-    // Rows [0, left) of the tile at `base` (ROWS at most) to LDS at `lds`.
+    // Rows [0, left) of the tile at `base` (ROWS at most) of tensor `which` to LDS at `lds`.
+    template <int WHICH>
     __device__ __forceinline__ void load(uint32_t lds, const char *base, int left) const
     {
         const int n = left < ROWS ? left : ROWS;
-        const v4i r = row_resource(base, n > 0 ? uint32_t(n - 1) * stride + width : 0);
+        const v4i r = row_resource(base, n > 0 ? uint32_t(n - 1) * stride[WHICH] + width : 0);
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i)
-            dma_row16(__builtin_amdgcn_readfirstlane(lds + slot + i * 1024), r, voff[i]);
+        for (int i = 0; i < COPIES; ++i) {
+            const uint32_t off =
+                WHICH == 0 ? voff[i]
+                           : voff[i] + shift0 + uint32_t(i * STEP) * (stride[1] - stride[0]);
+            dma_row16(__builtin_amdgcn_readfirstlane(lds + slot + i * 1024), r, off);
+        }
     }
+
+    // Offset of channels past dim: out of range whatever shift is added (a
+    // tile's offsets and shifts are below 2^30).
+    static constexpr uint32_t kOutside = 0x80000000u;
 };
 
 // The register operand of mm_rows: row `src` (dim values, 16-byte aligned),
@@ -150,20 +168,50 @@ __device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *src, int dim,
     }
 }
 
+// Waits for the loads of `f` here.  Without it the compiler waits at the first
+// use, inside the loop over the tiles, in every round -- and as it counts all
+// loads in order, for the copies of the next tile too.
+template <typename T, int DP> __device__ __forceinline__ void settle(Frag<T, DP> &f)
+{
+#pragma unroll
+    for (int k = 0; k < Row<T, DP>::STEPS; ++k)
+        asm volatile("" : "+v"(f[k].x), "+v"(f[k].y), "+v"(f[k].z), "+v"(f[k].w));
+}
+
+__device__ __forceinline__ void settle(float &v) { asm volatile("" : "+v"(v)); }
+
+// Issued reads must not sink to their uses: the scheduler would keep two in
+// flight, and every pair of MFMAs would wait for LDS.
+__device__ __forceinline__ void reads_first() { __builtin_amdgcn_sched_barrier(0); }
+
+// The staged operand of mm_rows: 32 rows at `tile`.
 template <typename T, int DP>
-__device__ __forceinline__ float16v mm_rows(const char *tile, const Frag<T, DP> &f,
-                                            int lane)
+__device__ __forceinline__ void load_rows(Frag<T, DP> &a, const char *tile, int lane)
 {
     using R = Row<T, DP>;
     const int row = lane & 31, half = lane >> 5, sw = R::swz(row);
     const char *p = tile + row * R::PITCH;
+#pragma unroll
+    for (int k = 0; k < R::STEPS; ++k)
+        a[k] = *reinterpret_cast<const uint4 *>(p + ((2 * k + half) ^ sw) * 16);
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ float16v mm_rows(const Frag<T, DP> &a, const Frag<T, DP> &f)
+{
     float16v s = {};
 #pragma unroll
-    for (int k = 0; k < R::STEPS; ++k) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p + ((2 * k + half) ^ sw) * 16);
-        s = Mma<T>::step(a, f[k], s);
-    }
+    for (int k = 0; k < Row<T, DP>::STEPS; ++k)
+        s = Mma<T>::step(a[k], f[k], s);
     return s;
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ float16v mm_rows(const char *tile, const Frag<T, DP> &f, int lane)
+{
+    Frag<T, DP> a;
+    load_rows<T, DP>(a, tile, lane);
+    return mm_rows<T, DP>(a, f);
 }
 
 // Registers r0.. of a 32x32 accumulator rounded to T (to nearest even) as the
@@ -223,9 +271,38 @@ __device__ __forceinline__ uint4 col_frag(const char *tile, int step, int blk, i
     return o;
 }
 
+// The staged operand of mm_cols: 32 rows at `tile`, every step and block.
+template <typename T, int DP> struct Cols {
+    using R = Row<T, DP>;
+    static constexpr int STEPS = 32 / R::KROWS;
+    uint4 f[STEPS][R::BLOCKS];
+
+    __device__ __forceinline__ void load(const char *tile, int lane)
+    {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int d = 0; d < R::BLOCKS; ++d)
+                f[s][d] = col_frag<T, DP>(tile, s, d, lane);
+    }
+};
+
 template <typename T, int DP>
-__device__ __forceinline__ void mm_cols(Acc<T, DP> &acc, const char *tile,
-                                        const float16v &p, int lane)
+__device__ __forceinline__ void mm_cols(Acc<T, DP> &acc, const Cols<T, DP> &t, const float16v &p)
+{
+    using R = Row<T, DP>;
+#pragma unroll
+    for (int s = 0; s < Cols<T, DP>::STEPS; ++s) {
+        const uint4 b = pack_p<T>(p, s * R::KROWS / 2);
+#pragma unroll
+        for (int d = 0; d < R::BLOCKS; ++d)
+            acc[d] = Mma<T>::step(t.f[s][d], b, acc[d]);
+    }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void mm_cols(Acc<T, DP> &acc, const char *tile, const float16v &p,
+                                        int lane)
 {
     using R = Row<T, DP>;
 #pragma unroll
@@ -240,7 +317,21 @@ __device__ __forceinline__ void mm_cols(Acc<T, DP> &acc, const char *tile,
 // Row of register r of an accumulator.
 __device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
 
-__device__ __forceinline__ float swap_halves(float v) { return __shfl_xor(v, 32, 64); }
+// The value of lane ^ 32.
+__device__ __forceinline__ float swap_halves(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float((threadIdx.x & 32) ? w[0] : w[1]);
+}
+
+// The larger of the two halves' values.
+__device__ __forceinline__ float max_halves(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
 
 // acc[d][c] * factor to row `dst` of lane c (null: nothing is stored).
 template <typename T, int DP>
@@ -288,41 +379,63 @@ template <typename T, int DP> struct Softmax {
         l = 0.0f;
     }
 
-    // Takes NS blocks of 32 scores (raw, -infinity where masked) and turns them into e^(c (s - m)).
-    template <int NS> __device__ __forceinline__ void step(float16v (&s)[NS], float c)
+    // The row's largest of NS blocks of 32 scores (raw, -infinity where masked).
+    template <int NS> static __device__ __forceinline__ float top_of(const float16v (&s)[NS])
     {
-        float top = s[0][0];
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top[i] = fmaxf(s[0][i], s[0][i + 4]);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                top = fmaxf(top, s[n][r]);
-        top = fmaxf(top, swap_halves(top));
-        if (__any(top > m + kRaise / c || (m == -INFINITY && top > m))) {
+            for (int r = n == 0 ? 8 : 0; r < 16; r += 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top[i] = fmaxf(fmaxf(top[i], s[n][r + i]), s[n][r + i + 4]);
+        return max_halves(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+    }
+
+    // Raises the maximum if `top` needs it; returns what is taken off the
+    // scores, in powers of two.
+    __device__ __forceinline__ float raise(float top, float c, float margin)
+    {
+        if (__ballot(top > m + margin)) {
             const float up = fmaxf(top, m);
-            const float f = up == -INFINITY ? 1.0f : exp2f((m - up) * c);
+            const float f = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - up) * c);
 #pragma unroll
             for (int b = 0; b < Row<T, DP>::BLOCKS; ++b)
                 o[b] *= f;
             l *= f;
             m = up;
         }
-        const float mc = m == -INFINITY ? 0.0f : m * c;
-        float sum = 0.0f;
+        return m == -INFINITY ? 0.0f : m * c;
+    }
+
+    // Turns scores into e^(scale (s - m)) and adds them up.
+    template <int NS> __device__ __forceinline__ void exps(float16v (&s)[NS], float c, float mc)
+    {
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[n][r] = __builtin_amdgcn_exp2f(fmaf(s[n][r], c, -mc));
-                sum += s[n][r];
+                sum[r & 3] += s[n][r];
             }
-        l += sum;
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+
+    template <int NS> __device__ __forceinline__ void step(float16v (&s)[NS], float c, float margin)
+    {
+        exps<NS>(s, c, raise(top_of<NS>(s), c, margin));
     }
 };
 
-// Recomputes the accumulators of keys [begin, last] one key at a time, each
-// lane for its own row: hidden keys are never touched, whatever they hold.
-template <typename T, int DP>
+// Recomputes the accumulators of keys [begin, end), of every KT keys the first
+// KB, one key at a time, each lane for its own row: hidden keys are never
+// touched, whatever they hold.
+template <typename T, int DP, int KB, int KT>
 __device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *qf, const char *k,
                                                     const char *v, uint32_t k_stride,
                                                     uint32_t v_stride, int begin, int end,
@@ -333,6 +446,8 @@ __device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *qf
     for (int b = 0; b < R::BLOCKS; ++b)
         o[b] = (float16v){};
     for (int j = begin; j < end; ++j) {
+        if (KB < KT && (j - begin) % KT >= KB)
+            continue;
         const T *kr = reinterpret_cast<const T *>(k + uint64_t(j) * k_stride);
         const T *vr = reinterpret_cast<const T *>(v + uint64_t(j) * v_stride);
         float s = 0.0f;
@@ -361,7 +476,7 @@ __device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *qf
 
 // After the tiles [begin, end) that a causal mask cuts, while the accumulators
 // hold nothing else: where they are not finite, recomputes them without the hidden keys.
-template <typename T, int DP>
+template <typename T, int DP, int KB, int KT>
 __device__ __forceinline__ void repair_hidden(Acc<T, DP> &acc, const Frag<T, DP> &qf,
                                               const char *k, const char *v, uint32_t k_stride,
                                               uint32_t v_stride, int begin, int end, int last,
@@ -380,10 +495,12 @@ __device__ __forceinline__ void repair_hidden(Acc<T, DP> &acc, const Frag<T, DP>
 #pragma unroll
         for (int i = 0; i < R::STEPS; ++i)
             f[i] = qf[i];
-        recompute<T, DP>(o, f, k, v, k_stride, v_stride, begin, end, last, m, c, dim, half);
+        recompute<T, DP, KB, KT>(o, f, k, v, k_stride, v_stride, begin, end, last, m, c, dim, half);
 #pragma unroll
-        for (int i = 0; i < R::BLOCKS; ++i)
+        for (int i = 0; i < R::BLOCKS; ++i) {
             acc[i] = o[i];
+            asm volatile("" : "+v"(acc[i]));             // as settle
+        }
     }
 }
 
