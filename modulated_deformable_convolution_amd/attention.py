@@ -35,12 +35,22 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream"):
         return _get(index) or None
 
 
+def _like(shape, dtype, device):
+    """A one-element tensor seen as `shape`: torch.empty_like of it is a third of
+    torch.empty's host time."""
+    return torch.empty((), dtype=dtype, device=device).expand(shape)
+
+
+def _new(template):
+    return torch.empty_like(template, memory_format=torch.contiguous_format)
+
+
 class Rotary:
     """Owns an mdcn_rotary handle."""
 
     def __init__(self, handle: int, dim: int, axes: tuple):
         self.handle, self.dim, self.axes = handle, dim, axes
-        self.calls = {}          # (shapes, strides) -> ctypes dims, as mdcn.Op's
+        self.calls = {}          # shapes, strides, ... -> what _rotary_call returns
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -56,7 +66,7 @@ class Attention:
         self.handle = handle
         self.q_heads, self.k_heads, self.dim = q_heads, k_heads, dim
         self.causal, self.scale = causal, scale
-        self.calls = {}          # (shapes, strides) -> (ctypes dims, workspace bytes)
+        self.calls = {}          # shapes, strides, ... -> what _attend_call returns
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -250,9 +260,9 @@ def norm_rotate_backward(op: Rotary, q, k, positions, q_gain, k_gain, grad_q_out
             n = ctypes.c_size_t()
             _m._check(lib.mdcn_norm_rotate_backward_workspace_bytes(op.handle, q.shape[0],
                                                                     ctypes.byref(n)), where)
-            call = _remember(op.calls, key, call + (n.value,))
+            call = _remember(op.calls, key, call + (_like((n.value,), torch.uint8, q.device),))
         if workspace is None:
-            workspace = torch.empty(call[2], dtype=torch.uint8, device=q.device)
+            workspace = _new(call[2])
     st = lib.mdcn_norm_rotate_backward(
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), positions.data_ptr(),
         q_gain.data_ptr(), k_gain.data_ptr(), eps, grad_q_out.data_ptr(), grad_k_out.data_ptr(),
@@ -266,7 +276,8 @@ def norm_rotate_backward(op: Rotary, q, k, positions, q_gain, k_gain, grad_q_out
 # ---------------------------------------------------------------- attention
 
 def _attend_call(op, where, views, cu_q, cu_k, used_k, grads):
-    """(dtype code, ctypes dims, workspace bytes) of a call."""
+    """(dtype code, ctypes dims, workspace or None, lse) of a call, the last two as
+    templates for _new."""
     q, k = views[:2]
     if q.dim() != 3 or k.dim() != 3:
         _fail(where, "q and k must be [tokens, heads, dim]")
@@ -291,7 +302,8 @@ def _attend_call(op, where, views, cu_q, cu_k, used_k, grads):
     lib = _m.library()
     fn = lib.mdcn_attend_backward_workspace_bytes if grads else lib.mdcn_attend_workspace_bytes
     _m._check(fn(op.handle, code, dims, ctypes.byref(n)), where)
-    return code, dims, n.value
+    return (code, dims, _like((n.value,), torch.uint8, q.device) if n.value else None,
+            _like((op.q_heads, q.shape[0]), torch.float32, q.device))
 
 
 def _check_lse(where, op, q, lse):
@@ -312,18 +324,18 @@ def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, 
     with ctx or _NO_CONTEXT:
         if out is None:
             out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((op.q_heads, q.shape[0]), dtype=torch.float32, device=q.device)
-        else:
-            _check_lse("attend", op, q, lse)
         key = (_sig(q), _sig(k), _sig(v), _sig(out), _sig(cu_q), _sig(cu_k),
                None if used_k is None else _sig(used_k))
         call = op.calls.get(key)
         if call is None:
             call = _remember(op.calls, key, _attend_call(op, "attend", (q, k, v, out), cu_q, cu_k,
                                                          used_k, False))
-        if workspace is None and call[2]:
-            workspace = torch.empty(call[2], dtype=torch.uint8, device=q.device)
+        if lse is None:
+            lse = _new(call[3])
+        else:
+            _check_lse("attend", op, q, lse)
+        if workspace is None and call[2] is not None:
+            workspace = _new(call[2])
     st = _m._lib.mdcn_attend(
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
         cu_k.data_ptr(), None if used_k is None else used_k.data_ptr(), out.data_ptr(),
@@ -350,7 +362,7 @@ def attend_backward(op: Attention, q, k, v, out, lse, grad_out, cu_q, cu_k, used
             call = _remember(op.calls, key, _attend_call(
                 op, where, (q, k, v, out, grad_out, dq, dk, dv), cu_q, cu_k, used_k, True))
         if workspace is None:
-            workspace = torch.empty(call[2], dtype=torch.uint8, device=q.device)
+            workspace = _new(call[2])
     st = _m._lib.mdcn_attend_backward(
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         lse.data_ptr(), grad_out.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),

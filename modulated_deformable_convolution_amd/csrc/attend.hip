@@ -44,11 +44,11 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attend_kernel(AttendArgs a)
     const int kv_head = blockIdx.x % a.k_heads;
     const int group = a.q_heads / a.k_heads;
     const int head = kv_head * group + (blockIdx.x / a.k_heads) % group;
-    int b, tile;
-    if (!find_tile(a.batch, int(blockIdx.x / a.q_heads), lane,
-                   [&](int i) { return (span_of(a, i).lq + ROWS - 1) / ROWS; }, b, tile))
+    Span sp;
+    int tile;
+    if (!find_tile(a, int(blockIdx.x / a.q_heads), lane,
+                   [](const Span &s) { return (s.lq + ROWS - 1) / ROWS; }, sp, tile))
         return;
-    const Span sp = span_of(a, b);
     tile = (sp.lq + ROWS - 1) / ROWS - 1 - tile;             // long rows first
 
     const int r0 = tile * ROWS + rg * 32;                    // wave's first row
@@ -216,10 +216,7 @@ hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 
 template <typename T, int DP> hipError_t launch(const AttendArgs &a, hipStream_t s)
 {
-    // Two workgroups of four waves fit a compute unit.  Up to one each, eight
-    // waves that share the keys two ways use the second half of it.
-    const int64_t blocks = (int64_t(a.q_tokens) / 128 + 1) * a.q_heads;
-    return blocks <= 320 ? launch_shape<T, DP, 4, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
+    return attend_small(a) ? launch_shape<T, DP, 2, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
 }
 
 template <typename T>
@@ -235,6 +232,16 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
 }
 
 }  // namespace
+
+bool attend_small(const AttendArgs &a)
+{
+    // Up to one workgroup of 128 queries a compute unit, workgroups of 64
+    // queries, two waves to the keys of each 32, spread further and end sooner
+    // (208 workgroups of eight f16 heads of 64: 20.8 us against 26.8; fp32, 48
+    // workgroups: 26 against 40).  Beyond, they stage twice the keys a
+    // query (528 workgroups of bf16 heads of 128: 75 us against 55).
+    return (int64_t(a.q_tokens) / 128 + 1) * a.q_heads <= 256;
+}
 
 hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s)
 {

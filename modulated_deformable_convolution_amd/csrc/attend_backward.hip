@@ -20,9 +20,11 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
 
+constexpr int kFar = 1 << 30;                 // more than any number of rows
+
 template <typename T> constexpr int tile_rows() { return sizeof(T) == 2 ? 64 : 32; }
 
-// delta: 16 lanes per (token, head)
+// {lse in powers of two, delta} of every (token, head), 16 lanes each
 template <typename T>
 __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
 {
@@ -44,39 +46,60 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
 #pragma unroll
     for (int m = 1; m < 16; m <<= 1)
         sum += __shfl_xor(sum, m, 64);
-    if ((threadIdx.x & 15) == 0)
-        a.delta[head * int64_t(a.q_tokens) + token] = sum;
+    if ((threadIdx.x & 15) == 0) {
+        const int64_t at = head * int64_t(a.q_tokens) + token;
+        a.stats[at] = make_float2(a.lse[at] * kLog2e, sum);
+    }
 }
 
-template <typename T, int DP>
-__global__ __launch_bounds__(64 * kWaves, 2) void attend_dq_kernel(AttendArgs a)
+template <typename T, int DP, int RW, int KW>
+__global__ __launch_bounds__(64 * RW * KW, 2) void attend_dq_kernel(AttendArgs a)
 {
     using R = Row<T, DP>;
-    constexpr int KB = tile_rows<T>();
-    constexpr int TILE = KB * R::PITCH;
+    constexpr int ROWS = 32 * RW;
+    constexpr int KB = tile_rows<T>();           // keys of a wave's part of a tile
+    constexpr int KT = KB * KW;                  // keys of a tile
+    constexpr int PART = KB * R::PITCH;
+    constexpr int TILE = KT * R::PITCH;
+    constexpr bool AHEAD = sizeof(T) == 2;       // as in attend.hip
     __shared__ __align__(1024) char smem[4 * TILE];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int rg = wave % RW, kg = wave / RW;
     const int half = lane >> 5;
     const int kv_head = blockIdx.x % a.k_heads;
     const int group = a.q_heads / a.k_heads;
     const int head = kv_head * group + (blockIdx.x / a.k_heads) % group;
-    int b, tile;
-    if (!find_tile(a.batch, int(blockIdx.x / a.q_heads), lane,
-                   [&](int i) { return (span_of(a, i).lq + kRows - 1) / kRows; }, b, tile))
+    Span sp;
+    int tile;
+    if (!find_tile(a, int(blockIdx.x / a.q_heads), lane,
+                   [](const Span &s) { return (s.lq + ROWS - 1) / ROWS; }, sp, tile))
         return;
-    const Span sp = span_of(a, b);
-    tile = (sp.lq + kRows - 1) / kRows - 1 - tile;
-    const int r0 = tile * kRows + wave * 32;
+    tile = (sp.lq + ROWS - 1) / ROWS - 1 - tile;
+    const int r0 = tile * ROWS + rg * 32;
     const int row = r0 + (lane & 31);
     const int shift = sp.lk - sp.lq;
     const bool live = row < sp.lq;
     const int last = a.causal ? row + shift : sp.lk - 1;
-    const int block_last = a.causal ? min(tile * kRows + kRows, sp.lq) - 1 + shift : sp.lk - 1;
-    const int nt = block_last < 0 ? 0 : (block_last + KB) / KB;
+    const int block_last = a.causal ? min(tile * ROWS + ROWS, sp.lq) - 1 + shift : sp.lk - 1;
+    const int nt = block_last < 0 ? 0 : block_last / KT + 1;
     const int wave_last = a.causal ? min(r0 + 31, sp.lq - 1) + shift : sp.lk - 1;
     const int wave_first = a.causal ? r0 + shift : sp.lk - 1;
+
+    const char *kbase = row_ptr<T>(a.k, sp.k0, kv_head);
+    const char *vbase = row_ptr<T>(a.v, sp.k0, kv_head);
+    Stager<T, DP, KT, RW * KW> st;
+    st.init(a.k.token_stride, a.v.token_stride, a.dim, wave, lane);
+    const uint32_t lds = lds_address(smem);
+    auto stage = [&](int t) {
+        const int left = sp.lk - t * KT;
+        const uint32_t at = lds + (t & 1) * 2 * TILE;
+        st.template load<0>(at, kbase + uint64_t(t * KT) * st.stride[0], left);
+        st.template load<1>(at + TILE, vbase + uint64_t(t * KT) * st.stride[1], left);
+    };
+    if (nt > 0)
+        stage(0);
 
     Frag<T, DP> qf, gf;
     const int64_t token = sp.q0 + row;
@@ -84,55 +107,87 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_dq_kernel(AttendArgs a)
                      a.dim, half);
     load_frag<T, DP>(gf, live ? reinterpret_cast<const T *>(row_ptr<T>(a.go, token, head)) : nullptr,
                      a.dim, half);
-    const int64_t stat = int64_t(head) * a.q_tokens + token;
-    float lse2 = live ? a.lse[stat] * kLog2e : 0.0f;
-    float delta = live ? a.delta[stat] : 0.0f;
+    float2 stat = make_float2(0.0f, 0.0f);
+    if (live)
+        stat = a.stats[int64_t(head) * a.q_tokens + token];
     settle<T, DP>(qf);
     settle<T, DP>(gf);
-    settle(lse2);
-    settle(delta);
-    const char *kbase = row_ptr<T>(a.k, sp.k0, kv_head);
-    const char *vbase = row_ptr<T>(a.v, sp.k0, kv_head);
-    Stager<T, DP, KB, kWaves> st;
-    st.init(a.k.token_stride, a.v.token_stride, a.dim, wave, lane);
-    const uint32_t lds = lds_address(smem);
+    settle(stat.x);
+    settle(stat.y);
     const float c = a.scale * kLog2e;
 
     Acc<T, DP> dq;
 #pragma unroll
     for (int i = 0; i < R::BLOCKS; ++i)
         dq[i] = (float16v){};
-    auto stage = [&](int t, int buf) {
-        const int left = sp.lk - t * KB;
-        st.template load<0>(lds + buf * 2 * TILE, kbase + uint64_t(t * KB) * st.stride[0], left);
-        st.template load<1>(lds + buf * 2 * TILE + TILE, vbase + uint64_t(t * KB) * st.stride[1],
-                            left);
-    };
-    if (nt > 0)
-        stage(0, 0);
     for (int t = 0; t < nt; ++t) {
         dma_wait<0>();
         lds_barrier();
         if (t + 1 < nt)
-            stage(t + 1, (t + 1) & 1);
-        if (t * KB > wave_last)
+            stage(t + 1);
+        const int key0 = t * KT + kg * KB;
+        if (key0 > wave_last)
             continue;
-        const char *kt = smem + (t & 1) * 2 * TILE;
-        const bool cut = t * KB + KB - 1 > wave_first;
+        const char *kt = smem + (t & 1) * 2 * TILE + kg * PART;
+        const bool cut = key0 + KB - 1 > wave_first;
 #pragma unroll
         for (int n = 0; n < KB / 32; ++n) {
             const char *kn = kt + n * 32 * R::PITCH;
-            float16v s = mm_rows<T, DP>(kn, qf, lane);
-            const float16v dp = mm_rows<T, DP>(kn + TILE, gf, lane);
+            float16v s, dp;
+            Cols<T, DP> kc;
+            if constexpr (AHEAD) {
+                Frag<T, DP> f;
+                load_rows<T, DP>(f, kn, lane);
+                reads_first();
+                s = mm_rows<T, DP>(f, qf);
+                load_rows<T, DP>(f, kn + TILE, lane);
+                reads_first();
+                dp = mm_rows<T, DP>(f, gf);
+                kc.load(kn, lane);
+                reads_first();
+            } else {
+                s = mm_rows<T, DP>(kn, qf, lane);
+                dp = mm_rows<T, DP>(kn + TILE, gf, lane);
+            }
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -stat.x)) * (dp[r] - stat.y);
             if (cut) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    s[r] = t * KB + n * 32 + acc_row(r, half) <= last ? s[r] : 0.0f;
+                    s[r] = key0 + n * 32 + acc_row(r, half) <= last ? s[r] : 0.0f;
             }
-            mm_cols<T, DP>(dq, kn, s, lane);
+            if constexpr (AHEAD)
+                mm_cols<T, DP>(dq, kc, s);
+            else
+                mm_cols<T, DP>(dq, kn, s, lane);
+        }
+    }
+    if constexpr (KW > 1) {
+        // the sums of the waves that shared a row's keys, through LDS
+        static_assert((KW - 1) * RW * DP * 32 * 4 <= 4 * TILE, "the sums fit the stages");
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(smem);
+        auto at = [&](int g) { return sums + ((g - 1) * RW + rg) * DP * 32 + (lane & 31); };
+        if (kg > 0) {
+            float *p = at(kg);
+#pragma unroll
+            for (int d = 0; d < R::BLOCKS; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    p[(d * 32 + acc_row(r, half)) * 32] = dq[d][r];
+        }
+        __syncthreads();
+        if (kg > 0)
+            return;
+#pragma unroll 1
+        for (int g = 1; g < KW; ++g) {
+            const float *p = at(g);
+#pragma unroll
+            for (int d = 0; d < R::BLOCKS; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    dq[d][r] += p[(d * 32 + acc_row(r, half)) * 32];
         }
     }
     if (live)
@@ -140,14 +195,90 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_dq_kernel(AttendArgs a)
                           dq, a.scale, a.dim, half);
 }
 
+// One round of a wave on 32 queries and its 32 keys, the instructions in the
+// order in which they are to run: the products q.k and go.v of the next 32
+// queries (rows at `q_next`, `g_next`), with the probabilities p and ds of
+// these ones computed between them; then p and ds times these queries' go and
+// q.  A wave has its SIMD to itself (it holds 2 x 32 x DP sums and its keys
+// and values in registers), so nothing else hides the vector work or LDS: each
+// MFMA comes with a read eight MFMAs ahead of its use and a share of the vector
+// instructions, and the scheduler may not move them.  The causal mask is always
+// applied: two more vector instructions a score fit under the MFMAs, and a
+// branch around them would have the sums moved between registers every round.
+template <typename T, int DP>
+__device__ __forceinline__ void dkv_round(Acc<T, DP> &dk, Acc<T, DP> &dv, float16v &s, float16v &dp,
+                                          const Frag<T, DP> &kf, const Frag<T, DP> &vf,
+                                          const char *q_next, const char *g_next,
+                                          const char *q_tile, const char *g_tile,
+                                          const float *stats, float c, int first_row, int lane)
+{
+    using R = Row<T, DP>;
+    constexpr int RM = 2 * R::STEPS;                       // row products
+    constexpr int CM = 2 * R::BLOCKS * (32 / R::KROWS);    // column products
+    constexpr int AHEAD = 8 < RM ? 8 : 4;
+    const int half = lane >> 5;
+    uint4 w[AHEAD];
+    auto read = [&](int k) -> uint4 {
+        if (k < RM)
+            return row_frag<T, DP>(k < R::STEPS ? q_next : g_next, k % R::STEPS, lane);
+        const int j = k - RM, d = j % (2 * R::BLOCKS);
+        return col_frag<T, DP>(d < R::BLOCKS ? g_tile : q_tile, j / (2 * R::BLOCKS),
+                               d % R::BLOCKS, lane);
+    };
+    float4v st[8];                                         // {lse, delta} of two rows each
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        w[k] = read(k);
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+        st[g] = *reinterpret_cast<const float4v *>(stats + 2 * acc_row(2 * g, half));
+    __builtin_amdgcn_sched_barrier(0);
+    float16v ns = {}, ndp = {};
+#pragma unroll
+    for (int k = 0; k < RM; ++k) {
+        if (k < R::STEPS)
+            ns = Mma<T>::step(w[k % AHEAD], kf[k], ns);
+        else
+            ndp = Mma<T>::step(w[k % AHEAD], vf[k - R::STEPS], ndp);
+        w[k % AHEAD] = read(k + AHEAD);
+#pragma unroll
+        for (int r = 16 * k / RM; r < 16 * (k + 1) / RM; ++r) {
+            // rows before first_row do not see the lane's key: p = 2^-infinity
+            const float lse =
+                acc_row(r, 0) >= first_row - 4 * half ? st[r / 2][2 * r % 4] : INFINITY;
+            s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse));
+            dp[r] = s[r] * (dp[r] - st[r / 2][2 * r % 4 + 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    uint4 pp, pd;
+#pragma unroll
+    for (int j = 0; j < CM; ++j) {
+        const int step = j / (2 * R::BLOCKS), d = j % (2 * R::BLOCKS);
+        if (d == 0) {
+            pp = pack_p<T>(s, step * R::KROWS / 2);
+            pd = pack_p<T>(dp, step * R::KROWS / 2);
+        }
+        if (d < R::BLOCKS)
+            dv[d] = Mma<T>::step(w[(RM + j) % AHEAD], pp, dv[d]);
+        else
+            dk[d - R::BLOCKS] = Mma<T>::step(w[(RM + j) % AHEAD], pd, dk[d - R::BLOCKS]);
+        if (j + AHEAD < CM)
+            w[(RM + j) % AHEAD] = read(RM + j + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    s = ns;
+    dp = ndp;
+}
+
 template <typename T, int DP>
 __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
 {
     using R = Row<T, DP>;
-    constexpr int QB = tile_rows<T>();
-    constexpr int TILE = QB * R::PITCH;
-    constexpr int STAGE = 2 * TILE + 512;                  // q, go, then lse and delta
-    __shared__ __align__(1024) char smem[2 * STAGE];
+    constexpr int TILE = 32 * R::PITCH;
+    constexpr int STAGE = 2 * TILE + 256;                  // q, go, then {lse, delta}
+    constexpr int STAGES = 4;
+    __shared__ __align__(1024) char smem[STAGES * STAGE];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -155,19 +286,62 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     const int kv_head = blockIdx.x % a.k_heads;
     const int group = a.q_heads / a.k_heads;
     const int part = (blockIdx.x / a.k_heads) % a.splits;
-    int b, tile;
-    if (!find_tile(a.batch, int(blockIdx.x / a.k_heads / a.splits), lane,
-                   [&](int i) { return (span_of(a, i).k_all + kRows - 1) / kRows; }, b, tile))
+    Span sp;
+    int tile;
+    if (!find_tile(a, int(blockIdx.x / a.k_heads / a.splits), lane,
+                   [](const Span &s) { return (s.k_all + kRows - 1) / kRows; }, sp, tile))
         return;
-    const Span sp = span_of(a, b);
     const int k0 = tile * kRows + wave * 32;               // wave's first key
     const int key = k0 + (lane & 31);
     const int shift = sp.lk - sp.lq;
     const bool live = key < sp.lk;
     // first query that sees any of the workgroup's keys
     const int q_first = a.causal ? max(0, tile * kRows - shift) : 0;
-    const int t0 = q_first / QB;
-    const int nt = tile * kRows < sp.lk ? max(0, (sp.lq + QB - 1) / QB - t0) : 0;
+    const int t0 = q_first / 32;
+    const int nt = tile * kRows < sp.lk ? max(0, (sp.lq + 31) / 32 - t0) : 0;
+    // this workgroup's part of the (head, 32 queries) pairs
+    const int i_begin = int(int64_t(nt) * group * part / a.splits);
+    const int i_end = int(int64_t(nt) * group * (part + 1) / a.splits);
+
+    // waves 0 and 1 stage the queries, 2 and 3 their gradients; the rounds are
+    // staged in order, so the next one's addresses are kept and stepped
+    const Heads &src = wave < 2 ? a.q : a.go;
+    Stager<T, DP, 32, 2> st;
+    st.init(src.token_stride, src.token_stride, a.dim, wave & 1, lane);
+    const int rows_step = 32 * int(st.stride[0]);
+    int s_head = kv_head * group, s_t = 0, s_stage = 0;
+    const char *s_row = nullptr;
+    const float2 *s_stat = nullptr;
+    auto stage_at = [&](int head, int t) {
+        s_head = head;
+        s_t = t;
+        s_row = row_ptr<T>(src, sp.q0, head) + int64_t(t) * rows_step;
+        s_stat = a.stats + int64_t(head) * a.q_tokens + sp.q0 + t * 32;
+    };
+    if (i_end > i_begin)
+        stage_at(kv_head * group + i_begin / nt, t0 + i_begin % nt);
+    const uint32_t lds = lds_address(smem) + (wave < 2 ? 0 : TILE);
+    auto stage = [&]() {
+        const int left = sp.lq - s_t * 32;
+        st.template load<0>(lds + s_stage, s_row, left);
+        if (wave == 0)
+            dma_row4(__builtin_amdgcn_readfirstlane(lds + s_stage + 2 * TILE),
+                     row_resource(reinterpret_cast<const char *>(s_stat),
+                                  uint32_t(left < 32 ? left : 32) * 8),
+                     uint32_t(lane) * 4);
+        s_stage = s_stage == (STAGES - 1) * STAGE ? 0 : s_stage + STAGE;
+        if (s_t + 1 < t0 + nt) {
+            ++s_t;
+            s_row += rows_step;
+            s_stat += 32;
+        } else {
+            stage_at(s_head + 1, t0);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (i_begin + i < i_end)
+            stage();
 
     Frag<T, DP> kf, vf;
     load_frag<T, DP>(
@@ -176,79 +350,40 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     load_frag<T, DP>(
         vf, live ? reinterpret_cast<const T *>(row_ptr<T>(a.v, sp.k0 + key, kv_head)) : nullptr,
         a.dim, half);
-    Stager<T, DP, QB, kWaves> st;
-    st.init(a.q.token_stride, a.go.token_stride, a.dim, wave, lane);
     settle<T, DP>(kf);
     settle<T, DP>(vf);
-    const uint32_t lds = lds_address(smem);
     const float c = a.scale * kLog2e;
 
     Acc<T, DP> dk, dv;
 #pragma unroll
     for (int i = 0; i < R::BLOCKS; ++i)
         dk[i] = dv[i] = (float16v){};
-
-    auto stage = [&](int i, int buf) {
-        const int head = kv_head * group + i / nt, t = t0 + i % nt;
-        const int left = sp.lq - t * QB;
-        const uint32_t at = lds + buf * STAGE;
-        st.template load<0>(at, row_ptr<T>(a.q, sp.q0, head) + uint64_t(t * QB) * st.stride[0],
-                            left);
-        st.template load<1>(at + TILE,
-                            row_ptr<T>(a.go, sp.q0, head) + uint64_t(t * QB) * st.stride[1], left);
-        if (wave < 2) {
-            const float *src = (wave == 0 ? a.lse : a.delta) + int64_t(head) * a.q_tokens + sp.q0 +
-                               t * QB;
-            const v4i r = row_resource(reinterpret_cast<const char *>(src),
-                                       uint32_t(left < QB ? left : QB) * 4);
-            dma_row4(__builtin_amdgcn_readfirstlane(at + 2 * TILE + wave * 256), r,
-                     uint32_t(lane) * 4);
-        }
-    };
-    // this workgroup's part of the (head, tile) pairs
-    const int i_begin = int(int64_t(nt) * group * part / a.splits);
-    const int i_end = int(int64_t(nt) * group * (part + 1) / a.splits);
-    if (i_end > i_begin)
-        stage(i_begin, 0);
-    for (int i = i_begin; i < i_end; ++i) {
+    float16v s = {}, dp = {};
+    if (i_end > i_begin) {
         dma_wait<0>();
         lds_barrier();
-        if (i + 1 < i_end)
-            stage(i + 1, (i + 1 - i_begin) & 1);
-        const int q_tile = (t0 + i % nt) * QB;
-        const char *qt = smem + ((i - i_begin) & 1) * STAGE;
-        const float *stat = reinterpret_cast<const float *>(qt + 2 * TILE);
-#pragma unroll
-        for (int n = 0; n < QB / 32; ++n) {
-            const int q0 = q_tile + n * 32;
-            // sees(q, key): key <= q + shift
-            if (a.causal && q0 + 31 + shift < k0)
-                continue;                                  // no row sees any of the wave's keys
-            const char *qn = qt + n * 32 * R::PITCH;
-            float16v s = mm_rows<T, DP>(qn, kf, lane);
-            float16v dp = mm_rows<T, DP>(qn + TILE, vf, lane);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4v ls = *reinterpret_cast<const float4v *>(stat + n * 32 + 8 * g + 4 * half);
-                const float4v de =
-                    *reinterpret_cast<const float4v *>(stat + 64 + n * 32 + 8 * g + 4 * half);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[4 * g + j] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + j], c, -ls[j] * kLog2e));
-                    dp[4 * g + j] = s[4 * g + j] * (dp[4 * g + j] - de[j]);
-                }
-            }
-            if (a.causal && q0 + shift < k0 + 31) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const bool sees = key <= q0 + acc_row(r, half) + shift;
-                    s[r] = sees ? s[r] : 0.0f;
-                    dp[r] = sees ? dp[r] : 0.0f;
-                }
-            }
-            mm_cols<T, DP>(dv, qn + TILE, s, lane);
-            mm_cols<T, DP>(dk, qn, dp, lane);
-        }
+        s = mm_rows<T, DP>(smem, kf, lane);
+        dp = mm_rows<T, DP>(smem + TILE, vf, lane);
+    }
+    int t = i_end > i_begin ? t0 + i_begin % nt : 0;
+    int at = 0;
+    for (int i = i_begin; i < i_end; ++i) {
+        // the next 32 queries have landed; those after them may be on their way
+        if (i + 2 < i_end)
+            dma_wait<Stager<T, DP, 32, 2>::COPIES>();
+        else
+            dma_wait<0>();
+        lds_barrier();
+        if (i + 3 < i_end)
+            stage();
+        const char *q_tile = smem + at;
+        at = at == (STAGES - 1) * STAGE ? 0 : at + STAGE;
+        const char *q_next = smem + at;                      // past the end: not used
+        const float *stats = reinterpret_cast<const float *>(q_tile + 2 * TILE);
+        // sees(q, key): key <= q + shift
+        dkv_round<T, DP>(dk, dv, s, dp, kf, vf, q_next, q_next + TILE, q_tile, q_tile + TILE, stats,
+                         c, a.causal ? key - shift - t * 32 : -kFar, lane);
+        t = t + 1 < t0 + nt ? t + 1 : t0;
     }
     if (key < sp.k_all) {
         // keys that are not used get zeros, whatever the sums hold
@@ -280,11 +415,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void attend_dkv_sum_kernel(AttendArgs a)
 {
     const int kv_head = blockIdx.x % a.k_heads;
-    int b, tile;
-    if (!find_tile(a.batch, int(blockIdx.x / a.k_heads), threadIdx.x & 63,
-                   [&](int i) { return (span_of(a, i).k_all + kSumRows - 1) / kSumRows; }, b, tile))
+    Span sp;
+    int tile;
+    if (!find_tile(a, int(blockIdx.x / a.k_heads), threadIdx.x & 63,
+                   [](const Span &s) { return (s.k_all + kSumRows - 1) / kSumRows; }, sp, tile))
         return;
-    const Span sp = span_of(a, b);
     const int vecs = a.dim / 4;
     const int rows = min(kSumRows, sp.k_all - tile * kSumRows);
     const int64_t all = int64_t(a.k_tokens) * a.k_heads * a.dim;
@@ -316,11 +451,11 @@ int64_t tiles_of(int64_t tokens, int64_t batch, int rows)
     return tokens / rows + (batch < tokens ? batch : tokens);
 }
 
-template <typename T, int DP>
-hipError_t launch(const AttendArgs &a, hipStream_t s)
+template <typename T, int DP, int RW, int KW>
+hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 {
     const int64_t rows = int64_t(a.q_tokens) * a.q_heads;
-    const int64_t q_blocks = tiles_of(a.q_tokens, a.batch, kRows) * a.q_heads;
+    const int64_t q_blocks = tiles_of(a.q_tokens, a.batch, 32 * RW) * a.q_heads;
     const int64_t k_tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t k_blocks = k_tiles * a.splits;
     const int64_t sum_blocks = tiles_of(a.k_tokens, a.batch, kSumRows) * a.k_heads;
@@ -338,10 +473,15 @@ hipError_t launch(const AttendArgs &a, hipStream_t s)
         }
     }
     if (e == hipSuccess && q_blocks > 0) {
-        attend_dq_kernel<T, DP><<<uint32_t(q_blocks), 64 * kWaves, 0, s>>>(a);
+        attend_dq_kernel<T, DP, RW, KW><<<uint32_t(q_blocks), 64 * RW * KW, 0, s>>>(a);
         e = hipGetLastError();
     }
     return e;
+}
+
+template <typename T, int DP> hipError_t launch(const AttendArgs &a, hipStream_t s)
+{
+    return attend_small(a) ? launch_shape<T, DP, 2, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
 }
 
 template <typename T>
@@ -358,13 +498,13 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
 
 }  // namespace
 
-int attend_backward_splits(mdcn_dtype dtype, const AttendArgs &a)
+int attend_backward_splits(const AttendArgs &a)
 {
     // Enough workgroups for two on each of the 256 compute units, with at
-    // least two tiles of queries to each (a part costs its sums' way through memory).
+    // least twice 32 queries to each (a part costs its sums' way through memory).
     const int64_t tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t queries = int64_t(a.q_heads / a.k_heads) * a.q_tokens /
-                            ((dtype == MDCN_F32 ? 32 : 64) * int64_t(a.batch > 0 ? a.batch : 1));
+                            (32 * int64_t(a.batch > 0 ? a.batch : 1));
     int64_t n = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
     n = n < queries / 2 ? n : queries / 2;
     return int(n < 1 ? 1 : n > 8 ? 8 : n);

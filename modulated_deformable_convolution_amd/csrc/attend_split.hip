@@ -32,32 +32,28 @@ template <typename T, int DP> constexpr int split_lds()
     return split_waves<T, DP>() * 4 * kUnit * Row<T, DP>::PITCH;
 }
 
-// Units of sequence b: `keys` per (key head, row tile), at least one.
+// Units of a sequence: `keys` per (key head, row tile), at least one.  A unit is
+// 32 << unit_shift keys, the shift chosen on the host so that the units of any batch of
+// this size can be counted in 31 bits (0 for all but huge caches).
 struct Units {
-    int tiles, keys;
-    int64_t all;
+    int tiles, keys, all;
 };
 
 __device__ __forceinline__ Units units_of(const AttendArgs &a, const Span &s)
 {
     Units u;
-    u.tiles = int((int64_t(s.lq) * (a.q_heads / a.k_heads) + kTileRows - 1) / kTileRows);
-    u.keys = s.lk > 0 ? (s.lk + kUnit - 1) / kUnit : 1;
-    u.all = int64_t(u.tiles) * a.k_heads * u.keys;
+    u.tiles = int((uint32_t(s.lq) * uint32_t(a.q_heads / a.k_heads) + kTileRows - 1) / kTileRows);
+    const int keys = kUnit << a.unit_shift;
+    u.keys = s.lk > keys ? (s.lk + keys - 1) >> (5 + a.unit_shift) : 1;
+    u.all = u.tiles * a.k_heads * u.keys;
     return u;
 }
 
-__device__ __forceinline__ int64_t shfl64(int64_t v, int l)
-{
-    const int lo = __shfl(int(uint32_t(v)), l, 64), hi = __shfl(int(v >> 32), l, 64);
-    return int64_t(uint64_t(uint32_t(hi)) << 32 | uint32_t(lo));
-}
-
-__device__ __forceinline__ int64_t scan64(int64_t v, int lane)
+__device__ __forceinline__ int scan(int v, int lane)
 {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-        const int64_t o = shfl64(v, lane - m);
+        const int o = __shfl_up(v, m, 64);
         v += lane >= m ? o : 0;
     }
     return v;
@@ -66,7 +62,7 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane)
 // The units of 64 sequences, one per lane: its own and those up to it.
 struct Chunk {
     Span span;
-    int64_t mine, upto;
+    int mine, upto;
 
     __device__ __forceinline__ void load(const AttendArgs &a, int b0, int lane)
     {
@@ -76,40 +72,50 @@ struct Chunk {
             span = span_of(a, b0 + lane);
             mine = units_of(a, span).all;
         }
-        upto = scan64(mine, lane);
+        upto = a.batch > 1 ? scan(mine, lane) : __builtin_amdgcn_readfirstlane(mine);
     }
 };
 
 // All units of the batch; `first` is the chunk of its first 64 sequences.
-__device__ __forceinline__ int64_t total_units(const AttendArgs &a, const Chunk &first, int lane)
+__device__ __forceinline__ int total_units(const AttendArgs &a, const Chunk &first, int lane)
 {
-    int64_t sum = shfl64(first.upto, 63);
+    int sum = __builtin_amdgcn_readlane(first.upto, 63);
     if (a.batch > 64) {
-        int64_t more = 0;
+        int more = 0;
         for (int b = 64 + lane; b < a.batch; b += 64)
             more += units_of(a, span_of(a, b)).all;
-        sum += shfl64(scan64(more, lane), 63);
+        sum += __builtin_amdgcn_readlane(scan(more, lane), 63);
     }
     return sum;
 }
 
-__device__ __forceinline__ Span span_in(const Chunk &c, int l)
-{
-    Span s;
-    s.q0 = __builtin_amdgcn_readlane(c.span.q0, l);
-    s.lq = __builtin_amdgcn_readlane(c.span.lq, l);
-    s.k0 = __builtin_amdgcn_readlane(c.span.k0, l);
-    s.lk = __builtin_amdgcn_readlane(c.span.lk, l);
-    s.k_all = __builtin_amdgcn_readlane(c.span.k_all, l);
-    return s;
-}
+// How the units are shared: `n` workgroups, enough units for all waves of each;
+// workgroup i has units [units * i / n, units * (i + 1) / n), so that equal items
+// are cut alike and none straddles two of them needlessly.
+struct Share {
+    int units, n, each, rest;
 
-// Workgroups that share the units: enough units for all waves of each.
-__device__ __forceinline__ int64_t sharers(int64_t units, int workers, int waves)
-{
-    const int64_t most = (units + waves - 1) / waves;
-    return most < workers ? most : workers;
-}
+    __device__ __forceinline__ Share(int units_, int workers, int waves) : units(units_)
+    {
+        n = min((units + waves - 1) / waves, workers);
+        each = n > 0 ? units / n : 0;
+        rest = units - each * n;
+    }
+
+    // units * i / n without the long product (n * n fits)
+    __device__ __forceinline__ int begin(int i) const { return i * each + i * rest / n; }
+
+    // the workgroup that has unit u
+    __device__ __forceinline__ int owner(int u) const
+    {
+        int i = min(int(float(u) * (float(n) / float(units))), n - 1);   // off by one at most
+        while (i + 1 < n && begin(i + 1) <= u)
+            ++i;
+        while (i > 0 && begin(i) > u)
+            --i;
+        return i;
+    }
+};
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
@@ -132,68 +138,66 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
 
     Chunk chunk;
     chunk.load(a, 0, lane);
-    const int64_t units = total_units(a, chunk, lane);
-    const int64_t share = sharers(units, a.workers, NW);
-    if (int64_t(blockIdx.x) >= share)
+    const int units = total_units(a, chunk, lane);
+    const Share share(units, a.workers, NW);
+    if (int(blockIdx.x) >= share.n)
         return;
-    const int64_t u_end = units * (int64_t(blockIdx.x) + 1) / share;
-    const int64_t u_begin = units * int64_t(blockIdx.x) / share;
+    const int u_begin = share.begin(int(blockIdx.x)), u_end = share.begin(int(blockIdx.x) + 1);
 
     Stager<T, DP, kUnit, 1> st;
     st.init(a.k.token_stride, a.v.token_stride, a.dim, 0, lane);
     char *own = smem + wave * 4 * TILE;
     const uint32_t lds = lds_address(own);
 
-    int64_t base = 0;
+    int base = 0;
     for (int b0 = 0; b0 < a.batch && base < u_end; b0 += 64) {
         if (b0 > 0)
             chunk.load(a, b0, lane);
-        const int64_t s_end_l = base + chunk.upto, s_begin_l = s_end_l - chunk.mine;
+        const int s_end_l = base + chunk.upto, s_begin_l = s_end_l - chunk.mine;
         uint64_t mine = __ballot(chunk.mine > 0 && s_end_l > u_begin && s_begin_l < u_end);
         for (; mine; mine &= mine - 1) {
             const int i = __builtin_ctzll(mine);
-            const int64_t s_end = shfl64(s_end_l, i), s_begin = shfl64(s_begin_l, i);
-            const Span sp = span_in(chunk, i);
+            const int s_end = __builtin_amdgcn_readlane(s_end_l, i);
+            const int s_begin = __builtin_amdgcn_readlane(s_begin_l, i);
+            const Span sp = span_in(chunk.span, i);
             const Units un = units_of(a, sp);
             const int shift = sp.lk - sp.lq;
-            const int64_t from = u_begin > s_begin ? u_begin : s_begin;
-            const int64_t to = u_end < s_end ? u_end : s_end;
-            for (int64_t u = from; u < to;) {
+            const int to = min(u_end, s_end);
+            for (int u = max(u_begin, s_begin); u < to;) {
                 // item: a (key head, row tile) of this sequence; keys [n0, n1) of it, in units
-                const int item = int((u - s_begin) / un.keys);
-                const int64_t i_begin = s_begin + int64_t(item) * un.keys;
-                const int n0 = int(u - i_begin);
-                const int n1 = int((to < i_begin + un.keys ? to : i_begin + un.keys) - i_begin);
+                const int item = (u - s_begin) / un.keys;
+                const int i_begin = s_begin + item * un.keys;
+                const int n0 = u - i_begin;
+                const int n1 = min(to - i_begin, un.keys);
                 u = i_begin + n1;
                 const int kv_head = item / un.tiles;
                 const int tile = item % un.tiles;
+                if (kv_head >= a.k_heads)
+                    return;                      // offsets that overlap beyond counting
 
-                const int64_t packed = int64_t(tile) * kTileRows + col;
-                const int row = int(packed / group);
-                const int head = kv_head * group + int(packed % group);
+                const uint32_t packed = uint32_t(tile) * kTileRows + col;
+                const int row = int(packed / uint32_t(group));
+                const int head = kv_head * group + int(packed % uint32_t(group));
                 const bool live = row < sp.lq;
                 const int last = a.causal ? row + shift : sp.lk - 1;
                 const int tile_first =
-                    a.causal ? int(int64_t(tile) * kTileRows / group) + shift : sp.lk - 1;
+                    a.causal ? int(uint32_t(tile) * kTileRows / uint32_t(group)) + shift : sp.lk - 1;
                 const int tile_last =
-                    a.causal ? min(int((int64_t(tile) * kTileRows + 31) / group), sp.lq - 1) + shift
+                    a.causal ? min(int((uint32_t(tile) * kTileRows + 31) / uint32_t(group)),
+                                   sp.lq - 1) + shift
                              : sp.lk - 1;
 
-                Frag<T, DP> qf;
-                load_frag<T, DP>(
-                    qf,
-                    live ? reinterpret_cast<const T *>(row_ptr<T>(a.q, sp.q0 + row, head)) : nullptr,
-                    a.dim, half);
                 const char *kbase = row_ptr<T>(a.k, sp.k0, kv_head);
                 const char *vbase = row_ptr<T>(a.v, sp.k0, kv_head);
                 Softmax<T, DP> sm;
                 sm.init();
                 bool check = a.causal != 0;
 
-                // this wave's units, from the last one down (see attend.hip)
-                const int w0 = n0 + int(int64_t(n1 - n0) * wave / NW);
+                // this wave's tiles of 32 keys, from the last one down (see attend.hip)
+                const int t0 = n0 << a.unit_shift, nt = (n1 - n0) << a.unit_shift;
                 const int visible = tile_last < 0 ? 0 : tile_last / kUnit + 1;
-                const int w1 = min(n0 + int(int64_t(n1 - n0) * (wave + 1) / NW), visible);
+                const int w0 = t0 + nt / NW * wave + min(nt % NW, wave);
+                const int w1 = min(t0 + nt / NW * (wave + 1) + min(nt % NW, wave + 1), visible);
                 auto stage = [&](int t, int buf) {
                     const int left = sp.lk - t * kUnit;
                     st.template load<0>(lds + buf * 2 * TILE,
@@ -201,14 +205,18 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                     st.template load<1>(lds + buf * 2 * TILE + TILE,
                                         vbase + uint64_t(t) * kUnit * st.stride[1], left);
                 };
+                Frag<T, DP> qf;
+                load_frag<T, DP>(
+                    qf,
+                    live ? reinterpret_cast<const T *>(row_ptr<T>(a.q, sp.q0 + row, head)) : nullptr,
+                    a.dim, half);
+                if (w1 > w0)
+                    stage(w1 - 1, 0);
                 auto repair = [&](int begin) {
                     repair_hidden<T, DP, 1, 1>(sm.o, qf, kbase, vbase, st.stride[0], st.stride[1],
                                          begin * kUnit, min(w1 * kUnit, sp.lk), last, sm.m, c,
                                          a.dim, half);
                 };
-                settle<T, DP>(qf);
-                if (w1 > w0)
-                    stage(w1 - 1, 0);
                 for (int j = 0; j < w1 - w0; ++j) {
                     const int t = w1 - 1 - j;
                     // the stage filled next was read last round: those reads are over
@@ -273,8 +281,9 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                                  f, o);
                     }
                     if (whole) {
-                        const int64_t pr = int64_t(tile) * kTileRows + r;
-                        const int qr = int(pr / group), qh = kv_head * group + int(pr % group);
+                        const uint32_t pr = uint32_t(tile) * kTileRows + r;
+                        const int qr = int(pr / uint32_t(group));
+                        const int qh = kv_head * group + int(pr % uint32_t(group));
                         if (d < a.dim)
                             reinterpret_cast<T *>(const_cast<char *>(
                                 row_ptr<T>(a.out, sp.q0 + qr, qh)))[d] =
@@ -293,7 +302,7 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                 __syncthreads();
             }
         }
-        base += shfl64(chunk.upto, 63);
+        base += __builtin_amdgcn_readlane(chunk.upto, 63);
     }
 }
 
@@ -315,39 +324,41 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
 
     Chunk chunk;
     chunk.load(a, 0, lane);
-    const int64_t units = total_units(a, chunk, lane);
-    const int64_t share = sharers(units, a.workers, NW);
-    int64_t base = 0;
+    const int units = total_units(a, chunk, lane);
+    const Share share(units, a.workers, NW);
+    int base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         if (b0 > 0)
             chunk.load(a, b0, lane);
         const uint64_t here =
             __ballot(token >= chunk.span.q0 && token < chunk.span.q0 + chunk.span.lq);
         if (!here) {
-            base += shfl64(chunk.upto, 63);
+            base += __builtin_amdgcn_readlane(chunk.upto, 63);
             continue;
         }
         const int l = __builtin_ctzll(here);
-        const Span sp = span_in(chunk, l);
+        const Span sp = span_in(chunk.span, l);
         const Units un = units_of(a, sp);
-        const int64_t packed = int64_t(token - sp.q0) * group + head % group;
+        const uint32_t packed = uint32_t(token - sp.q0) * group + head % group;
         const int tile = int(packed / kTileRows), r = int(packed % kTileRows);
-        const int64_t first = base + shfl64(chunk.upto, l) - shfl64(chunk.mine, l) +
-                              (int64_t(head / group) * un.tiles + tile) * un.keys;
-        const int64_t i0 = ((first + 1) * share - 1) / units;
-        const int64_t i1 = ((first + un.keys) * share - 1) / units;
-        if (i0 == i1)
+        const int first = base + __builtin_amdgcn_readlane(chunk.upto, l) -
+                          __builtin_amdgcn_readlane(chunk.mine, l) +
+                          (head / group * un.tiles + tile) * un.keys;
+        // (the bounds only matter to offsets that overlap beyond counting)
+        const int i0 = max(share.owner(first), 0);
+        const int i1 = min(share.owner(first + un.keys - 1), a.workers - 1);
+        if (i0 >= i1)
             return;                              // finished where it was computed
         float m = -INFINITY, sum = 0.0f, o[2] = {0.0f, 0.0f};
-        for (int64_t i = i0 + wave; i <= i1; i += 4 * AT_ONCE) {
+        for (int i = i0 + wave; i <= i1; i += 4 * AT_ONCE) {
             float pm[AT_ONCE], ps[AT_ONCE], po[AT_ONCE][2];
 #pragma unroll
             for (int n = 0; n < AT_ONCE; ++n) {
-                const int64_t j = i + 4 * n;
+                const int j = i + 4 * n;
                 const bool ok = j <= i1;
                 const float *p = a.partial +
                                  (2 * (ok ? j : i0) + (!ok || j == i0 ? 1 : 0)) *
-                                     (kTileRows * PART) + r * PART;
+                                     int64_t(kTileRows * PART) + r * PART;
                 pm[n] = ok ? p[0] : -INFINITY;
                 ps[n] = ok ? p[1] : 0.0f;
                 po[n][0] = ok && lane < DP ? p[2 + lane] : 0.0f;
@@ -447,8 +458,14 @@ size_t attend_split_bytes(mdcn_dtype dtype, int dim)
            sizeof(float);
 }
 
-hipError_t launch_attend_split(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s)
+hipError_t launch_attend_split(mdcn_dtype dtype, AttendArgs a, hipStream_t s)
 {
+    // Units of a batch: at most (row tiles) x (key heads) x (units of all keys).
+    const double tiles = double(a.q_tokens) * (a.q_heads / a.k_heads) / kTileRows + a.batch;
+    a.unit_shift = 0;
+    while (tiles * a.k_heads * (double(a.k_tokens >> (5 + a.unit_shift)) + 1) > 1e9 &&
+           a.unit_shift < 16)
+        ++a.unit_shift;
     switch (dtype) {
     case MDCN_F32:
         return launch_dim<float>(a, s);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime_api.h>
+#include <hip/hip_vector_types.h>
 
 #include <cstddef>
 #include <cstdint>
@@ -56,24 +57,27 @@ struct AttendArgs {
     Heads q, k, v, out;    // out: output of the forward, input of the backward
     Heads go, dq, dk, dv;  // backward
     float *lse;            // [q_heads][q_tokens]
-    float *delta;          // backward: [q_heads][q_tokens], sum over dim of go * out
+    float2 *stats;         // backward: [q_heads][q_tokens], {lse * log2(e), sum of go * out}
     const int32_t *cu_q, *cu_k, *used_k;
     int32_t batch, q_tokens, k_tokens;
     int32_t q_heads, k_heads, dim, causal;
     float scale;
-    int32_t workers;       // split kernel
+    int32_t workers;       // split kernel: workgroups, and its unit is 32 << unit_shift keys
+    int32_t unit_shift;
     int32_t splits;        // backward: workgroups that share a tile of keys
     float *partial;        // sums that several workgroups leave for one result
 };
 
+// Whether attend, and dq in the backward, take 64 queries a workgroup and not 128.
+bool attend_small(const AttendArgs &a);
 hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
 // Workgroups of the split kernel and the bytes of `partial` they need.
 int attend_split_workers(mdcn_dtype dtype, int dim);
 size_t attend_split_bytes(mdcn_dtype dtype, int dim);
-hipError_t launch_attend_split(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
+hipError_t launch_attend_split(mdcn_dtype dtype, AttendArgs a, hipStream_t s);
 // Workgroups that share the queries of a tile of keys; more than one need
 // splits * 2 * k_tokens * k_heads * dim floats of `partial`.
-int attend_backward_splits(mdcn_dtype dtype, const AttendArgs &a);
+int attend_backward_splits(const AttendArgs &a);
 hipError_t launch_attend_backward(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
 
 }  // namespace mdcn

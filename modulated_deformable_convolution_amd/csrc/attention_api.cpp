@@ -225,10 +225,10 @@ mdcn_status check_attend_view(View &v)
     return MDCN_OK;
 }
 
-// The backward's delta, up to the next 256 bytes.
-size_t delta_bytes(const AttendArgs &a)
+// The backward's row statistics, up to the next 256 bytes.
+size_t stats_bytes(const AttendArgs &a)
 {
-    return (size_t(a.q_heads) * a.q_tokens * sizeof(float) + 255) / 256 * 256;
+    return (size_t(a.q_heads) * a.q_tokens * sizeof(float2) + 255) / 256 * 256;
 }
 
 // The kernel for few query rows per sequence.
@@ -567,8 +567,8 @@ mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_
     const mdcn_status st = attend_dims(op, dtype, dims, &a);
     if (st != MDCN_OK)
         return st;
-    const int splits = mdcn::attend_backward_splits(dtype, a);
-    *bytes = delta_bytes(a) + 256;
+    const int splits = mdcn::attend_backward_splits(a);
+    *bytes = stats_bytes(a) + 256;
     if (splits > 1)
         *bytes += size_t(splits) * 2 * a.k_tokens * a.k_heads * a.dim * sizeof(float);
     return MDCN_OK;
@@ -641,9 +641,9 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
         a.dk = g[1].h;
         a.dv = g[2].h;
         a.lse = const_cast<float *>(lse);
-        a.delta = static_cast<float *>(align_up(workspace));
-        a.partial = reinterpret_cast<float *>(reinterpret_cast<char *>(a.delta) + delta_bytes(a));
-        a.splits = mdcn::attend_backward_splits(dtype, a);
+        a.stats = static_cast<float2 *>(align_up(workspace));
+        a.partial = reinterpret_cast<float *>(reinterpret_cast<char *>(a.stats) + stats_bytes(a));
+        a.splits = mdcn::attend_backward_splits(a);
         a.cu_q = cu_q;
         a.cu_k = cu_k;
         a.used_k = used_k;

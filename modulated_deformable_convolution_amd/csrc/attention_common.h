@@ -196,6 +196,16 @@ __device__ __forceinline__ void load_rows(Frag<T, DP> &a, const char *tile, int 
         a[k] = *reinterpret_cast<const uint4 *>(p + ((2 * k + half) ^ sw) * 16);
 }
 
+// Read k of load_rows alone.
+template <typename T, int DP>
+__device__ __forceinline__ uint4 row_frag(const char *tile, int k, int lane)
+{
+    using R = Row<T, DP>;
+    const int row = lane & 31;
+    return *reinterpret_cast<const uint4 *>(tile + row * R::PITCH +
+                                            ((2 * k + (lane >> 5)) ^ R::swz(row)) * 16);
+}
+
 template <typename T, int DP>
 __device__ __forceinline__ float16v mm_rows(const Frag<T, DP> &a, const Frag<T, DP> &f)
 {
@@ -529,15 +539,31 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b)
     return s;
 }
 
-// The sequence and its tile that hold tile t of the batch, where `count(b)`
-// is the number of tiles of sequence b; false past the last tile.  Every
-// lane of the wave must call it.
+// The span that lane l holds, for all lanes.
+__device__ __forceinline__ Span span_in(const Span &mine, int l)
+{
+    Span s;
+    s.q0 = __builtin_amdgcn_readlane(mine.q0, l);
+    s.lq = __builtin_amdgcn_readlane(mine.lq, l);
+    s.k0 = __builtin_amdgcn_readlane(mine.k0, l);
+    s.lk = __builtin_amdgcn_readlane(mine.lk, l);
+    s.k_all = __builtin_amdgcn_readlane(mine.k_all, l);
+    return s;
+}
+
+// The sequence and its tile that hold tile t of the batch, where count(span)
+// is the number of a sequence's tiles; false past the last tile.  Every lane
+// of the wave must call it.
 template <class F>
-__device__ __forceinline__ bool find_tile(int batch, int t, int lane, F &&count, int &b, int &tile)
+__device__ __forceinline__ bool find_tile(const AttendArgs &a, int t, int lane, F &&count, Span &sp,
+                                          int &tile)
 {
     int base = 0;
-    for (int b0 = 0; b0 < batch; b0 += 64) {
-        const int mine = b0 + lane < batch ? count(b0 + lane) : 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        Span s = {};
+        if (b0 + lane < a.batch)
+            s = span_of(a, b0 + lane);
+        const int mine = count(s);
         int upto = mine;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -547,12 +573,12 @@ __device__ __forceinline__ bool find_tile(int batch, int t, int lane, F &&count,
         const uint64_t past = __ballot(base + upto > t);
         if (past) {
             const int l = __builtin_ctzll(past);
-            b = __builtin_amdgcn_readfirstlane(b0 + l);
-            tile = __builtin_amdgcn_readfirstlane(
-                t - base - (__shfl(upto, l, 64) - __shfl(mine, l, 64)));
+            sp = span_in(s, l);
+            tile = t - base -
+                   (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
             return true;
         }
-        base += __shfl(upto, 63, 64);
+        base += __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
