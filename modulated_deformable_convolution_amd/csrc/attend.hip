@@ -21,7 +21,7 @@ namespace {
 template <typename T> constexpr int tile_keys() { return sizeof(T) == 2 ? 64 : 32; }
 
 template <typename T, int DP, int RW, int KW>
-__global__ __launch_bounds__(64 * RW * KW, 2) void attend_kernel(AttendArgs a)
+__global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void attend_kernel(AttendArgs a)
 {
     using R = Row<T, DP>;
     constexpr int ROWS = 32 * RW;

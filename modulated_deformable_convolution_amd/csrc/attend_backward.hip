@@ -53,7 +53,7 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
 }
 
 template <typename T, int DP, int RW, int KW>
-__global__ __launch_bounds__(64 * RW * KW, 2) void attend_dq_kernel(AttendArgs a)
+__global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void attend_dq_kernel(AttendArgs a)
 {
     using R = Row<T, DP>;
     constexpr int ROWS = 32 * RW;

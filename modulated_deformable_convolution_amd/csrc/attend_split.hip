@@ -12,6 +12,8 @@
 // for); the waves' results are joined in LDS.  A (sequence, head, tile) that lies
 // in one range is finished there; otherwise its parts (sums, maxima and
 // unscaled outputs in fp32) go to the workspace and a second kernel joins them.
+#include <cmath>
+
 #include "attention_common.h"
 
 namespace mdcn {
@@ -450,6 +452,28 @@ int attend_split_workers(mdcn_dtype dtype, int dim)
     // 256- or 512-byte row, less below)
     const int bytes = padded_dim(dim) * (dtype == MDCN_F32 ? 4 : 2);
     return kComputeUnits * (bytes > 128 ? 1 : bytes > 64 ? 2 : 4);
+}
+
+// In rounds of the tile kernel on 64 queries (1.75 us for bf16 heads of 128, 0.83
+// us for f16 of 64, 3.9 us for fp32 of 80): it takes one for each 128 keys (fp32:
+// 64) and 256 workgroups; the split kernel about 5/4 of one for each 32 keys x 32 rows of a
+// wave, four more to start and join, and one for 512 rows to be joined.
+// Measured on both sides (32 query and 8 key heads of 128 in bf16, one sequence; split
+// against tile, us): 1 query, 128 keys 17 / 12; 1 and 64 queries, 1024 keys 17 / 22 and
+// 30 / 23; 1, 128 and 512 queries, 8192 keys 18 / 123, 72 / 122 and 233 / 130.
+// Only averages are known here: the lengths are on the GPU.
+bool attend_prefers_split(mdcn_dtype dtype, const AttendArgs &a)
+{
+    if (a.batch == 0 || a.q_tokens == 0)
+        return false;
+    const double queries = double(a.q_tokens) / a.batch, keys = double(a.k_tokens) / a.batch;
+    const double group = a.q_heads / a.k_heads;
+    const double blocks = double(a.batch) * a.q_heads * std::ceil(queries / 64);
+    const double rounds = (keys / (dtype == MDCN_F32 ? 64 : 128) + 1) * std::ceil(blocks / 256);
+    const double units = double(a.batch) * a.k_heads * std::ceil(queries * group / kTileRows) *
+                         (keys / kUnit + 1);
+    const double waves = attend_split_workers(dtype, a.dim) * (dtype == MDCN_F32 && a.dim > 64 ? 2 : 4);
+    return 1.25 * std::ceil(units / waves) + 4 + double(a.q_tokens) * a.q_heads / 512 < rounds;
 }
 
 size_t attend_split_bytes(mdcn_dtype dtype, int dim)

@@ -71,6 +71,9 @@ struct AttendArgs {
 // Whether attend, and dq in the backward, take 64 queries a workgroup and not 128.
 bool attend_small(const AttendArgs &a);
 hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
+// Whether the kernel that splits keys over the chip is the faster one for a
+// batch of these sizes.
+bool attend_prefers_split(mdcn_dtype dtype, const AttendArgs &a);
 // Workgroups of the split kernel and the bytes of `partial` they need.
 int attend_split_workers(mdcn_dtype dtype, int dim);
 size_t attend_split_bytes(mdcn_dtype dtype, int dim);

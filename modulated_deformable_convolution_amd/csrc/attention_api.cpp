@@ -231,13 +231,6 @@ size_t stats_bytes(const AttendArgs &a)
     return (size_t(a.q_heads) * a.q_tokens * sizeof(float2) + 255) / 256 * 256;
 }
 
-// The kernel for few query rows per sequence.
-bool attend_uses_split(const AttendArgs &a)
-{
-    const int64_t rows = int64_t(a.q_tokens) * (a.q_heads / a.k_heads);
-    return rows <= int64_t(64) * a.batch;
-}
-
 }  // namespace
 
 extern "C" {
@@ -491,7 +484,7 @@ mdcn_status mdcn_attend_workspace_bytes(const mdcn_attention *op, mdcn_dtype dty
     const mdcn_status st = attend_dims(op, dtype, dims, &a);
     if (st != MDCN_OK)
         return st;
-    *bytes = attend_uses_split(a) ? mdcn::attend_split_bytes(dtype, a.dim) + 256 : 0;
+    *bytes = mdcn::attend_prefers_split(dtype, a) ? mdcn::attend_split_bytes(dtype, a.dim) + 256 : 0;
     return MDCN_OK;
 }
 

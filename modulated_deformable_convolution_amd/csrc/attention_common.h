@@ -367,6 +367,15 @@ __device__ __forceinline__ void store_cols(T *dst, const Acc<T, DP> &acc,
         }
 }
 
+// Waves a SIMD that a tile kernel's registers are to leave room for: two workgroups
+// of four waves, unless the LDS of one (two stages of K and V) leaves no room
+// or 256 registers do not hold a wave's sums and operands.
+template <typename T, int DP, int KW> constexpr int waves_per_simd()
+{
+    constexpr int lds = 4 * (sizeof(T) == 2 ? 64 : 32) * KW * Row<T, DP>::PITCH;
+    return lds > 80 * 1024 || (sizeof(T) == 4 && DP > 96) ? 1 : 2;
+}
+
 // ---- softmax ---------------------------------------------------------------
 
 // The running maximum is raised only when a score exceeds it by more than

@@ -151,10 +151,28 @@ __device__ __forceinline__ void angles(float (&c)[U][V], float (&s)[U][V], Angle
     }
 }
 
+template <int CTRL> __device__ __forceinline__ float lane_add(float v)
+{
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf,
+                                                          true));
+}
+
+// Sum over the `group` lanes (a power of two, aligned) that share a head.  Up to
+// 16 lanes without LDS: neighbours, pairs, then mirrored halves and rows.
 __device__ __forceinline__ float group_sum(float v, int group)
 {
-    for (int m = 1; m < group; m <<= 1)
-        v += __shfl_xor(v, m, 64);
+    if (group > 1)
+        v = lane_add<0xb1>(v);                       // quad: lane ^ 1
+    if (group > 2)
+        v = lane_add<0x4e>(v);                       // quad: lane ^ 2
+    if (group > 4)
+        v = lane_add<0x141>(v);                      // 7 - lane of each 8
+    if (group > 8)
+        v = lane_add<0x140>(v);                      // 15 - lane of each 16
+    if (group > 16)
+        v += __shfl_xor(v, 16, 64);
+    if (group > 32)
+        v += __shfl_xor(v, 32, 64);
     return v;
 }
 

@@ -118,8 +118,9 @@ def attend_status(dtype=2, q_tokens=300, change={}, ptr={}, ws=1 << 26):
     (dict(ptr={"q": 0}), "NULL"), (dict(ptr={"v": 0}), "NULL"), (dict(ptr={"cu_q": 0}), "NULL"),
     (dict(ptr={"cu_k": 0}), "NULL"), (dict(ptr={"lse": 0}), "NULL"),
     (dict(ptr={"out": BASE}), "ALIAS"), (dict(ptr={"lse": BASE}), "ALIAS"),
-    (dict(q_tokens=3, ws=16), "WORKSPACE"), (dict(q_tokens=3, ptr={"ws": 0}), "WORKSPACE"),
-    (dict(q_tokens=3, ptr={"ws": BASE}), "ALIAS"),
+    (dict(q_tokens=3, change={2: 60000}, ws=16), "WORKSPACE"),
+    (dict(q_tokens=3, change={2: 60000}, ptr={"ws": 0}), "WORKSPACE"),
+    (dict(q_tokens=3, change={2: 60000}, ptr={"ws": BASE}), "ALIAS"),
 ])
 def test_attend_refuses(kw, code):
     assert attend_status(**kw) == getattr(mdcn, "MDCN_E_" + code)

@@ -192,15 +192,16 @@ def test_attend(case, dt):
 def test_attend_dims(dim, dt):
     check_attend(([37, 130], None, 2, 1, dim, True), DTYPES[dt])
     check_attend(([2, 1], [37, 130], 2, 1, dim, True), DTYPES[dt])
+    check_attend(([2, 1], [2500, 1300], 2, 1, dim, True), DTYPES[dt], train=False)
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("new", [1, 2, 5])
 @pytest.mark.parametrize("heads", [(8, 2), (7, 1), (4, 4), (32, 1)])
-def test_decode(heads, new, dt):
+@pytest.mark.parametrize("size", [300, 2600])
+def test_decode(size, heads, new, dt):
     hq, hk = heads
-    size = 300
-    used = [new, 300, 31, 32, 33, 0, 257, 64, 128, 1]
+    used = [new, size, 31, 32, 33, 0, 257, 64, 128, 1, size - 1]
     case = ([new] * len(used), [size] * len(used), hq, hk, 64 if new == 2 else 128, True)
     check_attend(case, DTYPES[dt], train=False, used=used)
 
@@ -220,11 +221,11 @@ def test_training_against_a_partly_used_cache(dt):
 
 
 @pytest.mark.parametrize("causal", [False, True])
-@pytest.mark.parametrize("rows", [1, 3, 200])
+@pytest.mark.parametrize("rows,size", [(1, 250), (3, 250), (200, 250), (1, 3001), (3, 3001)])
 @pytest.mark.parametrize("dt", list(DTYPES))
-def test_unused_cache_rows_are_never_used(dt, rows, causal):
+def test_unused_cache_rows_are_never_used(dt, rows, size, causal):
     dtype = DTYPES[dt]
-    case = ([rows, rows], [250, 333], 4, 2, 64, causal)
+    case = ([rows, rows], [size, 333], 4, 2, 64, causal)
     op, q, k, v, dq, dk, dv, cq, ck = attend_case(case, dtype)
     used = [211, 33]
     for x in (dk, dv):
@@ -237,14 +238,14 @@ def test_unused_cache_rows_are_never_used(dt, rows, causal):
 
 
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("rows", [4, 150])
+@pytest.mark.parametrize("rows,keys", [(4, 170), (150, 170), (4, 3000)])
 @pytest.mark.parametrize("dt", list(DTYPES))
-def test_hidden_values_reach_no_row(dt, rows, value):
+def test_hidden_values_reach_no_row(dt, rows, keys, value):
     """A row of k and v that is not finite shows in the rows that see it only."""
     dtype = DTYPES[dt]
-    case = ([rows, 3], [170, 3], 2, 1, 64, True)
+    case = ([rows, 3], [keys, 3], 2, 1, 64, True)
     op, q, k, v, dq, dk, dv, cq, ck = attend_case(case, dtype)
-    at = 170 - 2                                       # seen by the last two rows of sequence 0
+    at = keys - 2                                       # seen by the last two rows of sequence 0
     ref = R.attend(q, k, v, cq, ck, None, True, op.scale, dtype)
     for x in (dv, dk):
         x[at] = value
@@ -315,12 +316,18 @@ def test_offsets_outside_the_tensors_stay_inside():
     op = A.mdcn_attention_create(2, 1, 64, True)
     q, kv = rand(20, 2, 64, seed=1, dtype=torch.bfloat16).cuda(), \
         rand(20, 1, 64, seed=2, dtype=torch.bfloat16).cuda()
+    cache = torch.zeros(7000, 1, 64, dtype=torch.bfloat16, device="cuda")
     for offsets in ([0, 1 << 30], [-5, 400, 20], [20, 3, -7], [7, 7, 7], [1 << 30, -(1 << 30)]):
         out = torch.full((20, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
         out, lse = A.attend(op, q, kv, kv, ints(offsets), ints(offsets), out=out)
         A.attend_backward(op, q, kv, kv, out, lse, q, ints(offsets), ints(offsets))
         used = ints([1 << 30] * (len(offsets) - 1))
         A.attend(op, q[:2], kv, kv, ints(offsets), ints(offsets), used_k=used)
+        A.attend(op, q[:2], cache, cache, ints(offsets), ints([min(5000 * v, 1 << 30) for v in offsets[:-1]] +
+                                                              [7000]), used_k=used)
+    # sequences that all claim the whole cache
+    many = ints([0, 2] * 300 + [0])
+    A.attend(op, q[:2], cache, cache, many, ints([0, 7000] * 300 + [0]))
     torch.cuda.synchronize()
 
 
