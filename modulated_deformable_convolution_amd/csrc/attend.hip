@@ -87,9 +87,9 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     bool check = a.causal != 0;                              // hidden keys seen so far
     auto repair = [&](int i) {
         // this wave's keys of the rounds before i, one round at a time
-        repair_hidden<T, DP, KB, KT>(sm.o, qf, kbase, vbase, st.stride[0], st.stride[1],
-                                     (nt - i) * KT + kg * KB, min(wave_last + 1, sp.lk), last, sm.m,
-                                     c, a.dim, half);
+        repair_hidden<T, DP, KB, KT, false>(
+            sm.o, qf, qf, kbase, vbase, st.stride[0], st.stride[1], (nt - i) * KT + kg * KB,
+            min(wave_last + 1, sp.lk), RowTerms{last, sm.m, 0.0f, c}, a.dim, half);
     };
 
     for (int i = 0; i < nt; ++i) {

@@ -92,9 +92,12 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     Stager<T, DP, KT, RW * KW> st;
     st.init(a.k.token_stride, a.v.token_stride, a.dim, wave, lane);
     const uint32_t lds = lds_address(smem);
-    auto stage = [&](int t) {
+    // round i handles tile nt - 1 - i, in stage i & 1: the tiles that a causal
+    // mask cuts come first (see repair_hidden)
+    auto stage = [&](int i) {
+        const int t = nt - 1 - i;
         const int left = sp.lk - t * KT;
-        const uint32_t at = lds + (t & 1) * 2 * TILE;
+        const uint32_t at = lds + (i & 1) * 2 * TILE;
         st.template load<0>(at, kbase + uint64_t(t * KT) * st.stride[0], left);
         st.template load<1>(at + TILE, vbase + uint64_t(t * KT) * st.stride[1], left);
     };
@@ -120,16 +123,26 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
 #pragma unroll
     for (int i = 0; i < R::BLOCKS; ++i)
         dq[i] = (float16v){};
-    for (int t = 0; t < nt; ++t) {
+    bool check = a.causal != 0;                              // hidden keys seen so far
+    auto repair = [&](int i) {
+        repair_hidden<T, DP, KB, KT, true>(
+            dq, qf, gf, kbase, vbase, st.stride[0], st.stride[1], (nt - i) * KT + kg * KB,
+            min(wave_last + 1, sp.lk), RowTerms{last, stat.x, stat.y, c}, a.dim, half);
+    };
+    for (int i = 0; i < nt; ++i) {
         dma_wait<0>();
         lds_barrier();
-        if (t + 1 < nt)
-            stage(t + 1);
-        const int key0 = t * KT + kg * KB;
+        if (i + 1 < nt)
+            stage(i + 1);
+        const int key0 = (nt - 1 - i) * KT + kg * KB;
         if (key0 > wave_last)
             continue;
-        const char *kt = smem + (t & 1) * 2 * TILE + kg * PART;
+        const char *kt = smem + (i & 1) * 2 * TILE + kg * PART;
         const bool cut = key0 + KB - 1 > wave_first;
+        if (check && !cut) {
+            repair(i);
+            check = false;
+        }
 #pragma unroll
         for (int n = 0; n < KB / 32; ++n) {
             const char *kn = kt + n * 32 * R::PITCH;
@@ -163,6 +176,8 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
                 mm_cols<T, DP>(dq, kn, s, lane);
         }
     }
+    if (check && nt > 0)
+        repair(nt);
     if constexpr (KW > 1) {
         // the sums of the waves that shared a row's keys, through LDS
         static_assert((KW - 1) * RW * DP * 32 * 4 <= 4 * TILE, "the sums fit the stages");

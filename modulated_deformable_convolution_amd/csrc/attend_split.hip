@@ -215,9 +215,9 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                 if (w1 > w0)
                     stage(w1 - 1, 0);
                 auto repair = [&](int begin) {
-                    repair_hidden<T, DP, 1, 1>(sm.o, qf, kbase, vbase, st.stride[0], st.stride[1],
-                                         begin * kUnit, min(w1 * kUnit, sp.lk), last, sm.m, c,
-                                         a.dim, half);
+                    repair_hidden<T, DP, 1, 1, false>(
+                        sm.o, qf, qf, kbase, vbase, st.stride[0], st.stride[1], begin * kUnit,
+                        min(w1 * kUnit, sp.lk), RowTerms{last, sm.m, 0.0f, c}, a.dim, half);
                 };
                 for (int j = 0; j < w1 - w0; ++j) {
                     const int t = w1 - 1 - j;

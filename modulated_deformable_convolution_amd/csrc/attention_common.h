@@ -319,8 +319,9 @@ __device__ __forceinline__ void mm_cols(Acc<T, DP> &acc, const char *tile, const
     for (int s = 0; s < 32 / R::KROWS; ++s) {
         const uint4 b = pack_p<T>(p, s * R::KROWS / 2);
 #pragma unroll
-        for (int d = 0; d < R::BLOCKS; ++d)
+        for (int d = 0; d < R::BLOCKS; ++d) {
             acc[d] = Mma<T>::step(col_frag<T, DP>(tile, s, d, lane), b, acc[d]);
+        }
     }
 }
 
@@ -451,17 +452,43 @@ template <typename T, int DP> struct Softmax {
     }
 };
 
+// What a row's accumulators are made of: sum over its keys of weight(s, v row) *
+// the row of k or v, for the forward and for the gradient of the queries.
+struct RowTerms {
+    int last;                 // last visible key
+    float m;                  // forward: maximum; backward: lse in powers of two
+    float delta;              // backward only
+    float c;
+};
+
+template <typename T, int DP>
+__device__ __forceinline__ float half_dot(const uint4 *f, const T *row, int dim, int half)
+{
+    constexpr int E = 16 / sizeof(T);
+    float s = 0.0f;
+    for (int i = 0; i < Row<T, DP>::STEPS; ++i) {
+        const int d = (2 * i + half) * E;
+        if (d >= dim)
+            break;
+        Vec16<T> a;
+        a.raw = f[i];
+        const Vec16<T> b = load16(row + d);
+        for (int e = 0; e < E; ++e)
+            s = fmaf(to_f32(a.e[e]), to_f32(b.e[e]), s);
+    }
+    return s + swap_halves(s);
+}
+
 // Recomputes the accumulators of keys [begin, end), of every KT keys the first
 // KB, one key at a time, each lane for its own row: hidden keys are never
-// touched, whatever they hold.
+// touched, whatever they hold.  `g` is null in the forward.
 template <typename T, int DP, int KB, int KT>
-__device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *qf, const char *k,
-                                                    const char *v, uint32_t k_stride,
+__device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *q, const uint4 *g,
+                                                    const char *k, const char *v, uint32_t k_stride,
                                                     uint32_t v_stride, int begin, int end,
-                                                    int last, float m, float c, int dim, int half)
+                                                    const RowTerms *t, int dim, int half)
 {
     using R = Row<T, DP>;
-    constexpr int E = 16 / sizeof(T);
     for (int b = 0; b < R::BLOCKS; ++b)
         o[b] = (float16v){};
     for (int j = begin; j < end; ++j) {
@@ -469,37 +496,30 @@ __device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *qf
             continue;
         const T *kr = reinterpret_cast<const T *>(k + uint64_t(j) * k_stride);
         const T *vr = reinterpret_cast<const T *>(v + uint64_t(j) * v_stride);
-        float s = 0.0f;
-        for (int i = 0; i < R::STEPS; ++i) {
-            const int d = (2 * i + half) * E;
-            if (d >= dim)
-                break;
-            Vec16<T> qv;
-            qv.raw = qf[i];
-            const Vec16<T> kv = load16(kr + d);
-            for (int e = 0; e < E; ++e)
-                s = fmaf(to_f32(qv.e[e]), to_f32(kv.e[e]), s);
-        }
-        s += swap_halves(s);
-        if (j > last)
+        const float s = half_dot<T, DP>(q, kr, dim, half);
+        const float dp = g ? half_dot<T, DP>(g, vr, dim, half) : 0.0f;
+        if (j > t->last)
             continue;
-        const float p = exp2f(fmaf(s, c, -m * c));
+        float w = exp2f(fmaf(s, t->c, g ? -t->m : -t->m * t->c));
+        if (g)
+            w *= dp - t->delta;
+        const T *row = g ? kr : vr;
         for (int b = 0; b < R::BLOCKS; ++b)
             for (int r = 0; r < 16; ++r) {
                 const int d = b * 32 + acc_row(r, half);
                 if (d < dim)
-                    o[b][r] = fmaf(p, to_f32(vr[d]), o[b][r]);
+                    o[b][r] = fmaf(w, to_f32(row[d]), o[b][r]);
             }
     }
 }
 
 // After the tiles [begin, end) that a causal mask cuts, while the accumulators
 // hold nothing else: where they are not finite, recomputes them without the hidden keys.
-template <typename T, int DP, int KB, int KT>
+template <typename T, int DP, int KB, int KT, bool BACKWARD>
 __device__ __forceinline__ void repair_hidden(Acc<T, DP> &acc, const Frag<T, DP> &qf,
-                                              const char *k, const char *v, uint32_t k_stride,
-                                              uint32_t v_stride, int begin, int end, int last,
-                                              float m, float c, int dim, int half)
+                                              const Frag<T, DP> &gf, const char *k, const char *v,
+                                              uint32_t k_stride, uint32_t v_stride, int begin,
+                                              int end, const RowTerms &terms, int dim, int half)
 {
     using R = Row<T, DP>;
     float bad = 0.0f;
@@ -510,11 +530,16 @@ __device__ __forceinline__ void repair_hidden(Acc<T, DP> &acc, const Frag<T, DP>
             bad += acc[i][r] * 0.0f;
     if (__any(bad != 0.0f)) {
         Acc<T, DP> o;                                    // copies: only they are
-        Frag<T, DP> f;                                   // addressed in memory
+        Frag<T, DP> f, g;                                // addressed in memory
+        const RowTerms t = terms;
 #pragma unroll
-        for (int i = 0; i < R::STEPS; ++i)
+        for (int i = 0; i < R::STEPS; ++i) {
             f[i] = qf[i];
-        recompute<T, DP, KB, KT>(o, f, k, v, k_stride, v_stride, begin, end, last, m, c, dim, half);
+            if (BACKWARD)
+                g[i] = gf[i];
+        }
+        recompute<T, DP, KB, KT>(o, f, BACKWARD ? g : nullptr, k, v, k_stride, v_stride, begin, end,
+                                 &t, dim, half);
 #pragma unroll
         for (int i = 0; i < R::BLOCKS; ++i) {
             acc[i] = o[i];

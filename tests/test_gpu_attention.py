@@ -257,6 +257,24 @@ def test_hidden_values_reach_no_row(dt, rows, keys, value):
         assert not out[~clean].isfinite().any()
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_hidden_keys_reach_no_query_gradient(dt, value):
+    dtype = DTYPES[dt]
+    case = ([150, 3], [170, 3], 2, 1, 64, True)
+    op, q, k, v, dq, dk, dv, cq, ck = attend_case(case, dtype)
+    go = rand(*q.shape, seed=9, dtype=dtype)
+    ref = R.attend(q, k, v, cq, ck, None, True, op.scale, dtype, go)
+    clean = torch.ones(153, dtype=torch.bool)
+    clean[148:150] = False                             # the rows that see key 168
+    for x in (dv, dk):
+        x[168] = value
+        out, lse = A.attend(op, dq, dk, dv, ints(cq), ints(ck))
+        got = A.attend_backward(op, dq, dk, dv, out, lse, go.cuda(), ints(cq), ints(ck))["q"]
+        within(got[clean.cuda()], (ref["q"][0][clean], ref["q"][1][clean]), "dq")
+        assert not got[~clean.cuda()].isfinite().all(-1).any()
+
+
 def test_masked_rows_with_extreme_scores():
     """Scores at the ends of the range: the softmax stays exact where it is defined."""
     for dtype in DTYPES.values():
