@@ -46,10 +46,9 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     const int head = kv_head * group + (blockIdx.x / a.k_heads) % group;
     Span sp;
     int tile;
-    if (!find_tile(a, int(blockIdx.x / a.q_heads), lane,
+    if (!find_tile(a, int(blockIdx.x / a.q_heads), lane, a.causal,
                    [](const Span &s) { return (s.lq + ROWS - 1) / ROWS; }, sp, tile))
         return;
-    tile = (sp.lq + ROWS - 1) / ROWS - 1 - tile;             // long rows first
 
     const int r0 = tile * ROWS + rg * 32;                    // wave's first row
     const int row = r0 + (lane & 31);

@@ -73,10 +73,9 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     const int head = kv_head * group + (blockIdx.x / a.k_heads) % group;
     Span sp;
     int tile;
-    if (!find_tile(a, int(blockIdx.x / a.q_heads), lane,
+    if (!find_tile(a, int(blockIdx.x / a.q_heads), lane, a.causal,
                    [](const Span &s) { return (s.lq + ROWS - 1) / ROWS; }, sp, tile))
         return;
-    tile = (sp.lq + ROWS - 1) / ROWS - 1 - tile;
     const int r0 = tile * ROWS + rg * 32;
     const int row = r0 + (lane & 31);
     const int shift = sp.lk - sp.lq;
@@ -303,9 +302,10 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     const int part = (blockIdx.x / a.k_heads) % a.splits;
     Span sp;
     int tile;
-    if (!find_tile(a, int(blockIdx.x / a.k_heads / a.splits), lane,
+    if (!find_tile(a, int(blockIdx.x / a.k_heads / a.splits), lane, a.causal,
                    [](const Span &s) { return (s.k_all + kRows - 1) / kRows; }, sp, tile))
         return;
+    tile = (sp.k_all + kRows - 1) / kRows - 1 - tile;       // the first keys are seen by most rows
     const int k0 = tile * kRows + wave * 32;               // wave's first key
     const int key = k0 + (lane & 31);
     const int shift = sp.lk - sp.lq;
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(256) void attend_dkv_sum_kernel(AttendArgs a)
     const int kv_head = blockIdx.x % a.k_heads;
     Span sp;
     int tile;
-    if (!find_tile(a, int(blockIdx.x / a.k_heads), threadIdx.x & 63,
+    if (!find_tile(a, int(blockIdx.x / a.k_heads), threadIdx.x & 63, false,
                    [](const Span &s) { return (s.k_all + kSumRows - 1) / kSumRows; }, sp, tile))
         return;
     const int vecs = a.dim / 4;

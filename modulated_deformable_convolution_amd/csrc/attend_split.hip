@@ -51,16 +51,6 @@ __device__ __forceinline__ Units units_of(const AttendArgs &a, const Span &s)
     return u;
 }
 
-__device__ __forceinline__ int scan(int v, int lane)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const int o = __shfl_up(v, m, 64);
-        v += lane >= m ? o : 0;
-    }
-    return v;
-}
-
 // The units of 64 sequences, one per lane: its own and those up to it.
 struct Chunk {
     Span span;
@@ -74,7 +64,7 @@ struct Chunk {
             span = span_of(a, b0 + lane);
             mine = units_of(a, span).all;
         }
-        upto = a.batch > 1 ? scan(mine, lane) : __builtin_amdgcn_readfirstlane(mine);
+        upto = wave_scan(mine);
     }
 };
 
@@ -86,7 +76,7 @@ __device__ __forceinline__ int total_units(const AttendArgs &a, const Chunk &fir
         int more = 0;
         for (int b = 64 + lane; b < a.batch; b += 64)
             more += units_of(a, span_of(a, b)).all;
-        sum += __builtin_amdgcn_readlane(scan(more, lane), 63);
+        sum += wave_sum(more);
     }
     return sum;
 }
