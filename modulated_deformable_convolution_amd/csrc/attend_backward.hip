@@ -24,31 +24,34 @@ constexpr int kFar = 1 << 30;                 // more than any number of rows
 
 template <typename T> constexpr int tile_rows() { return sizeof(T) == 2 ? 64 : 32; }
 
-// {lse in powers of two, delta} of every (token, head), 16 lanes each
-template <typename T>
+// {lse in powers of two, delta} of every (token, head): the diagonal of go.out for
+// 32 tokens of a head a wave.  On the matrix cores not for their rate (the reads
+// bound it), but to add in the order in which the other kernels add go.v: a row that
+// sees one key has out = v, and its ds is then exactly zero, as it should be.
+template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
 {
-    constexpr int E = 16 / sizeof(T);
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 4;
-    if (i >= int64_t(a.q_tokens) * a.q_heads)
+    const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+    const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int64_t block = w / a.q_heads;
+    const int head = int(w % a.q_heads);
+    if (block * 32 >= a.q_tokens)
         return;
-    const int64_t token = i / a.q_heads;
-    const int head = int(i % a.q_heads);
-    const T *o = reinterpret_cast<const T *>(row_ptr<T>(a.out, token, head));
-    const T *g = reinterpret_cast<const T *>(row_ptr<T>(a.go, token, head));
-    float sum = 0.0f;
-    for (int d = (threadIdx.x & 15) * E; d < a.dim; d += 16 * E) {
-        const Vec16<T> x = load16(o + d), y = load16(g + d);
+    const int64_t token = block * 32 + col;
+    const bool live = token < a.q_tokens;
+    Frag<T, DP> g, o;
+    load_frag<T, DP>(g, live ? reinterpret_cast<const T *>(row_ptr<T>(a.go, token, head)) : nullptr,
+                     a.dim, half);
+    load_frag<T, DP>(o, live ? reinterpret_cast<const T *>(row_ptr<T>(a.out, token, head)) : nullptr,
+                     a.dim, half);
+    const float16v s = mm_rows<T, DP>(g, o);
+    float delta = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            sum = fmaf(to_f32(x.e[e]), to_f32(y.e[e]), sum);
-    }
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1)
-        sum += __shfl_xor(sum, m, 64);
-    if ((threadIdx.x & 15) == 0) {
+    for (int r = 0; r < 16; ++r)
+        delta = acc_row(r, half) == col ? s[r] : delta;
+    if (live && half == (col >> 2 & 1)) {
         const int64_t at = head * int64_t(a.q_tokens) + token;
-        a.stats[at] = make_float2(a.lse[at] * kLog2e, sum);
+        a.stats[at] = make_float2(a.lse[at] * kLog2e, delta);
     }
 }
 
@@ -469,15 +472,15 @@ int64_t tiles_of(int64_t tokens, int64_t batch, int rows)
 template <typename T, int DP, int RW, int KW>
 hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 {
-    const int64_t rows = int64_t(a.q_tokens) * a.q_heads;
+    const int64_t d_blocks = ((int64_t(a.q_tokens) + 31) / 32 * a.q_heads + 3) / 4;
     const int64_t q_blocks = tiles_of(a.q_tokens, a.batch, 32 * RW) * a.q_heads;
     const int64_t k_tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t k_blocks = k_tiles * a.splits;
     const int64_t sum_blocks = tiles_of(a.k_tokens, a.batch, kSumRows) * a.k_heads;
-    if (sum_blocks > INT32_MAX || (rows + 15) / 16 > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
+    if (sum_blocks > INT32_MAX || d_blocks > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
         return hipErrorInvalidValue;
-    if (rows > 0)
-        attend_delta_kernel<T><<<uint32_t((rows + 15) / 16), 256, 0, s>>>(a);
+    if (d_blocks > 0)
+        attend_delta_kernel<T, DP><<<uint32_t(d_blocks), 256, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k_blocks > 0) {
         attend_dkv_kernel<T, DP><<<uint32_t(k_blocks), 64 * kWaves, 0, s>>>(a);

@@ -416,8 +416,7 @@ template <typename T, int DP> struct Softmax {
         return max_halves(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
     }
 
-    // Raises the maximum if `top` needs it; returns what is taken off the
-    // scores, in powers of two.
+    // Raises the maximum if `top` needs it; returns what exps takes off the scores.
     __device__ __forceinline__ float raise(float top, float c, float margin)
     {
         if (__ballot(top > m + margin)) {
@@ -429,18 +428,21 @@ template <typename T, int DP> struct Softmax {
             l *= f;
             m = up;
         }
-        return m == -INFINITY ? 0.0f : m * c;
+        return m == -INFINITY ? 0.0f : sizeof(T) == 4 ? m : m * c;
     }
 
-    // Turns scores into e^(scale (s - m)) and adds them up.
-    template <int NS> __device__ __forceinline__ void exps(float16v (&s)[NS], float c, float mc)
+    // Turns scores into e^(scale (s - m)) and adds them up.  16-bit types: one fma,
+    // m c taken off, which leaves 2^-24 |m c| at s = m; fp32: the difference
+    // first, so that a row of one key has p = 1 exactly.
+    template <int NS> __device__ __forceinline__ void exps(float16v (&s)[NS], float c, float off)
     {
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[n][r] = __builtin_amdgcn_exp2f(fmaf(s[n][r], c, -mc));
+                s[n][r] = __builtin_amdgcn_exp2f(sizeof(T) == 4 ? (s[n][r] - off) * c
+                                                                : fmaf(s[n][r], c, -off));
                 sum[r & 3] += s[n][r];
             }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);

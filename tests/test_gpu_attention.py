@@ -289,6 +289,22 @@ def test_masked_rows_with_extreme_scores():
         within(lse, ref["lse"], "lse")
 
 
+@pytest.mark.parametrize("dim", [32, 80, 128])
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_a_row_that_sees_one_key_has_no_score_gradient(dt, dim):
+    """softmax of one score is 1 whatever the score: dq and dk are exactly zero."""
+    dtype = DTYPES[dt]
+    n = 70
+    op = A.mdcn_attention_create(4, 2, dim, True)
+    q, k, v, go = (rand(n, h, dim, seed=s, dtype=dtype).cuda()
+                   for s, h in ((1, 4), (2, 2), (3, 2), (4, 4)))
+    c = ints(list(range(n + 1)))
+    out, lse = A.attend(op, q, k, v, c, c)
+    g = A.attend_backward(op, q, k, v, out, lse, go, c, c)
+    assert torch.equal(out, v.repeat_interleave(2, 1))
+    assert (g["q"] == 0).all() and (g["k"] == 0).all()
+
+
 def test_gradients_repeat_to_the_bit_and_match_differences():
     case = ([50, 90], None, 4, 2, 32, True)
     op, q, k, v, dq, dk, dv, cq, ck = attend_case(case, torch.float32)
