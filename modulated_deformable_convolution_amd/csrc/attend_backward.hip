@@ -6,11 +6,18 @@
 //   dk_j = scale sum_i ds_ij q_i       (i over the rows of all heads that share j's head)
 // p is recomputed from lse, so nothing of size queries x keys is stored.
 //
-// Kernels: delta; dk and dv, a workgroup per 128 keys walking over the
-// queries of its group's heads, or several that share them, whose sums in the
-// workspace a fourth kernel adds up; dq, a workgroup per 128 queries walking over the keys.  Scores and go.v are computed in both (7 products
-// instead of 5), in exchange for which no gradient is accumulated through
-// memory: no atomics, the same bits every run, one rounding of each gradient.
+// Kernels: delta; dk and dv, a workgroup per 128 keys walking over the queries of
+// its group's heads, or several that share them, whose sums in the workspace a
+// fourth kernel adds up; dq, a workgroup per 128 queries walking over the keys.
+// Scores and go.v are computed in both (7 products instead of 5), in exchange for
+// which no gradient is accumulated through memory: no atomics, the same bits
+// every run, one rounding of each gradient.
+//
+// One MI355X, bf16, 16 query and 4 key heads of 128, 4096 x 4096 full: dk and dv
+// 377 us (730 TFLOP/s of its four products), dq 203 us (1020 of its three).
+// Sequences of 2048 to 1 tokens, causal: 10 + 90 + 13 + 66 us, where the
+// longest rows of tiles and the start of a workgroup (about 8 us) bound it: 592
+// workgroups cannot be spread evenly.
 #include "attention_common.h"
 
 namespace mdcn {
@@ -25,38 +32,74 @@ constexpr int kFar = 1 << 30;                 // more than any number of rows
 template <typename T> constexpr int tile_rows() { return sizeof(T) == 2 ? 64 : 32; }
 
 // {lse in powers of two, delta} of every (token, head): the diagonal of go.out for
-// 32 tokens of a head a wave.  On the matrix cores not for their rate (the reads
+// 32 rows of a head a wave.  On the matrix cores not for their rate (the reads
 // bound it), but to add in the order in which the other kernels add go.v: a row that
 // sees one key has out = v, and its ds is then exactly zero, as it should be.
+//
+// out has been rounded, and its error is in every score gradient of its row: little
+// among many keys, but of the size of all other roundings together in rows that see
+// few (causal sequences of 8 rows, bf16: dq off by 0.0029 instead of 0.0024, of which
+// the rounding of dq itself is 0.0016).  In 16 bits rows that see 2 to 32 keys
+// take sum(p go.v) over these instead, one more product of 32 keys a wave.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
 {
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
-    const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int64_t block = w / a.q_heads;
-    const int head = int(w % a.q_heads);
-    if (block * 32 >= a.q_tokens)
+    const int w = int(blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
+    const int head = w % a.q_heads;
+    Span sp;
+    int tile;
+    if (!find_tile(a, w / a.q_heads, lane, false, [](const Span &s) { return (s.lq + 31) / 32; },
+                   sp, tile))
         return;
-    const int64_t token = block * 32 + col;
-    const bool live = token < a.q_tokens;
+    const int row = tile * 32 + col;
+    const int64_t token = sp.q0 + row;
+    const bool live = row < sp.lq;
+    const int last = a.causal ? row + sp.lk - sp.lq : sp.lk - 1;
+    const int64_t at = head * int64_t(a.q_tokens) + token;
+    const float lse = live ? a.lse[at] * kLog2e : 0.0f;
     Frag<T, DP> g, o;
     load_frag<T, DP>(g, live ? reinterpret_cast<const T *>(row_ptr<T>(a.go, token, head)) : nullptr,
                      a.dim, half);
     load_frag<T, DP>(o, live ? reinterpret_cast<const T *>(row_ptr<T>(a.out, token, head)) : nullptr,
                      a.dim, half);
-    const float16v s = mm_rows<T, DP>(g, o);
+    const float16v d = mm_rows<T, DP>(g, o);
     float delta = 0.0f;
 #pragma unroll
     for (int r = 0; r < 16; ++r)
-        delta = acc_row(r, half) == col ? s[r] : delta;
-    if (live && half == (col >> 2 & 1)) {
-        const int64_t at = head * int64_t(a.q_tokens) + token;
-        a.stats[at] = make_float2(a.lse[at] * kLog2e, delta);
+        delta = acc_row(r, half) == col ? d[r] : delta;
+    const bool few = sizeof(T) == 2 && live && last > 0 && last < 32;
+    if (sizeof(T) == 2 && __any(few)) {
+        const int kv_head = head / (a.q_heads / a.k_heads);
+        const bool held = col < sp.lk;
+        Frag<T, DP> q, kv;
+        load_frag<T, DP>(
+            q, live ? reinterpret_cast<const T *>(row_ptr<T>(a.q, token, head)) : nullptr, a.dim,
+            half);
+        load_frag<T, DP>(
+            kv, held ? reinterpret_cast<const T *>(row_ptr<T>(a.k, sp.k0 + col, kv_head)) : nullptr,
+            a.dim, half);
+        const float16v s = mm_rows<T, DP>(kv, q);
+        load_frag<T, DP>(
+            kv, held ? reinterpret_cast<const T *>(row_ptr<T>(a.v, sp.k0 + col, kv_head)) : nullptr,
+            a.dim, half);
+        const float16v dp = mm_rows<T, DP>(kv, g);
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale * kLog2e, -lse));
+            sum += acc_row(r, half) <= last ? p * dp[r] : 0.0f;
+        }
+        sum += __shfl_xor(sum, 32);
+        delta = few ? sum : delta;
     }
+    if (live && half == (col >> 2 & 1))
+        a.stats[at] = make_float2(lse, delta);
 }
 
 template <typename T, int DP, int RW, int KW>
-__global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void attend_dq_kernel(AttendArgs a)
+__global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void attend_dq_kernel(
+    AttendArgs a)
 {
     using R = Row<T, DP>;
     constexpr int ROWS = 32 * RW;
@@ -472,7 +515,7 @@ int64_t tiles_of(int64_t tokens, int64_t batch, int rows)
 template <typename T, int DP, int RW, int KW>
 hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 {
-    const int64_t d_blocks = ((int64_t(a.q_tokens) + 31) / 32 * a.q_heads + 3) / 4;
+    const int64_t d_blocks = (tiles_of(a.q_tokens, a.batch, 32) * a.q_heads + 3) / 4;
     const int64_t q_blocks = tiles_of(a.q_tokens, a.batch, 32 * RW) * a.q_heads;
     const int64_t k_tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t k_blocks = k_tiles * a.splits;
@@ -518,13 +561,18 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
 
 int attend_backward_splits(const AttendArgs &a)
 {
-    // Enough workgroups for two on each of the 256 compute units, with at
-    // least twice 32 queries to each (a part costs its sums' way through memory).
+    // Enough workgroups for nearly two on each of the 256 compute units (dk and dv of
+    // the training step above: 296 workgroups 151 us, 444 109, 592 91; the last few
+    // are not worth a third on some: fp32, 1000 queries, 504 workgroups 39 us,
+    // 576 46).  At least 3/2 times 32 queries to each, as a part costs its sums'
+    // way through memory (fp32, 400 and fewer queries, 64 tiles: twice 44.6 + 5.5 us,
+    // 3/2 times 38.3 + 6.6, once 44.8 + 8.6).
     const int64_t tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t queries = int64_t(a.q_heads / a.k_heads) * a.q_tokens /
                             (32 * int64_t(a.batch > 0 ? a.batch : 1));
-    int64_t n = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
-    n = n < queries / 2 ? n : queries / 2;
+    int64_t n = tiles > 0 ? (480 + tiles - 1) / tiles : 1;
+    const int64_t most = (2 * queries + 2) / 3;
+    n = n < most ? n : most;
     return int(n < 1 ? 1 : n > 8 ? 8 : n);
 }
 

@@ -305,6 +305,28 @@ def test_a_row_that_sees_one_key_has_no_score_gradient(dt, dim):
     assert (g["q"] == 0).all() and (g["k"] == 0).all()
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens", [[2] * 40, [8] * 20, [33, 70, 5, 1, 31], [300]], ids=str)
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_score_gradients_carry_two_roundings(dt, lens, causal):
+    """dq and dk: the score gradients are rounded for the product and the results once more, which
+    are errors of one size and independent, sqrt(2) = 1.42 times the last one's alone.  The
+    rounding of out, which is an input here, adds less than 0.08 of them in rows of
+    more than 32 keys, and nothing in rows of fewer."""
+    dtype = DTYPES[dt]
+    n, c = sum(lens), cu(lens)
+    q, k, v, go = (rand(n, 8, 64, seed=60 + i, dtype=dtype) for i in range(4))
+    op = A.mdcn_attention_create(8, 8, 64, causal)
+    dev = [t.cuda() for t in (q, k, v)]
+    out, lse = A.attend(op, *dev, ints(c), ints(c))
+    got = A.attend_backward(op, *dev, out, lse, go.cuda(), ints(c), ints(c))
+    want = R.attend(q, k, v, c, c, None, causal, 64 ** -0.5, dtype, go)
+    for name in ("q", "k"):
+        exact = want[name][0]
+        last = (exact.to(dtype).double() - exact).norm()
+        assert float((got[name].double().cpu() - exact).norm() / last) < 1.5, name
+
+
 def test_gradients_repeat_to_the_bit_and_match_differences():
     case = ([50, 90], None, 4, 2, 32, True)
     op, q, k, v, dq, dk, dv, cq, ck = attend_case(case, torch.float32)
