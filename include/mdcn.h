@@ -381,10 +381,14 @@ mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_
                         void *workspace, size_t workspace_bytes, void *stream);
 
 /* Gradients of mdcn_attend's out with respect to q, k and v, from grad_out and
- * the forward's out and lse.  dims[0..10] as there, dims[11..18] token and
- * head stride of grad_out, grad_q, grad_k, grad_v.  The gradients of shared
- * key heads are the sums over their query heads; keys that are not used get
- * zeros.  No atomics: repeated calls give the same bits. */
+ * the forward's out and lse for the same q, k and v.  dims[0..10] as there,
+ * dims[11..18] token and head stride of grad_out, grad_q, grad_k, grad_v.  The
+ * gradients of shared key heads are the sums over their query heads; keys that are not used get
+ * zeros.  A row that sees no key has a zero gradient and adds to none.  Hidden
+ * keys and values that are infinite or NaN reach no gradient; such values in a
+ * row of q or grad_out do reach the keys of the whole sequence, hidden ones
+ * too.  Sums in fp32, probabilities and score gradients rounded to the inputs'
+ * type for the products.  No atomics: repeated calls give the same bits. */
 mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_dtype dtype,
                                                  const int64_t dims[19], size_t *bytes);
 mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,

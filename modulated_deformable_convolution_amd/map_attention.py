@@ -84,12 +84,15 @@ class Decoder(_Layer):
         self.keys, self.values = (torch.empty((batch * room, k_heads, dim), dtype=dtype,
                                               device="cuda") for _ in range(2))
         self.used = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.longest = 0
         self.first = torch.arange(batch, device="cuda") * room
         self.new_ends = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
         self.cache_ends = self.new_ends * room
 
     def prompt(self, tokens, lengths):
         """Packed prompts (lengths: a list): fills the cache, returns the outputs."""
+        if len(lengths) != self.batch or max(lengths) > self.room:
+            raise ValueError("%d prompts of at most %d tokens" % (self.batch, self.room))
         steps = torch.cat([torch.arange(n) for n in lengths]).cuda()
         rows = torch.repeat_interleave(self.first, torch.tensor(lengths).cuda()) + steps
         ends = torch.tensor([0] + lengths).cumsum(0).to("cuda", torch.int32)
@@ -97,10 +100,14 @@ class Decoder(_Layer):
         q, k = attention.rotate(self.rotary, q, k, steps.to(torch.int32)[None])
         self.keys[rows], self.values[rows] = k, v
         self.used = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        self.longest = max(lengths)
         return attention.attend(self.attention, q, k, v, ends, ends)[0].flatten(1)
 
     def step(self, tokens):
         """The next token of every sequence, [batch, channels]."""
+        if self.longest == self.room:
+            raise ValueError("the cache is full")
+        self.longest += 1
         q, k, v = self.project(tokens)
         q, k = attention.rotate(self.rotary, q, k, self.used[None])
         rows = self.first + self.used
