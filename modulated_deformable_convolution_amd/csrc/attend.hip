@@ -28,15 +28,13 @@ namespace mdcn {
 
 namespace {
 
-template <typename T> constexpr int tile_keys() { return sizeof(T) == 2 ? 64 : 32; }
-
 template <typename T, int DP, int RW, int KW>
 __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void attend_kernel(
     AttendArgs a)
 {
     using R = Row<T, DP>;
     constexpr int ROWS = 32 * RW;
-    constexpr int KB = tile_keys<T>();           // keys of a wave's part of a tile
+    constexpr int KB = tile_keys<T, DP, KW>();   // keys of a wave's part of a tile
     constexpr int NS = KB / 32;
     constexpr int KT = KB * KW;                  // keys of a tile
     constexpr int PART = KB * R::PITCH;
@@ -226,7 +224,11 @@ hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 
 template <typename T, int DP> hipError_t launch(const AttendArgs &a, hipStream_t s)
 {
-    return attend_small(a) ? launch_shape<T, DP, 2, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
+    const int waves = attend_key_waves(sizeof(T) == 4 ? MDCN_F32 : MDCN_F16, a);
+    if constexpr (sizeof(T) == 2)
+        if (waves == 4)
+            return launch_shape<T, DP, 2, 4>(a, s);
+    return waves == 2 ? launch_shape<T, DP, 2, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
 }
 
 template <typename T>
@@ -243,14 +245,24 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
 
 }  // namespace
 
-bool attend_small(const AttendArgs &a)
+int attend_key_waves(mdcn_dtype dtype, const AttendArgs &a)
 {
     // Up to one workgroup of 128 queries a compute unit, workgroups of 64
     // queries, two waves to the keys of each 32, spread further and end sooner
     // (208 workgroups of eight f16 heads of 64: 20.8 us against 26.8; fp32, 48
     // workgroups: 26 against 40).  Beyond, they stage twice the keys a
     // query (528 workgroups of bf16 heads of 128: 75 us against 55).
-    return (int64_t(a.q_tokens) / 128 + 1) * a.q_heads <= 256;
+    if ((int64_t(a.q_tokens) / 128 + 1) * a.q_heads > 256)
+        return 1;
+    // Of those, four waves to the keys fill a compute unit that has no second
+    // workgroup to run (bf16, one sequence, eight heads of 128, 1500 tokens: 23.9 us
+    // against 29.7, dq 28.9 against 33.2; 16 heads, 700 tokens, causal: 17.0 against 18.8)
+    // if the keys are many (200 and fewer: 8.4 against 7.6) and the workgroups no
+    // more than the compute units (448: 26.4 against 19.6).  In fp32 a single wave
+    // keeps the matrix cores busy (32.2 against 33.0, dq 41.5 against 40.6).
+    const int64_t batch = a.batch < a.q_tokens ? a.batch : a.q_tokens;
+    const int64_t blocks = (int64_t(a.q_tokens) / 64 + batch) * a.q_heads;
+    return dtype != MDCN_F32 && blocks <= 256 && a.k_tokens >= 512 * int64_t(a.batch) ? 4 : 2;
 }
 
 hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s)

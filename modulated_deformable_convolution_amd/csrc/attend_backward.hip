@@ -29,8 +29,6 @@ constexpr int kRows = 32 * kWaves;
 
 constexpr int kFar = 1 << 30;                 // more than any number of rows
 
-template <typename T> constexpr int tile_rows() { return sizeof(T) == 2 ? 64 : 32; }
-
 // {lse in powers of two, delta} of every (token, head): the diagonal of go.out for
 // 32 rows of a head a wave.  On the matrix cores not for their rate (the reads
 // bound it), but to add in the order in which the other kernels add go.v: a row that
@@ -103,7 +101,7 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
 {
     using R = Row<T, DP>;
     constexpr int ROWS = 32 * RW;
-    constexpr int KB = tile_rows<T>();           // keys of a wave's part of a tile
+    constexpr int KB = tile_keys<T, DP, KW>();   // keys of a wave's part of a tile
     constexpr int KT = KB * KW;                  // keys of a tile
     constexpr int PART = KB * R::PITCH;
     constexpr int TILE = KT * R::PITCH;
@@ -542,7 +540,11 @@ hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
 
 template <typename T, int DP> hipError_t launch(const AttendArgs &a, hipStream_t s)
 {
-    return attend_small(a) ? launch_shape<T, DP, 2, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
+    const int waves = attend_key_waves(sizeof(T) == 4 ? MDCN_F32 : MDCN_F16, a);
+    if constexpr (sizeof(T) == 2)
+        if (waves == 4)
+            return launch_shape<T, DP, 2, 4>(a, s);
+    return waves == 2 ? launch_shape<T, DP, 2, 2>(a, s) : launch_shape<T, DP, 4, 1>(a, s);
 }
 
 template <typename T>

@@ -68,8 +68,9 @@ struct AttendArgs {
     float *partial;        // sums that several workgroups leave for one result
 };
 
-// Whether attend, and dq in the backward, take 64 queries a workgroup and not 128.
-bool attend_small(const AttendArgs &a);
+// Waves that share the keys of 32 queries in attend, and of dq in the backward: 1 in
+// workgroups of 128 queries, 2 or 4 in workgroups of 64.
+int attend_key_waves(mdcn_dtype dtype, const AttendArgs &a);
 hipError_t launch_attend(mdcn_dtype dtype, const AttendArgs &a, hipStream_t s);
 // Whether the kernel that splits keys over the chip is the faster one for a
 // batch of these sizes.

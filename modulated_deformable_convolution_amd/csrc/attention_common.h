@@ -368,12 +368,19 @@ __device__ __forceinline__ void store_cols(T *dst, const Acc<T, DP> &acc,
         }
 }
 
+// Keys of a wave's part of a tile of K or V: four parts of 64 rows of 256 bytes, with
+// two stages of both, would not fit the LDS.
+template <typename T, int DP, int KW> constexpr int tile_keys()
+{
+    return sizeof(T) == 2 && (KW < 4 || Row<T, DP>::PITCH <= 128) ? 64 : 32;
+}
+
 // Waves a SIMD that a tile kernel's registers are to leave room for: two workgroups
 // of four waves, unless the LDS of one (two stages of K and V) leaves no room
 // or 256 registers do not hold a wave's sums and operands.
 template <typename T, int DP, int KW> constexpr int waves_per_simd()
 {
-    constexpr int lds = 4 * (sizeof(T) == 2 ? 64 : 32) * KW * Row<T, DP>::PITCH;
+    constexpr int lds = 4 * tile_keys<T, DP, KW>() * KW * Row<T, DP>::PITCH;
     return lds > 80 * 1024 || (sizeof(T) == 4 && DP > 96) ? 1 : 2;
 }
 

@@ -237,6 +237,39 @@ def test_unused_cache_rows_are_never_used(dt, rows, size, causal):
     within(lse, ref["lse"], "lse")
 
 
+LONG = [
+    # few heads of long sequences: workgroups no more than the compute units
+    ([700], None, 2, 1, 64, True),
+    ([515], None, 2, 2, 128, False),
+    ([130, 700, 1], [1100, 700, 300], 3, 1, 32, True),
+    ([90, 400], [1300, 33], 2, 1, 80, True),               # rows that see nothing
+    ([700], [1025], 2, 1, 96, False),
+]
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_sequences_of_few_heads(case, dt):
+    check_attend(case, DTYPES[dt])
+
+
+@pytest.mark.parametrize("at", [1023, 1000, 700, 100])
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_hidden_rows_of_long_sequences(dt, at):
+    """As the two tests below, where waves share a row's keys."""
+    dtype = DTYPES[dt]
+    op, q, k, v, dq, dk, dv, cq, ck = attend_case(([1024], None, 2, 1, 128, True), dtype)
+    go = rand(*q.shape, seed=9, dtype=dtype)
+    ref = R.attend(q, k, v, cq, ck, None, True, op.scale, dtype, go)
+    for x in (dv, dk):
+        x[at] = math.nan
+        out, lse = A.attend(op, dq, dk, dv, ints(cq), ints(ck))
+        got = A.attend_backward(op, dq, dk, dv, out, lse, go.cuda(), ints(cq), ints(ck))["q"]
+        within(out[:at], (ref["out"][0][:at], ref["out"][1][:at]), "out")
+        within(got[:at], (ref["q"][0][:at], ref["q"][1][:at]), "dq")
+        assert not out[at:].isfinite().any() and not got[at:].isfinite().all(-1).any()
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("rows,keys", [(4, 170), (150, 170), (4, 3000)])
 @pytest.mark.parametrize("dt", list(DTYPES))
