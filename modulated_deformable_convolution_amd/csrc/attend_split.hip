@@ -16,6 +16,7 @@
 // One MI355X, bf16, 32 query and 8 key heads of 128: 48 caches of 1 to 16384
 // tokens 268 us (1.6 GB, 6.0 TB/s; a copy's reads and writes reach 4.8) and 8 us
 // to join; one cache of 4097 tokens 9.8 us and 5 us, round trips to memory.
+#include <algorithm>
 #include <cmath>
 
 #include "attention_common.h"
@@ -448,26 +449,35 @@ int attend_split_workers(mdcn_dtype dtype, int dim)
     return kComputeUnits * (bytes > 128 ? 1 : bytes > 64 ? 2 : 4);
 }
 
-// In rounds of the tile kernel on 64 queries (1.75 us for bf16 heads of 128, 0.83
-// us for f16 of 64, 3.9 us for fp32 of 80): it takes one for each 128 keys (fp32:
-// 64) and 256 workgroups; the split kernel about 5/4 of one for each 32 keys x 32 rows of a
-// wave, four more to start and join, and one for 512 rows to be joined.
-// Measured on both sides (32 query and 8 key heads of 128 in bf16, one sequence; split
-// against tile, us): 1 query, 128 keys 17 / 12; 1 and 64 queries, 1024 keys 17 / 22 and
-// 30 / 23; 1, 128 and 512 queries, 8192 keys 18 / 123, 72 / 122 and 233 / 130.
+// The two kernels' times in us beyond a launch.  The tile kernel on 64 queries takes
+// 0.83 for each 128 keys (16 bits, up to 64 channels; 0.62 if four waves share
+// them), 1.75 (more channels; 1.35) or, fp32, 3.9 for 64, and runs 256 workgroups at a
+// time; the split kernel 1.0, 1.5 or 3.9 for each 32 keys x 32 rows of a wave, 7 for its
+// second launch, 3.5 to pass on full tiles of more than 64 channels, and 3.4 ns
+// for each row that is joined.  Measured on both sides (split against tile, us, 10
+// of the host in both): 32 query and 8 key heads of 128 in bf16, one sequence of 1024
+// keys, 1 and 8 queries 18 / 18 and 23 / 18; 8192 keys, 1, 128 and 256 queries 18 / 77,
+// 73 / 82 and 125 / 86; eight heads of 64 in f16, 1024 keys 17 / 12, eight sequences
+// of 8192 keys, 64 and 128 queries 44 / 50 and 72 / 53; fp32 of 80, 1024 keys, 512
+// queries 57 / 68, in eight sequences, 128 queries 105 / 72.
 // Only averages are known here: the lengths are on the GPU.
 bool attend_prefers_split(mdcn_dtype dtype, const AttendArgs &a)
 {
     if (a.batch == 0 || a.q_tokens == 0)
         return false;
+    const bool f32 = dtype == MDCN_F32, wide = a.dim > 64;
+    const bool four = attend_key_waves(dtype, a) == 4;
     const double queries = double(a.q_tokens) / a.batch, keys = double(a.k_tokens) / a.batch;
-    const double group = a.q_heads / a.k_heads;
+    const double tile_rows = queries * (a.q_heads / a.k_heads) / kTileRows;
+    const double round = f32 ? 3.9 : wide ? (four ? 1.35 : 1.75) : (four ? 0.62 : 0.83);
     const double blocks = double(a.batch) * a.q_heads * std::ceil(queries / 64);
-    const double rounds = (keys / (dtype == MDCN_F32 ? 64 : 128) + 1) * std::ceil(blocks / 256);
-    const double units = double(a.batch) * a.k_heads * std::ceil(queries * group / kTileRows) *
-                         (keys / kUnit + 1);
-    const double waves = attend_split_workers(dtype, a.dim) * (dtype == MDCN_F32 && a.dim > 64 ? 2 : 4);
-    return 1.25 * std::ceil(units / waves) + 4 + double(a.q_tokens) * a.q_heads / 512 < rounds;
+    const double tile = round * (keys / (f32 ? 64 : 128) + 0.5) * std::ceil(blocks / 256);
+    const double units = double(a.batch) * a.k_heads * std::ceil(tile_rows) * (keys / kUnit + 1);
+    const double waves = attend_split_workers(dtype, a.dim) * (f32 && wide ? 2 : 4);
+    const double split = (f32 ? 3.9 : wide ? 1.5 : 1.0) * std::max(1.0, units / waves) + 7 +
+                         (wide ? 3.5 * std::min(1.0, tile_rows) : 0.0) +
+                         0.0034 * a.q_tokens * a.q_heads;
+    return split < tile;
 }
 
 size_t attend_split_bytes(mdcn_dtype dtype, int dim)
