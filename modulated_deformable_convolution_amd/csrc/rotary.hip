@@ -101,11 +101,15 @@ __device__ __forceinline__ void unit_offsets(int u, int pairs, int &lo, int &hi)
     }
 }
 
-// x[0..V) and x[V..2V) are a unit's two vectors.
+// x[0..V) and x[V..2V) are a unit's two vectors.  V divides the pairs, so a unit is
+// turned or left as it is as a whole: a turn by the angle 0 would multiply each
+// channel by the other's 0, which is not nothing where that one is not finite.
 template <int V, bool ADJ>
 __device__ __forceinline__ void turn_unit(float (&x)[2 * V], const float (&c)[V],
-                                          const float (&s)[V])
+                                          const float (&s)[V], bool turned)
 {
+    if (!turned)
+        return;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (ADJ) {
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int grou
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (live && ok[u]) {
-                turn_unit<V, ADJ>(x[u], c[u], s[u]);
+                turn_unit<V, ADJ>(x[u], c[u], s[u], at[u] < a.pairs);
                 Unit<T, V> y;
                 y.set(x[u]);
                 y.store(dst, lo[u], hi[u]);
@@ -368,7 +372,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_backward_kernel(RotaryAr
             for (int u = 0; u < U; ++u) {
                 const Unit<T, V> wu = is_q ? gain_q[u] : gain_k[u];
                 wu.get(w[u]);
-                turn_unit<V, ADJ>(g[u], c[u], s[u]);     // s is -sin here
+                turn_unit<V, ADJ>(g[u], c[u], s[u], at[u] < a.pairs);   // s is -sin here
 #pragma unroll
                 for (int j = 0; j < 2 * V; ++j) {
                     sum += x[u][j] * x[u][j];

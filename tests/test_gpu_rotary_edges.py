@@ -1,0 +1,81 @@
+"""Rotary positions and norms on the GPU where they can go wrong."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as R
+from helpers import ensure_built
+from modulated_deformable_convolution_amd import attention as A
+from test_gpu_attention import DTYPES, rand, within
+
+pytestmark = pytest.mark.gpu
+ensure_built()
+
+
+# channels, pairs of each axis, first channel of a row in its tensor: every vector width
+PARTLY = [(96, [24], 0), (96, [12, 12], 4), (64, [8, 8], 1), (40, [6], 2), (16, [3], 0), (128, [16], 8),
+          (250, [63], 0)]
+
+
+def partly_case(dim, axes, at, adjacent, dtype, seed):
+    op = A.mdcn_rotary_create(dim, axes, adjacent=adjacent)
+    t, rest = 5, 2 * sum(axes)
+    wide = rand(t, 3, dim + at, seed=seed, dtype=dtype)
+    x = wide[..., at:]
+    values = [math.inf, math.nan, -math.inf, -0.0, 0.0]
+    for i in range(t):
+        for h in range(3):
+            for n in range(1 + (i + h) % 3):
+                x[i, h, rest + (7 * i + 3 * h + 5 * n) % (dim - rest)] = values[(i + h + n) % 5]
+    pos = torch.arange(t * len(axes), dtype=torch.int32).view(len(axes), t) * 3
+    return op, x, wide.cuda()[..., at:], pos, R.angles(axes, 10000.0, False, False, pos), rest
+
+
+def bits(x):
+    return x.contiguous().view(torch.int32 if x.dtype == torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("case", PARTLY, ids=str)
+def test_channels_past_the_pairs_stay_as_they_are(case, dt, adjacent):
+    op, x, dx, pos, theta, rest = partly_case(*case, adjacent, DTYPES[dt], 1)
+    for call, angle in ((A.rotate, theta), (A.rotate_backward, -theta)):
+        a, b = call(op, dx[:, :2], dx[:, 2:], pos.cuda())
+        y = torch.cat((a, b), 1).cpu()
+        assert torch.equal(bits(y[..., rest:]), bits(x[..., rest:]))
+        v, e = R.rotate(x, angle, adjacent, DTYPES[dt])
+        within(y[..., :rest], (v[..., :rest], e[..., :rest]), "turned channels")
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("case", PARTLY, ids=str)
+def test_norms_of_channels_past_the_pairs_do_not_mix(case, dt, adjacent):
+    """An infinite channel takes 1 / rms to zero: it is NaN itself, all others are zero."""
+    op, x, dx, pos, theta, rest = partly_case(*case, adjacent, DTYPES[dt], 2)
+    dim = x.shape[-1]
+    w = rand(dim, seed=5, dtype=torch.float32, scale=0.2).add(1).to(DTYPES[dt])
+    a, b = A.norm_rotate(op, dx[:, :2], dx[:, 2:], pos.cuda(), w.cuda(), w.cuda())
+    v, e = R.norm_rotate(x, w, 1e-6, theta, adjacent, DTYPES[dt])
+    e = torch.where(e.isnan() & v.isfinite(), torch.zeros_like(e), e)
+    within(torch.cat((a, b), 1), (v, e), "norm")
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("case", PARTLY, ids=str)
+def test_gain_gradients_past_the_pairs_do_not_mix(case, dt, adjacent):
+    """A gradient that is not finite in a channel that is not turned shows in that gain only."""
+    dtype = DTYPES[dt]
+    op, gy, dgy, pos, theta, rest = partly_case(*case, adjacent, dtype, 3)
+    dim = gy.shape[-1]
+    x = rand(*gy.shape, seed=4, dtype=dtype)
+    w = torch.ones(dim, dtype=dtype)
+    dx = x.cuda()
+    g = A.norm_rotate_backward(op, dx[:, :2], dx[:, 2:], pos.cuda(), w.cuda(), w.cuda(), dgy[:, :2],
+                               dgy[:, 2:])
+    for name, part in (("q_gain", slice(0, 2)), ("k_gain", slice(2, 3))):
+        v, e = R.norm_rotate_backward(x[:, part], w, 1e-6, theta, adjacent, gy[:, part], dtype)[1]
+        within(g[name], (v, e.nan_to_num(0.0)), name)
