@@ -333,7 +333,9 @@ mdcn_status mdcn_norm_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const int6
 /* Gradients of mdcn_norm_rotate from those of its outputs: grad_q, grad_k and
  * the gains' (sums over all tokens and heads, in fp32, in a fixed order).
  * dims[0..7] as above, dims[8..15] token and head stride of grad_q_out,
- * grad_k_out, grad_q, grad_k.  No tokens: the gains' gradients are zero. */
+ * grad_k_out, grad_q, grad_k.  No tokens: the gains' gradients are zero.  No
+ * heads on one side: its gain may be NULL, and its gain's gradient is zero, or
+ * NULL and not written. */
 mdcn_status mdcn_norm_rotate_backward_workspace_bytes(const mdcn_rotary *op, int64_t tokens,
                                                       size_t *bytes);
 mdcn_status mdcn_norm_rotate_backward(const mdcn_rotary *op, mdcn_dtype dtype,

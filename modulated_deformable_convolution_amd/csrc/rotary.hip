@@ -436,8 +436,7 @@ constexpr int kSumCols = 16, kSumRows = 64;
 template <typename T>
 __global__ __launch_bounds__(kSumCols * kSumRows) void gain_sum_kernel(const float *partial,
                                                                        int blocks, int dim,
-                                                                       int k_heads, T *dq_gain,
-                                                                       T *dk_gain)
+                                                                       T *dq_gain, T *dk_gain)
 {
     __shared__ float part[kSumRows][kSumCols + 1];
     const int x = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;
@@ -463,7 +462,7 @@ __global__ __launch_bounds__(kSumCols * kSumRows) void gain_sum_kernel(const flo
         if (col < dim) {
             if (dq_gain)
                 dq_gain[col] = from_f32<T>(part[0][x]);
-        } else if (k_heads > 0) {
+        } else if (dk_gain) {
             dk_gain[col - dim] = from_f32<T>(part[0][x]);
         }
     }
@@ -581,7 +580,7 @@ template <typename T>
 static hipError_t gain_sum(const RotaryArgs &a, void *dq, void *dk, hipStream_t s)
 {
     gain_sum_kernel<T><<<(2 * a.dim + kSumCols - 1) / kSumCols, kSumCols * kSumRows, 0, s>>>(
-        a.partial, rotary_backward_blocks(a.tokens), a.dim, a.k_heads, static_cast<T *>(dq),
+        a.partial, rotary_backward_blocks(a.tokens), a.dim, static_cast<T *>(dq),
         static_cast<T *>(dk));
     return hipGetLastError();
 }

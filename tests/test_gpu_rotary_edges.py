@@ -13,6 +13,14 @@ pytestmark = pytest.mark.gpu
 ensure_built()
 
 
+def poison(nbytes=1 << 24):
+    """Leaves NaN in the memory that torch hands out next."""
+    blocks = [torch.full((n // 4,), math.nan, device="cuda") for n in (512, 4096, 1 << 16, nbytes)
+              for _ in range(4)]
+    torch.cuda.synchronize()
+    del blocks
+
+
 # channels, pairs of each axis, first channel of a row in its tensor: every vector width
 PARTLY = [(96, [24], 0), (96, [12, 12], 4), (64, [8, 8], 1), (40, [6], 2), (16, [3], 0), (128, [16], 8),
           (250, [63], 0)]
@@ -79,3 +87,19 @@ def test_gain_gradients_past_the_pairs_do_not_mix(case, dt, adjacent):
     for name, part in (("q_gain", slice(0, 2)), ("k_gain", slice(2, 3))):
         v, e = R.norm_rotate_backward(x[:, part], w, 1e-6, theta, adjacent, gy[:, part], dtype)[1]
         within(g[name], (v, e.nan_to_num(0.0)), name)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_gain_gradients_of_a_side_without_heads_are_zero(dt):
+    op = A.mdcn_rotary_create(64, [32])
+    x = rand(9, 2, 64, seed=1, dtype=DTYPES[dt]).cuda()
+    w = torch.ones(64, dtype=DTYPES[dt], device="cuda")
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")[None]
+    none = x[:, :0]
+    for _ in range(3):
+        poison()
+        g = A.norm_rotate_backward(op, x, none, pos, w, w, x, none)
+        assert (g["k_gain"] == 0).all() and g["q_gain"].isfinite().all()
+        poison()
+        g = A.norm_rotate_backward(op, none, x, pos, w, w, none, x)
+        assert (g["q_gain"] == 0).all() and g["k_gain"].isfinite().all()
