@@ -315,8 +315,8 @@ void mdcn_rotary_destroy(mdcn_rotary *op);
  *   its pointers are then ignored), dims[3] stride of positions between axes;
  *   dims[4..11] token and head stride of q, k, q_out, k_out.
  *   positions: int32 [axes][tokens].
- * q_out may be q and k_out k (same view).  Angles are reduced in double, so
- * that any int32 position is exact to fp32.
+ * q_out may be q and k_out k (same view).  Angles are reduced in 64-bit integers:
+ * cosine and sine at any int32 position are within 2^-24 of the exact ones.
  * Errors: MDCN_E_NULL, MDCN_E_SHAPE, MDCN_E_DTYPE, MDCN_E_ALIAS,
  * MDCN_E_DEVICE, MDCN_E_LAUNCH. */
 mdcn_status mdcn_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const int64_t dims[12],

@@ -22,11 +22,11 @@ struct Heads {
     int64_t token_stride, head_stride;
 };
 
-// The angle of pair i at position p is 2 pi * turns[i] * p.  Passed to the
-// kernels by value (1.2 KB of kernel arguments), so a handle holds no device
-// memory.
+// The angle of pair i at position p is turns[i] * p, in units of 2^-64 turns, modulo
+// a turn.  Passed to the kernels by value (1.2 KB of kernel arguments), so a handle
+// holds no device memory.
 struct RotaryTable {
-    double turns[kMaxRotaryDim / 2];
+    uint64_t turns[kMaxRotaryDim / 2];
     uint8_t axis[kMaxRotaryDim / 2];
 };
 

@@ -263,9 +263,13 @@ mdcn_status mdcn_rotary_create(int32_t dim, int32_t axes, const int32_t *pairs, 
     // dealt in turn: pair j of every axis that has one, then pair j + 1
     int32_t n = 0;
     auto put = [&](int32_t axis, int32_t j) {
-        const double e = per_axis ? double(j) / pairs[axis] : double(n) / total;
+        constexpr long double kPi = 3.14159265358979323846264338327950288L;
+        const long double e = per_axis ? static_cast<long double>(j) / pairs[axis]
+                                       : static_cast<long double>(n) / total;
+        const long double turns = std::pow(static_cast<long double>(base), -e) / (2 * kPi);
+        const long double rounded = std::rint(std::ldexp(turns - std::floor(turns), 64));
         r->table.axis[n] = uint8_t(axis);
-        r->table.turns[n] = std::pow(base, -e) / (2.0 * M_PI);
+        r->table.turns[n] = rounded < std::ldexp(1.0L, 64) ? uint64_t(rounded) : 0;
         ++n;
     };
     if (round_robin) {

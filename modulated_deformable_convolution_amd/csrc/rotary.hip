@@ -9,10 +9,12 @@
 // Pair i is channels (i, i + pairs), or (2i, 2i + 1) when adjacent; channels
 // from 2 * pairs on are not turned.
 //
-// Angles: position * frequency in turns is taken in double and reduced to
-// [-1/2, 1/2] there, so far positions (10^6 and more) lose nothing; sine and
-// cosine of the rest in fp32.  A wave computes the pairs of a token once, one
-// or two per lane, and shares them through LDS for all heads of the token.
+// Angles: in units of 2^-64 turns, as 64-bit integers whose product with a position drops
+// the whole turns by itself: off by 2^-34 turns at most at any int32 position (a
+// rounded product of rounded doubles by 3e-7 rad at 2^31), of which the upper 32 bits
+// are taken; sine and cosine in fp32.  A wave computes the
+// pairs of a token once, one or two per lane, and shares them through LDS for all
+// heads of the token.
 //
 // A head is spread over G lanes (a power of two), each holding units of V
 // values from the first channels of its pairs and the V second channels, so
@@ -117,6 +119,29 @@ __device__ __forceinline__ void turn_unit(float (&x)[2 * V], const float (&c)[V]
     }
 }
 
+// Sine and cosine of an angle in units of 2^-32 turns: quarter turns taken off, and the
+// Taylor series on [-pi/4, pi/4] up to the terms below 2^-30.  The angle enters as a
+// float and what that leaves, so that both are within 2^-24 of the exact values.
+__device__ __forceinline__ void sine_cosine(int32_t angle, float &sine, float &cosine)
+{
+    const int n = int(uint32_t(angle) + (1u << 29)) >> 30;
+    const double theta = double(int32_t(uint32_t(angle) - (uint32_t(n) << 30))) *
+                         (6.283185307179586 / 4294967296.0);
+    const float t = float(theta), rest = float(theta - double(t));
+    const float z = t * t, z_rest = fmaf(t, t, -z) + 2.0f * t * rest;
+    float p = fmaf(z, 1.0f / 362880, -1.0f / 5040);
+    p = fmaf(z, p, 1.0f / 120);
+    p = fmaf(z, p, -1.0f / 6);
+    const float s = t + fmaf(t * z, p, rest);
+    float q = fmaf(z, -1.0f / 3628800, 1.0f / 40320);
+    q = fmaf(z, q, -1.0f / 720);
+    q = fmaf(z, q, 1.0f / 24);
+    const float c = 1.0f + (fmaf(z * z, q, -0.5f * z_rest) - 0.5f * z);
+    const float a = n & 1 ? c : s, b = n & 1 ? s : c;
+    sine = n & 2 ? -a : a;
+    cosine = (n + 1) & 2 ? -b : b;
+}
+
 // Cosines and sines of one token's pairs, in LDS: each lane computes every
 // 64th pair and all read what their units need, (1, 0) past the turned
 // pairs.  A wave writes and reads its own table only.
@@ -132,10 +157,8 @@ __device__ __forceinline__ void angles(float (&c)[U][V], float (&s)[U][V], Angle
     for (int i = lane; i < a.dim / 2; i += 64) {
         float cv = 1.0f, sv = 0.0f;
         if (i < a.pairs) {
-            const int p = a.positions[a.table.axis[i] * a.axis_stride + t];
-            double turns = double(p) * a.table.turns[i];
-            turns -= rint(turns);
-            sincospif(float(2.0 * turns), &sv, &cv);
+            const int64_t p = a.positions[a.table.axis[i] * a.axis_stride + t];
+            sine_cosine(int32_t(uint64_t(p) * a.table.turns[i] >> 32), sv, cv);
         }
         table.c[i] = cv;
         table.s[i] = a.inverse ? -sv : sv;

@@ -103,3 +103,27 @@ def test_gain_gradients_of_a_side_without_heads_are_zero(dt):
         poison()
         g = A.norm_rotate_backward(op, none, x, pos, w, w, none, x)
         assert (g["q_gain"] == 0).all() and g["k_gain"].isfinite().all()
+
+
+@pytest.mark.parametrize("far", [0, 10 ** 6, 10 ** 9, 2 ** 31 - 400, -2 ** 31])
+@pytest.mark.parametrize("base", [100.0, 10000.0, 1000000.0])
+def test_angles_of_far_positions(far, base):
+    """Cosine and sine at far int32 positions against 60 digits: 3 x 2^-24, two for the sine and
+    cosine of an angle within a turn (a unit in the last place each way), one for the
+    angle's rest that they leave out."""
+    mp = pytest.importorskip("mpmath")
+    dim, t = 64, 60
+    op = A.mdcn_rotary_create(dim, [dim // 2], base=base)
+    x = torch.zeros(t, 1, dim)
+    x[..., :dim // 2] = 1.0
+    pos = [far + 2 * i for i in range(t)]
+    y = A.rotate(op, x.cuda(), x.cuda()[:, :0], torch.tensor([pos], dtype=torch.int32).cuda())[0]
+    y = y.double().cpu()[:, 0]
+    worst = 0.0
+    with mp.workdps(60):
+        freq = [mp.mpf(base) ** (-mp.mpf(i) / (dim // 2)) for i in range(dim // 2)]
+        for n, p in enumerate(pos):
+            for i, f in enumerate(freq):
+                worst = max(worst, abs(mp.cos(p * f) - float(y[n, i])),
+                            abs(mp.sin(p * f) - float(y[n, i + dim // 2])))
+    assert float(worst) <= 3 * R.E32, "%.2f x 2^-24" % (float(worst) / R.E32)
