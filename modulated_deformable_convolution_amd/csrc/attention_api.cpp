@@ -115,6 +115,25 @@ bool same_view(const View &a, const View &b)
            a.h.head_stride == b.h.head_stride && a.tokens == b.tokens && a.heads == b.heads;
 }
 
+// A buffer without strides, and whether the call writes it.
+struct Block {
+    const void *p;
+    size_t n;
+    bool written;
+};
+
+// Whether a written one shares bytes with any other.
+template <int N> bool blocks_overlap(const Block (&blocks)[N])
+{
+    for (const Block &x : blocks)
+        for (const Block &y : blocks) {
+            const char *a = static_cast<const char *>(x.p), *b = static_cast<const char *>(y.p);
+            if (&x != &y && x.written && a && b && overlap(a, a + x.n, b, b + y.n))
+                return true;
+        }
+    return false;
+}
+
 mdcn_status launched(hipError_t e) { return e == hipSuccess ? MDCN_OK : MDCN_E_LAUNCH; }
 
 void *align_up(void *p)
@@ -407,31 +426,22 @@ mdcn_status mdcn_norm_rotate_backward(const mdcn_rotary *op, mdcn_dtype dtype,
         if (!workspace || workspace_bytes < need)
             return MDCN_E_WORKSPACE;
         const size_t gain_bytes = size_t(a.dim) * elem_size(dtype);
-        const struct {
-            const void *p;
-            size_t n;
-            bool written;
-        } small[] = {{workspace, workspace_bytes, true}, {grad_q_gain, gain_bytes, true},
-                     {grad_k_gain, gain_bytes, true},    {q_gain, gain_bytes, false},
-                     {k_gain, gain_bytes, false},        {positions, a.tokens ? size_t((op->axes - 1) * a.axis_stride + a.tokens) * 4 : 0,
-                      false}};
-        for (const auto &x : small) {
+        const size_t pos_bytes =
+            a.tokens ? size_t((op->axes - 1) * a.axis_stride + a.tokens) * 4 : 0;
+        const Block small[] = {{workspace, workspace_bytes, true}, {grad_q_gain, gain_bytes, true},
+                               {grad_k_gain, gain_bytes, true},    {q_gain, gain_bytes, false},
+                               {k_gain, gain_bytes, false},        {positions, pos_bytes, false}};
+        if (blocks_overlap(small))
+            return MDCN_E_ALIAS;
+        for (const Block &x : small) {
             if (!x.p)
                 continue;
             for (const View &v : out)
                 if (overlap(v, x.p, x.n))
                     return MDCN_E_ALIAS;
-            if (!x.written)
-                continue;
             for (const View &v : in)
-                if (overlap(v, x.p, x.n))
+                if (x.written && overlap(v, x.p, x.n))
                     return MDCN_E_ALIAS;
-            const char *c = static_cast<const char *>(x.p);
-            for (const auto &y : small) {
-                const char *d = static_cast<const char *>(y.p);
-                if (&x != &y && d && overlap(c, c + x.n, d, d + y.n))
-                    return MDCN_E_ALIAS;
-            }
         }
         if ((st = mdcn::check_device()) != MDCN_OK)
             return st;
@@ -532,6 +542,13 @@ mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_
             if (share_values(x, o) || overlap(x, lse, lse_bytes) ||
                 (split && overlap(x, workspace, workspace_bytes)))
                 return MDCN_E_ALIAS;
+        const Block small[] = {{lse, lse_bytes, true},
+                               {split ? workspace : nullptr, workspace_bytes, true},
+                               {cu_q, cu_bytes, false},
+                               {cu_k, cu_bytes, false},
+                               {used_k, size_t(a.batch) * 4, false}};
+        if (blocks_overlap(small))
+            return MDCN_E_ALIAS;
         if (a.q_tokens == 0 || a.batch == 0)
             return MDCN_OK;
         if ((st = mdcn::check_device()) != MDCN_OK)
@@ -625,6 +642,13 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
         for (const View &x : in)
             if (overlap(x, workspace, workspace_bytes))
                 return MDCN_E_ALIAS;
+        const Block small[] = {{workspace, workspace_bytes, true},
+                               {lse, lse_bytes, false},
+                               {cu_q, cu_bytes, false},
+                               {cu_k, cu_bytes, false},
+                               {used_k, size_t(a.batch) * 4, false}};
+        if (blocks_overlap(small))
+            return MDCN_E_ALIAS;
         if (a.batch == 0 || (a.q_tokens == 0 && a.k_tokens == 0))
             return MDCN_OK;
         if ((st = mdcn::check_device()) != MDCN_OK)

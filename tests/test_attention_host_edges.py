@@ -1,0 +1,49 @@
+"""More that the attention entry points refuse or take, before any GPU is asked for
+anything (the pointers here are addresses that nothing reads)."""
+import pytest
+import torch
+
+from helpers import ensure_built
+from modulated_deformable_convolution_amd import mdcn
+from test_attention_host import attend_status, backward_status
+
+ensure_built()
+BASE, STEP = 1 << 20, 1 << 24
+# where test_attention_host puts the buffers
+FORWARD = {n: BASE + i * STEP for i, n in enumerate(
+    ["q", "k", "v", "cu_q", "cu_k", "used", "out", "lse", "ws"])}
+BACKWARD = {n: BASE + i * STEP for i, n in enumerate(
+    ["q", "k", "v", "out", "lse", "go", "cu_q", "cu_k", "used", "gq", "gk", "gv", "ws"])}
+FEW = dict(q_tokens=3, change={2: 60000}, ws=9 << 20)        # few rows, many keys: with a workspace
+
+
+@pytest.mark.parametrize("other", ["cu_q", "cu_k", "used"])
+@pytest.mark.parametrize("kw", [{}, FEW], ids=["tiles", "split"])
+def test_lse_over_what_the_forward_reads(kw, other):
+    assert attend_status(ptr={"lse": FORWARD[other]}, **kw) == mdcn.MDCN_E_ALIAS
+    assert attend_status(ptr={"lse": FORWARD[other] - 4}, **kw) == mdcn.MDCN_E_ALIAS
+
+
+@pytest.mark.parametrize("other", ["cu_q", "cu_k", "used", "lse"])
+def test_forward_workspace_over_other_buffers(other):
+    assert attend_status(ptr={"ws": FORWARD[other]}, **FEW) == mdcn.MDCN_E_ALIAS
+    assert attend_status(ptr={"ws": FORWARD[other] - 256}, **FEW) == mdcn.MDCN_E_ALIAS
+
+
+@pytest.mark.parametrize("other", ["cu_q", "cu_k", "used", "lse"])
+def test_backward_workspace_over_other_buffers(other):
+    assert backward_status(ptr={"ws": BACKWARD[other]}) == mdcn.MDCN_E_ALIAS
+    assert backward_status(ptr={"ws": BACKWARD[other] - 256}) == mdcn.MDCN_E_ALIAS
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would run on the GPU")
+def test_buffers_side_by_side_are_taken():
+    """Buffers of one arena that touch and do not overlap."""
+    lse = FORWARD["cu_q"] - 4 * 300 * 4
+    assert attend_status(ptr={"lse": lse}) == mdcn.MDCN_E_DEVICE
+    assert attend_status(ptr={"lse": FORWARD["cu_q"] + 16}) == mdcn.MDCN_E_DEVICE
+    assert attend_status(**FEW) == mdcn.MDCN_E_DEVICE
+    # the tile kernel has no workspace: whatever is given is not looked at
+    assert attend_status(ptr={"ws": FORWARD["cu_q"]}) == mdcn.MDCN_E_DEVICE
+    assert backward_status(ptr={"ws": BACKWARD["cu_q"] - (1 << 22)}) == mdcn.MDCN_E_DEVICE
+    assert backward_status(ptr={"used": 0}) == mdcn.MDCN_E_DEVICE
