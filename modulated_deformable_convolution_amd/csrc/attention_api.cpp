@@ -77,9 +77,10 @@ bool distinct_rows(const View &v)
                   : t >= v.dim && h >= (v.tokens - 1) * t + v.dim;
 }
 
+// (an empty range overlaps nothing, wherever it lies)
 bool overlap(const char *a0, const char *a1, const char *b0, const char *b1)
 {
-    return a0 < b1 && b0 < a1;
+    return a0 < a1 && b0 < b1 && a0 < b1 && b0 < a1;
 }
 
 bool overlap(const View &a, const View &b) { return overlap(a.lo(), a.hi(), b.lo(), b.hi()); }

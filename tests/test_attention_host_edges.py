@@ -47,3 +47,12 @@ def test_buffers_side_by_side_are_taken():
     assert attend_status(ptr={"ws": FORWARD["cu_q"]}) == mdcn.MDCN_E_DEVICE
     assert backward_status(ptr={"ws": BACKWARD["cu_q"] - (1 << 22)}) == mdcn.MDCN_E_DEVICE
     assert backward_status(ptr={"used": 0}) == mdcn.MDCN_E_DEVICE
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would run on the GPU")
+def test_empty_views_share_nothing():
+    """No keys: their pointers may lie anywhere, inside an output too."""
+    inside = {"k": FORWARD["out"] + 512, "v": FORWARD["out"] + 1024}
+    assert attend_status(change={2: 0}, ptr=inside) == mdcn.MDCN_E_DEVICE
+    assert attend_status(change={2: 0}, ptr={"k": FORWARD["lse"] + 512}) == mdcn.MDCN_E_DEVICE
+    assert attend_status(change={2: 200}, ptr=inside) == mdcn.MDCN_E_ALIAS
