@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <new>
+#include <numeric>
 
 #include "attention.h"
 #include "entry.h"
@@ -91,23 +92,45 @@ bool overlap(const View &a, const void *p, size_t bytes)
     return overlap(a.lo(), a.hi(), c, c + bytes);
 }
 
-// Views that interleave in one allocation (queries, keys and values in the rows
-// of one projection) may overlap as address ranges without sharing a value:
-// with one token stride, their rows are compared within a token.
-bool share_values(const View &a, const View &b)
+// Views that interleave in one allocation may overlap as address ranges without
+// sharing a value.  Queries, keys and values in the rows of one projection: with one
+// token stride, their rows are compared within a token.
+bool apart_in_tokens(const View &a, const View &b)
 {
-    if (!overlap(a, b))
-        return false;
     const int64_t t = a.h.token_stride * int64_t(a.elem);
     if (a.h.token_stride != b.h.token_stride || a.elem != b.elem || t == 0 || a.tokens <= 1)
-        return true;
+        return false;
     const int64_t wa = ((a.heads - 1) * a.h.head_stride + a.dim) * int64_t(a.elem);
     const int64_t wb = ((b.heads - 1) * b.h.head_stride + b.dim) * int64_t(b.elem);
     int64_t off = int64_t(reinterpret_cast<uintptr_t>(b.lo()) -
                           reinterpret_cast<uintptr_t>(a.lo())) % t;
     if (off < 0)
         off += t;
-    return !(wa <= off && off + wb <= t);
+    return wa <= off && off + wb <= t;
+}
+
+// Queries, keys and values of one head side by side: all rows of a view begin at one
+// address modulo any divisor of the strides that are stepped over.
+bool apart_in_heads(const View &a, const View &b)
+{
+    int64_t g = 0;
+    for (const View *v : {&a, &b}) {
+        g = std::gcd(g, v->tokens > 1 ? v->h.token_stride : 0);
+        g = std::gcd(g, v->heads > 1 ? v->h.head_stride : 0);
+    }
+    g *= int64_t(a.elem);
+    if (g == 0 || a.elem != b.elem)
+        return false;
+    int64_t off = int64_t(reinterpret_cast<uintptr_t>(b.lo()) -
+                          reinterpret_cast<uintptr_t>(a.lo())) % g;
+    if (off < 0)
+        off += g;
+    return a.dim * int64_t(a.elem) <= off && off + b.dim * int64_t(b.elem) <= g;
+}
+
+bool share_values(const View &a, const View &b)
+{
+    return overlap(a, b) && !apart_in_tokens(a, b) && !apart_in_heads(a, b);
 }
 
 bool same_view(const View &a, const View &b)

@@ -5,7 +5,7 @@ import torch
 
 from helpers import ensure_built
 from modulated_deformable_convolution_amd import mdcn
-from test_attention_host import attend_status, backward_status
+from test_attention_host import attend_status, backward_status, dims, rotate_status
 
 ensure_built()
 BASE, STEP = 1 << 20, 1 << 24
@@ -56,3 +56,22 @@ def test_empty_views_share_nothing():
     assert attend_status(change={2: 0}, ptr=inside) == mdcn.MDCN_E_DEVICE
     assert attend_status(change={2: 0}, ptr={"k": FORWARD["lse"] + 512}) == mdcn.MDCN_E_DEVICE
     assert attend_status(change={2: 200}, ptr=inside) == mdcn.MDCN_E_ALIAS
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would run on the GPU")
+@pytest.mark.parametrize("tokens", [1, 10])
+def test_rotation_in_place_of_queries_and_keys_that_alternate(tokens):
+    """[tokens][heads][query, key, value][dim]: no value belongs to two views."""
+    def status(q, k, q_out, k_out, heads=2, row=48):
+        d = dims(tokens, heads, heads, tokens, row, 24, row, 24, row, 24, row, 24)
+        return rotate_status(d, q=q, k=k, pos=BASE - 8192, qo=q_out, ko=k_out)
+    key = BASE + 8 * 4
+    assert status(BASE, key, BASE, key) == mdcn.MDCN_E_DEVICE
+    assert status(BASE, key, key, BASE) == mdcn.MDCN_E_ALIAS              # exchanged
+    assert status(BASE, key, BASE + 16 * 4, key) == mdcn.MDCN_E_DEVICE    # into the values' place
+    assert status(BASE, key, BASE + 4 * 4, key) == mdcn.MDCN_E_ALIAS      # half of it
+    assert status(BASE, key, BASE + 20 * 4, key) == mdcn.MDCN_E_ALIAS     # over the next head's
+    assert status(BASE, key, BASE, BASE + 4 * 4) == mdcn.MDCN_E_ALIAS
+    # rows whose stride the heads' does not divide
+    assert status(BASE, key, BASE, key, row=50) == (
+        mdcn.MDCN_E_ALIAS if tokens > 1 else mdcn.MDCN_E_DEVICE)

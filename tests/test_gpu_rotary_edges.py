@@ -127,3 +127,18 @@ def test_angles_of_far_positions(far, base):
                 worst = max(worst, abs(mp.cos(p * f) - float(y[n, i])),
                             abs(mp.sin(p * f) - float(y[n, i + dim // 2])))
     assert float(worst) <= 3 * R.E32, "%.2f x 2^-24" % (float(worst) / R.E32)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 30])
+def test_alternating_queries_and_keys_in_place(dim, dt):
+    """[tokens][heads][query, key, value][dim]."""
+    op = A.mdcn_rotary_create(dim, [dim // 2])
+    x = rand(130, 3, 3, dim, seed=1, dtype=DTYPES[dt])
+    pos = torch.arange(130, dtype=torch.int32)[None]
+    theta = R.angles([dim // 2], 10000.0, False, False, pos)
+    d = x.cuda()
+    A.rotate(op, d[:, :, 0], d[:, :, 1], pos.cuda(), q_out=d[:, :, 0], k_out=d[:, :, 1])
+    within(d[:, :, 0], R.rotate(x[:, :, 0], theta, False, DTYPES[dt]), "q")
+    within(d[:, :, 1], R.rotate(x[:, :, 1], theta, False, DTYPES[dt]), "k")
+    assert torch.equal(d[:, :, 2].cpu(), x[:, :, 2])
