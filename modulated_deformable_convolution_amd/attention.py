@@ -130,6 +130,14 @@ def _check_ints(where, name, t, like, shape):
         _fail(where, "%s must be contiguous" % name)
 
 
+def _workspace_bytes(where, workspace, like):
+    if workspace is None:
+        return 0
+    if workspace.device != like.device or not workspace.is_contiguous():
+        _fail(where, "workspace must be contiguous on the tensors' device", _m.MDCN_E_WORKSPACE)
+    return workspace.numel() * workspace.element_size()
+
+
 def _strides(t):
     # a dimension of one element is never stepped over; whatever stride torch
     # gives it must not be refused
@@ -267,7 +275,7 @@ def norm_rotate_backward(op: Rotary, q, k, positions, q_gain, k_gain, grad_q_out
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), positions.data_ptr(),
         q_gain.data_ptr(), k_gain.data_ptr(), eps, grad_q_out.data_ptr(), grad_k_out.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dq_gain.data_ptr(), dk_gain.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), stream)
+        workspace.data_ptr(), _workspace_bytes(where, workspace, q), stream)
     if st:
         _m._check(st, where)
     return {"q": dq, "k": dk, "q_gain": dq_gain, "k_gain": dk_gain}
@@ -340,7 +348,7 @@ def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, 
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
         cu_k.data_ptr(), None if used_k is None else used_k.data_ptr(), out.data_ptr(),
         lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), stream)
+        _workspace_bytes("attend", workspace, q), stream)
     if st:
         _m._check(st, "attend")
     return out, lse
@@ -367,7 +375,7 @@ def attend_backward(op: Attention, q, k, v, out, lse, grad_out, cu_q, cu_k, used
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         lse.data_ptr(), grad_out.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
         None if used_k is None else used_k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-        dv.data_ptr(), workspace.data_ptr(), workspace.numel(), stream)
+        dv.data_ptr(), workspace.data_ptr(), _workspace_bytes(where, workspace, q), stream)
     if st:
         _m._check(st, where)
     return {"q": dq, "k": dk, "v": dv}

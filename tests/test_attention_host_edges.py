@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from helpers import ensure_built
+from modulated_deformable_convolution_amd import attention as A
 from modulated_deformable_convolution_amd import mdcn
 from test_attention_host import attend_status, backward_status, dims, rotate_status
 
@@ -75,3 +76,18 @@ def test_rotation_in_place_of_queries_and_keys_that_alternate(tokens):
     # rows whose stride the heads' does not divide
     assert status(BASE, key, BASE, key, row=50) == (
         mdcn.MDCN_E_ALIAS if tokens > 1 else mdcn.MDCN_E_DEVICE)
+
+
+@pytest.mark.parametrize("bad", [
+    torch.zeros(64, dtype=torch.uint8, device="meta"), torch.zeros(64, 2, dtype=torch.uint8)[:, 0],
+    torch.zeros(64, dtype=torch.uint8).expand(2, 64),
+])
+def test_workspaces_elsewhere_are_refused(bad):
+    """A workspace on another device, or with gaps, would be written past its memory."""
+    like = torch.zeros(1)
+    with pytest.raises(mdcn.MdcnError) as e:
+        A._workspace_bytes("attend", bad, like)
+    assert e.value.status == mdcn.MDCN_E_WORKSPACE
+    assert A._workspace_bytes("attend", torch.zeros(64, dtype=torch.uint8), like) == 64
+    assert A._workspace_bytes("attend", torch.zeros(3, 5), like) == 60
+    assert A._workspace_bytes("attend", None, like) == 0
