@@ -7,7 +7,8 @@ Tensors are [tokens, heads, dim] views of device memory with the channels of a
 head together (slices of a projection's output are taken as they are), one
 dtype per call.  Outputs and workspaces are allocated with torch, on the stream
 the call runs on; every step of the computation runs in the library's HIP
-kernels.  Calls enqueue work and return; they raise MdcnError on bad arguments.
+kernels.  Calls enqueue work on the current device, which must be the tensors', and
+return; they raise MdcnError on bad arguments.
 """
 from __future__ import annotations
 
@@ -33,6 +34,10 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream"):
     # the same handle without building a Stream object (a microsecond a call)
     def _raw_stream(index, _get=torch._C._cuda_getCurrentRawStream):  # noqa: F811
         return _get(index) or None
+
+
+# torch.cuda.current_device without its checks
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _like(shape, dtype, device):
@@ -117,10 +122,16 @@ def _check_view(where, name, t, like, shape):
         _fail(where, "the channels of a head of %s must lie together" % name)
 
 
+def _check_current(where, index):
+    if index != _current_device():
+        _fail(where, "the tensors' device must be the current one", _m.MDCN_E_DEVICE)
+
+
 def _device_tensors(where, *tensors):
     for t in tensors:
         if not t.is_cuda:
             _fail(where, "tensors must be device tensors", MDCN_E_NULL)
+    _check_current(where, tensors[0].get_device())
 
 
 def _check_ints(where, name, t, like, shape):

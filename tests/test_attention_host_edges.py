@@ -91,3 +91,12 @@ def test_workspaces_elsewhere_are_refused(bad):
     assert A._workspace_bytes("attend", torch.zeros(64, dtype=torch.uint8), like) == 64
     assert A._workspace_bytes("attend", torch.zeros(3, 5), like) == 60
     assert A._workspace_bytes("attend", None, like) == 0
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Kernels are launched on the current device."""
+    monkeypatch.setattr(A, "_current_device", lambda: 0)
+    A._check_current("attend", 0)
+    with pytest.raises(mdcn.MdcnError) as e:
+        A._check_current("attend", 1)
+    assert e.value.status == mdcn.MDCN_E_DEVICE
