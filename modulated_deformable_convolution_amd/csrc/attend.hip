@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     settle<T, DP>(qf);
     Softmax<T, DP> sm;
     sm.init();
-    const float c = a.scale * kLog2e, margin = kRaise / c;
+    const float c = a.scale * kLog2e, margin = raise_margin(c);
     bool check = a.causal != 0;                              // hidden keys seen so far
     auto repair = [&](int i) {
         // this wave's keys of the rounds before i, one round at a time

@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
     const int half = lane >> 5;
     const int col = lane & 31;
     const int group = a.q_heads / a.k_heads;
-    const float c = a.scale * kLog2e, margin = kRaise / c;
+    const float c = a.scale * kLog2e, margin = raise_margin(c);
 
     Chunk chunk;
     chunk.load(a, 0, lane);

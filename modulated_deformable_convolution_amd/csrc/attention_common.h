@@ -391,6 +391,10 @@ template <typename T, int DP, int KW> constexpr int waves_per_simd()
 // costs no accuracy in fp32 sums and saves most rescalings.
 constexpr float kRaise = 8.0f;
 
+// The same in raw scores.  Finite, so that the first score raises the maximum from -infinity
+// however small the scale is.
+__device__ __forceinline__ float raise_margin(float c) { return fminf(kRaise / c, 3.0e38f); }
+
 // Softmax state of one query row (both halves of the wave hold the same
 // maximum; the sums are those of the half's own keys).
 template <typename T, int DP> struct Softmax {
