@@ -382,11 +382,18 @@ mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_
                         const int32_t *cu_k, const int32_t *used_k, void *out, float *lse,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* The same, and tokens before the first sequence and after the last get what a
+ * row that sees no key gets: zeros in out if fill & 1, -infinity in lse if fill & 2. */
+mdcn_status mdcn_attend_filled(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[11],
+                               const void *q, const void *k, const void *v, const int32_t *cu_q,
+                               const int32_t *cu_k, const int32_t *used_k, int32_t fill, void *out,
+                               float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Gradients of mdcn_attend's out with respect to q, k and v, from grad_out and
  * the forward's out and lse for the same q, k and v.  dims[0..10] as there,
  * dims[11..18] token and head stride of grad_out, grad_q, grad_k, grad_v.  The
- * gradients of shared key heads are the sums over their query heads; keys that are not used get
- * zeros.  A row that sees no key has a zero gradient and adds to none.  Hidden
+ * gradients of shared key heads are the sums over their query heads; keys that are not used,
+ * and tokens before the first sequence and after the last, get zeros.  A row that sees no key has a zero gradient and adds to none.  Hidden
  * keys and values that are infinite or NaN reach no gradient; such values in a
  * row of q or grad_out do reach the keys of the whole sequence, hidden ones
  * too.  Sums in fp32, probabilities and score gradients rounded to the inputs'

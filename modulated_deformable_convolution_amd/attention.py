@@ -337,9 +337,12 @@ def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, 
     [k_tokens, k_heads, dim], cu_q and cu_k int32 [batch + 1] offsets of the
     sequences.  used_k (int32 [batch]): the keys that sequence b's part of k and
     v holds so far, for a cache with room.  Returns (out, lse) with lse fp32
-    [q_heads, q_tokens]."""
+    [q_heads, q_tokens].  Tokens before the first sequence and after the last get
+    zeros and -infinity, like a row that sees no key; in an out or lse that the
+    caller gives they are left as they are."""
     _device_tensors("attend", q, k, v, cu_q, cu_k)
     stream, ctx = _stream_of(stream, q)
+    fill = (1 if out is None else 0) | (2 if lse is None else 0)
     with ctx or _NO_CONTEXT:
         if out is None:
             out = torch.empty_like(q)
@@ -355,9 +358,9 @@ def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, 
             _check_lse("attend", op, q, lse)
         if workspace is None and call[2] is not None:
             workspace = _new(call[2])
-    st = _m._lib.mdcn_attend(
+    st = _m._lib.mdcn_attend_filled(
         op.handle, call[0], call[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
-        cu_k.data_ptr(), None if used_k is None else used_k.data_ptr(), out.data_ptr(),
+        cu_k.data_ptr(), None if used_k is None else used_k.data_ptr(), fill, out.data_ptr(),
         lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
         _workspace_bytes("attend", workspace, q), stream)
     if st:
@@ -367,7 +370,8 @@ def attend(op: Attention, q, k, v, cu_q, cu_k, used_k=None, out=None, lse=None, 
 
 def attend_backward(op: Attention, q, k, v, out, lse, grad_out, cu_q, cu_k, used_k=None,
                     workspace=None, stream=None):
-    """Gradients of attend: a dict of q, k, v.  out and lse are the forward's."""
+    """Gradients of attend: a dict of q, k, v, with zeros for tokens of no sequence.  out
+    and lse are the forward's."""
     where = "attend_backward"
     _device_tensors(where, q, k, v, out, lse, grad_out, cu_q, cu_k)
     _check_lse(where, op, q, lse)

@@ -48,6 +48,17 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     const int rg = wave % RW, kg = wave / RW;
     const int half = lane >> 5;
 
+    if (int(blockIdx.x) >= a.fill_from) {
+        const int part = int(blockIdx.x) - a.fill_from, parts = int(gridDim.x) - a.fill_from;
+        if (a.fill & kFillOut)
+            zero_outside<T>(a.out, a.cu_q, a.batch, a.q_tokens, a.q_heads, a.dim, part, parts);
+        if (a.fill & kFillLse)
+            outside_rows(a.cu_q, a.batch, a.q_tokens, a.q_heads, part, parts, [&](int t, int h) {
+                a.lse[int64_t(h) * a.q_tokens + t] = -INFINITY;
+            });
+        return;
+    }
+
     // Key heads vary fastest over workgroups: neighbours on one XCD (every
     // eighth workgroup) then read the same keys and values through its L2.
     const int kv_head = blockIdx.x % a.k_heads;
@@ -209,11 +220,14 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
 }
 
 template <typename T, int DP, int RW, int KW>
-hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
+hipError_t launch_shape(AttendArgs a, hipStream_t s)
 {
     constexpr int ROWS = 32 * RW;
     const int64_t tiles = int64_t(a.q_tokens / ROWS) + (a.batch < a.q_tokens ? a.batch : a.q_tokens);
-    const int64_t blocks = tiles * a.q_heads;
+    int64_t blocks = tiles * a.q_heads;
+    a.fill_from = blocks < INT32_MAX ? int(blocks) : INT32_MAX;
+    if (a.fill)
+        blocks += fill_blocks(int64_t(a.q_tokens) * a.q_heads * a.dim * sizeof(T));
     if (blocks > INT32_MAX)
         return hipErrorInvalidValue;
     if (blocks == 0)

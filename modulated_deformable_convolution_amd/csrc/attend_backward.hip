@@ -42,6 +42,14 @@ constexpr int kFar = 1 << 30;                 // more than any number of rows
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
 {
+    if (int(blockIdx.x) >= a.fill_from) {
+        // gradients of tokens that belong to no sequence
+        const int part = int(blockIdx.x) - a.fill_from, parts = int(gridDim.x) - a.fill_from;
+        zero_outside<T>(a.dq, a.cu_q, a.batch, a.q_tokens, a.q_heads, a.dim, part, parts);
+        zero_outside<T>(a.dk, a.cu_k, a.batch, a.k_tokens, a.k_heads, a.dim, part, parts);
+        zero_outside<T>(a.dv, a.cu_k, a.batch, a.k_tokens, a.k_heads, a.dim, part, parts);
+        return;
+    }
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int w = int(blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
     const int head = w % a.q_heads;
@@ -511,17 +519,19 @@ int64_t tiles_of(int64_t tokens, int64_t batch, int rows)
 }
 
 template <typename T, int DP, int RW, int KW>
-hipError_t launch_shape(const AttendArgs &a, hipStream_t s)
+hipError_t launch_shape(AttendArgs a, hipStream_t s)
 {
     const int64_t d_blocks = (tiles_of(a.q_tokens, a.batch, 32) * a.q_heads + 3) / 4;
     const int64_t q_blocks = tiles_of(a.q_tokens, a.batch, 32 * RW) * a.q_heads;
     const int64_t k_tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t k_blocks = k_tiles * a.splits;
     const int64_t sum_blocks = tiles_of(a.k_tokens, a.batch, kSumRows) * a.k_heads;
-    if (sum_blocks > INT32_MAX || d_blocks > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
+    if (sum_blocks > INT32_MAX || 4 * d_blocks > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
         return hipErrorInvalidValue;
-    if (d_blocks > 0)
-        attend_delta_kernel<T, DP><<<uint32_t(d_blocks), 256, 0, s>>>(a);
+    a.fill_from = int(d_blocks);
+    const int fill = fill_blocks((int64_t(a.q_tokens) * a.q_heads + 2 * int64_t(a.k_tokens) * a.k_heads) *
+                                 a.dim * sizeof(T));
+    attend_delta_kernel<T, DP><<<uint32_t(d_blocks + fill), 256, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k_blocks > 0) {
         attend_dkv_kernel<T, DP><<<uint32_t(k_blocks), 64 * kWaves, 0, s>>>(a);

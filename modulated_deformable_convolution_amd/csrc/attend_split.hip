@@ -407,6 +407,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
         }
         return;
     }
+    // the token belongs to no sequence
+    if ((a.fill & kFillOut) && int(threadIdx.x) < a.dim)
+        reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.out, token, head)))[threadIdx.x] =
+            T(0.0f);
+    if ((a.fill & kFillLse) && threadIdx.x == 0)
+        a.lse[int64_t(head) * a.q_tokens + token] = -INFINITY;
 }
 
 template <typename T, int DP>

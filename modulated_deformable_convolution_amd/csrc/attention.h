@@ -65,8 +65,13 @@ struct AttendArgs {
     int32_t workers;       // split kernel: workgroups, and its unit is 32 << unit_shift keys
     int32_t unit_shift;
     int32_t splits;        // backward: workgroups that share a tile of keys
+    int32_t fill;          // forward: kFillOut, kFillLse
+    int32_t fill_from;     // first of the workgroups that fill (see outside_rows)
     float *partial;        // sums that several workgroups leave for one result
 };
+
+// Whether tokens that belong to no sequence get zeros in out and -infinity in lse.
+constexpr int kFillOut = 1, kFillLse = 2;
 
 // Waves that share the keys of 32 queries in attend, and of dq in the backward: 1 in
 // workgroups of 128 queries, 2 or 4 in workgroups of 64.

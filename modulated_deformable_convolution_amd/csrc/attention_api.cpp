@@ -526,10 +526,11 @@ mdcn_status mdcn_attend_workspace_bytes(const mdcn_attention *op, mdcn_dtype dty
     return MDCN_OK;
 }
 
-mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[11],
-                        const void *q, const void *k, const void *v, const int32_t *cu_q,
-                        const int32_t *cu_k, const int32_t *used_k, void *out, float *lse,
-                        void *workspace, size_t workspace_bytes, void *stream_ptr)
+mdcn_status mdcn_attend_filled(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[11],
+                               const void *q, const void *k, const void *v, const int32_t *cu_q,
+                               const int32_t *cu_k, const int32_t *used_k, int32_t fill, void *out,
+                               float *lse, void *workspace, size_t workspace_bytes,
+                               void *stream_ptr)
 {
     try {
         AttendArgs a = {};
@@ -573,7 +574,8 @@ mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_
                                {used_k, size_t(a.batch) * 4, false}};
         if (blocks_overlap(small))
             return MDCN_E_ALIAS;
-        if (a.q_tokens == 0 || a.batch == 0)
+        a.fill = fill & (mdcn::kFillOut | mdcn::kFillLse);
+        if (a.q_tokens == 0 || (a.batch == 0 && !a.fill))
             return MDCN_OK;
         if ((st = mdcn::check_device()) != MDCN_OK)
             return st;
@@ -594,6 +596,15 @@ mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_
     } catch (...) {
         return MDCN_E_INTERNAL;
     }
+}
+
+mdcn_status mdcn_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[11],
+                        const void *q, const void *k, const void *v, const int32_t *cu_q,
+                        const int32_t *cu_k, const int32_t *used_k, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    return mdcn_attend_filled(op, dtype, dims, q, k, v, cu_q, cu_k, used_k, 0, out, lse, workspace,
+                              workspace_bytes, stream);
 }
 
 mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_dtype dtype,
@@ -673,7 +684,7 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
                                {used_k, size_t(a.batch) * 4, false}};
         if (blocks_overlap(small))
             return MDCN_E_ALIAS;
-        if (a.batch == 0 || (a.q_tokens == 0 && a.k_tokens == 0))
+        if (a.q_tokens == 0 && a.k_tokens == 0)
             return MDCN_OK;
         if ((st = mdcn::check_device()) != MDCN_OK)
             return st;

@@ -620,6 +620,50 @@ __device__ __forceinline__ int wave_sum(int v)
     return __builtin_amdgcn_readlane(wave_scan(v), 63);
 }
 
+template <typename T>
+__device__ __forceinline__ const char *row_ptr(const Heads &h, int64_t token, int head)
+{
+    return reinterpret_cast<const char *>(static_cast<const T *>(h.data) + token * h.token_stride +
+                                          head * h.head_stride);
+}
+
+// Calls f(token, i), i in [0, each), for the tokens before the first sequence and after
+// the last (offsets `cu`), neighbouring i in neighbouring threads of `parts` workgroups.
+template <class F>
+__device__ __forceinline__ void outside_rows(const int32_t *cu, int batch, int tokens, int each,
+                                             int part, int parts, F &&f)
+{
+    const int begin = clamp_int(cu[0], 0, tokens);
+    const int end = clamp_int(cu[batch], begin, tokens);
+    const int64_t all = int64_t(begin + tokens - end) * each;
+    for (int64_t e = int64_t(part) * blockDim.x + threadIdx.x; e < all;
+         e += int64_t(parts) * blockDim.x) {
+        const int r = int(e / each);
+        f(r < begin ? r : end + r - begin, int(e % each));
+    }
+}
+
+// Zeros in the rows of `h` outside every sequence.
+template <typename T>
+__device__ __forceinline__ void zero_outside(const Heads &h, const int32_t *cu, int batch, int tokens,
+                                             int heads, int dim, int part, int parts)
+{
+    const int vecs = dim / int(16 / sizeof(T));
+    outside_rows(cu, batch, tokens, heads * vecs, part, parts, [&](int token, int i) {
+        char *row = const_cast<char *>(row_ptr<T>(h, token, i / vecs));
+        *reinterpret_cast<uint4 *>(row + i % vecs * 16) = make_uint4(0, 0, 0, 0);
+    });
+}
+
+// Workgroups that fill beyond those of the tiles, for rows of `bytes` bytes in all.  They
+// are there in every call, as only the GPU knows the offsets, and cost next to nothing
+// where nothing is outside.
+inline int fill_blocks(int64_t bytes)
+{
+    const int64_t n = bytes >> 18;
+    return n < 1 ? 1 : n > 64 ? 64 : int(n);
+}
+
 // The sequence and its tile that hold tile t of the batch, where count(span)
 // is the number of a sequence's tiles; false past the last tile.  Every lane
 // of the wave must call it.
@@ -674,13 +718,6 @@ __device__ __forceinline__ bool find_tile(const AttendArgs &a, int t, int lane, 
         base += __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
-}
-
-template <typename T>
-__device__ __forceinline__ const char *row_ptr(const Heads &h, int64_t token, int head)
-{
-    return reinterpret_cast<const char *>(static_cast<const T *>(h.data) + token * h.token_stride +
-                                          head * h.head_stride);
 }
 
 }  // namespace mdcn

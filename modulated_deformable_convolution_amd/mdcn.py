@@ -54,7 +54,7 @@ EXPORTED = [
     "mdcn_rotary_create", "mdcn_rotary_destroy", "mdcn_rotate", "mdcn_norm_rotate",
     "mdcn_norm_rotate_backward_workspace_bytes", "mdcn_norm_rotate_backward",
     "mdcn_attention_create", "mdcn_attention_destroy", "mdcn_attend_workspace_bytes",
-    "mdcn_attend", "mdcn_attend_backward_workspace_bytes", "mdcn_attend_backward",
+    "mdcn_attend", "mdcn_attend_filled", "mdcn_attend_backward_workspace_bytes", "mdcn_attend_backward",
 ]
 
 # bytes of the device array mdcn_forward_noalloc works in (include/mdcn.h)
@@ -129,6 +129,8 @@ def _bind(lib):
         "mdcn_attend_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
         "mdcn_attend": ([_vp, ctypes.c_int, _i64p] + [_vp] * 9 + [ctypes.c_size_t, _vp],
                         ctypes.c_int),
+        "mdcn_attend_filled": ([_vp, ctypes.c_int, _i64p] + [_vp] * 6 + [ctypes.c_int32] +
+                               [_vp] * 3 + [ctypes.c_size_t, _vp], ctypes.c_int),
         "mdcn_attend_backward_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
         "mdcn_attend_backward": ([_vp, ctypes.c_int, _i64p] + [_vp] * 13 + [ctypes.c_size_t, _vp],
                                  ctypes.c_int),

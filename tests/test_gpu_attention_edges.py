@@ -1,10 +1,14 @@
 """Attention on the GPU where it can go wrong."""
+import math
+
 import pytest
+import torch
 
 import attention_reference as R
 from helpers import ensure_built
 from modulated_deformable_convolution_amd import attention as A
-from test_gpu_attention import DTYPES, attend_case, ints, within
+from test_gpu_attention import DTYPES, attend_case, ints, rand, within
+from test_gpu_rotary_edges import poison
 
 pytestmark = pytest.mark.gpu
 ensure_built()
@@ -24,3 +28,60 @@ def test_scales_near_zero(dt, scale):
         out, lse = A.attend(op, dq, dk, dv, ints(cq), ints(ck))
         within(out, ref["out"], "out")
         within(lse, ref["lse"], "lse")
+
+
+# ---------------------------------------------------------------- tokens outside every sequence
+
+OUTSIDE = [
+    # query tokens, offsets, key tokens, offsets, query heads, key heads
+    (300, [10, 200], 260, [0, 50], 2, 1),                    # tile kernel
+    (300, [0, 100, 250], 260, [7, 100, 260], 4, 2),
+    (5, [1, 2, 4], 9000, [3, 4000, 8000], 4, 2),             # split kernel
+    (700, [600, 700], 700, [0, 1], 96, 24),
+    (40, [0, 40], 900, [100, 500], 8, 8),                    # parts of dk and dv in the workspace
+    (30, [0, 0], 20, [0, 20], 2, 2),
+    (6, [0], 7, [0], 2, 2),                                  # no sequences
+    (0, [0, 0], 33, [4, 20], 2, 2),                          # no queries
+]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("case", OUTSIDE, ids=str)
+def test_tokens_outside_every_sequence_get_zeros(case, dt, causal):
+    """Results that the call allocates are those of a row that sees nothing."""
+    tq, cq, tk, ck, hq, hk = case
+    dtype = DTYPES[dt]
+    op = A.mdcn_attention_create(hq, hk, 64, causal)
+    q, k, v = (rand(n, h, 64, seed=s, dtype=dtype) for n, h, s in ((tq, hq, 1), (tk, hk, 2), (tk, hk, 3)))
+    go = rand(tq, hq, 64, seed=4, dtype=dtype)
+    ref = R.attend(q, k, v, cq, ck, None, causal, op.scale, dtype, go)
+    ref = {n: (x[0].masked_fill(x[0].isnan(), -math.inf if n == "lse" else 0.0),
+               x[1].masked_fill(x[1].isnan(), 0.0)) for n, x in ref.items()}
+    dev = [t.cuda() for t in (q, k, v)]
+    go = go.cuda()
+    for _ in range(2):
+        poison()
+        out, lse = A.attend(op, *dev, ints(cq), ints(ck))
+        within(out, ref["out"], "out")
+        within(lse, ref["lse"], "lse")
+        poison()
+        g = A.attend_backward(op, *dev, out, lse, go, ints(cq), ints(ck))
+        for n in "qkv":
+            within(g[n], ref[n], "d" + n)
+
+
+def test_what_the_caller_gave_is_left_outside_the_sequences():
+    op = A.mdcn_attention_create(2, 1, 64, False)
+    q = rand(300, 2, 64, seed=1, dtype=torch.float16).cuda()
+    for cq, ck in (([10, 200], [0, 50]), ([10, 12], [0, 300])):
+        out = torch.full((300, 2, 64), 3.0, dtype=torch.float16, device="cuda")
+        lse = torch.full((2, 300), 5.0, device="cuda")
+        poison()
+        got, own = A.attend(op, q, q[:, :1], q[:, 1:], ints(cq), ints(ck), out=out)
+        assert got is out and (out[:10] == 3).all() and (out[cq[1]:] == 3).all()
+        assert (own[:, :10] == -math.inf).all() and (own[:, cq[1]:] == -math.inf).all()
+        poison()
+        own, got = A.attend(op, q, q[:, :1], q[:, 1:], ints(cq), ints(ck), lse=lse)
+        assert got is lse and (lse[:, :10] == 5).all() and (lse[:, cq[1]:] == 5).all()
+        assert (own[:10] == 0).all() and (own[cq[1]:] == 0).all()
