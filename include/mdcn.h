@@ -397,7 +397,8 @@ mdcn_status mdcn_attend_filled(const mdcn_attention *op, mdcn_dtype dtype, const
  * keys and values that are infinite or NaN reach no gradient; such values in a
  * row of q or grad_out do reach the keys of the whole sequence, hidden ones
  * too.  Sums in fp32, probabilities and score gradients rounded to the inputs'
- * type for the products.  No atomics: repeated calls give the same bits. */
+ * type for the products (fp16: scaled by powers of two first, so that neither
+ * overflows, and small ones keep their bits).  No atomics: repeated calls give the same bits. */
 mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_dtype dtype,
                                                  const int64_t dims[19], size_t *bytes);
 mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,

@@ -29,6 +29,56 @@ constexpr int kRows = 32 * kWaves;
 
 constexpr int kFar = 1 << 30;                 // more than any number of rows
 
+// fp16 holds 2^-24 to 2^16, and probabilities p and score gradients p (go.v - delta)
+// are often outside: among 2^14 keys p is about 2^-14, and go has any size.  Both are
+// scaled by powers of two before they are rounded, which changes nothing else: p to
+// 2^15 p, the score gradients by what takes
+//   |go.v - delta| <= dim max|go| max|v| + max|delta|
+// to at most 2^15.  The maxima are those of the rows that a sum runs over (values that
+// are not finite left out), taken in the first kernel 32 rows at a time.  Cost of it all
+// (16 query and 4 key heads of 128, the training step above): 176 -> 179 us; 64 sequences of
+// 200, eight heads of 64: 63 -> 68.
+template <typename T> constexpr bool kScaled = false;
+template <> constexpr bool kScaled<half_t> = true;
+constexpr int kTop = 15;
+
+// The exponent of the scale for score gradients of at most `bound`.
+__device__ __forceinline__ int scale_exponent(float bound)
+{
+    return bound > 0.0f ? kTop - __builtin_amdgcn_frexp_expf(bound) : 0;
+}
+
+// The largest finite |x| of a row's half that the lane holds.
+template <typename T, int DP> __device__ __forceinline__ float top_of_row(const Frag<T, DP> &f)
+{
+    uint32_t top = 0;
+    auto take = [&](uint32_t w) {
+        const uint32_t lo = w & 0x7fff, hi = w >> 16 & 0x7fff;
+        top = max(top, max(lo < 0x7c00 ? lo : 0, hi < 0x7c00 ? hi : 0));
+    };
+#pragma unroll
+    for (int k = 0; k < Row<T, DP>::STEPS; ++k) {
+        take(f[k].x);
+        take(f[k].y);
+        take(f[k].z);
+        take(f[k].w);
+    }
+    const uint16_t bits = uint16_t(top);
+    half_t v;
+    __builtin_memcpy(&v, &bits, 2);
+    return float(v);
+}
+
+__device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; }
+
+__device__ __forceinline__ float wave_top(float v)
+{
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1)
+        v = fmaxf(v, __shfl_xor(v, m));
+    return v;
+}
+
 // {lse in powers of two, delta} of every (token, head): the diagonal of go.out for
 // 32 rows of a head a wave.  On the matrix cores not for their rate (the reads
 // bound it), but to add in the order in which the other kernels add go.v: a row that
@@ -51,10 +101,27 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
         return;
     }
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
-    const int w = int(blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
-    const int head = w % a.q_heads;
     Span sp;
     int tile;
+    if (kScaled<T> && int(blockIdx.x) >= a.tops_from) {
+        const int w = int((blockIdx.x - a.tops_from) * 4 +
+                          __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
+        const int kv_head = w % a.k_heads;
+        if (!find_tile(a, w / a.k_heads, lane, false,
+                       [](const Span &s) { return (s.lk + 31) / 32; }, sp, tile))
+            return;
+        const int key = tile * 32 + col;
+        Frag<T, DP> v;
+        load_frag<T, DP>(
+            v, key < sp.lk ? reinterpret_cast<const T *>(row_ptr<T>(a.v, sp.k0 + key, kv_head)) : nullptr,
+            a.dim, half);
+        const float top = wave_top(top_of_row<T, DP>(v));
+        if (lane == 0)
+            a.key_tops[int64_t(kv_head) * a.k_tokens + sp.k0 + tile * 32] = top;
+        return;
+    }
+    const int w = int(blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
+    const int head = w % a.q_heads;
     if (!find_tile(a, w / a.q_heads, lane, false, [](const Span &s) { return (s.lq + 31) / 32; },
                    sp, tile))
         return;
@@ -100,7 +167,15 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(AttendArgs a)
         delta = few ? sum : delta;
     }
     if (live && half == (col >> 2 & 1))
-        a.stats[at] = make_float2(lse, delta);
+        a.stats[at] = make_float2(kScaled<T> ? lse - kTop : lse, delta);
+    if constexpr (kScaled<T>) {
+        // (the lane of the other half holds no delta of its row)
+        const bool own = live && half == (col >> 2 & 1);
+        const float top_g = wave_top(top_of_row<T, DP>(g));
+        const float top_d = wave_top(own ? finite_or_0(delta) : 0.0f);
+        if (lane == 0)
+            a.row_tops[head * int64_t(a.q_tokens) + sp.q0 + tile * 32] = make_float2(top_g, top_d);
+    }
 }
 
 template <typename T, int DP, int RW, int KW>
@@ -169,6 +244,20 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     settle(stat.x);
     settle(stat.y);
     const float c = a.scale * kLog2e;
+    float factor = a.scale;
+    if constexpr (kScaled<T>) {
+        // a row's own scale, which goes into its exponent: e^(s - lse) 2^x
+        float top = 0.0f;
+        const int keys = min(block_last + 1, sp.lk);
+        const float *tops = a.key_tops + int64_t(kv_head) * a.k_tokens + sp.k0;
+        for (int j = lane * 32; j < keys; j += 64 * 32)
+            top = fmaxf(top, tops[j]);
+        top = wave_top(top);
+        const int x = scale_exponent(float(a.dim) * top * max_halves(top_of_row<T, DP>(gf)) +
+                                     finite_or_0(stat.y));
+        stat.x += float(kTop - x);
+        factor = ldexpf(a.scale, -x);
+    }
 
     Acc<T, DP> dq;
 #pragma unroll
@@ -258,7 +347,7 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
     }
     if (live)
         store_cols<T, DP>(reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.dq, token, head))),
-                          dq, a.scale, a.dim, half);
+                          dq, factor, a.dim, half);
 }
 
 // One round of a wave on 32 queries and its 32 keys, the instructions in the
@@ -276,7 +365,8 @@ __device__ __forceinline__ void dkv_round(Acc<T, DP> &dk, Acc<T, DP> &dv, float1
                                           const Frag<T, DP> &kf, const Frag<T, DP> &vf,
                                           const char *q_next, const char *g_next,
                                           const char *q_tile, const char *g_tile,
-                                          const float *stats, float c, int first_row, int lane)
+                                          const float *stats, float c, float ds_scale,
+                                          int first_row, int lane)
 {
     using R = Row<T, DP>;
     constexpr int RM = 2 * R::STEPS;                       // row products
@@ -313,7 +403,8 @@ __device__ __forceinline__ void dkv_round(Acc<T, DP> &dk, Acc<T, DP> &dv, float1
             const float lse =
                 acc_row(r, 0) >= first_row - 4 * half ? st[r / 2][2 * r % 4] : INFINITY;
             s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse));
-            dp[r] = s[r] * (dp[r] - st[r / 2][2 * r % 4 + 1]);
+            dp[r] = dp[r] - st[r / 2][2 * r % 4 + 1];
+            dp[r] = s[r] * (kScaled<T> ? dp[r] * ds_scale : dp[r]);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -420,6 +511,23 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
     settle<T, DP>(kf);
     settle<T, DP>(vf);
     const float c = a.scale * kLog2e;
+    float ds_scale = 1.0f, dk_factor = 1.0f, dv_factor = 1.0f;
+    if constexpr (kScaled<T>) {
+        // a key's own scale, beyond that of p
+        float top_g = 0.0f, top_d = 0.0f;
+        for (int i = i_begin + lane; i < i_end; i += 64) {
+            const float2 t = a.row_tops[int64_t(kv_head * group + i / nt) * a.q_tokens + sp.q0 +
+                                        (t0 + i % nt) * 32];
+            top_g = fmaxf(top_g, t.x);
+            top_d = fmaxf(top_d, t.y);
+        }
+        const int x = scale_exponent(float(a.dim) * wave_top(top_g) *
+                                         max_halves(top_of_row<T, DP>(vf)) +
+                                     wave_top(top_d));
+        ds_scale = ldexpf(1.0f, x - kTop);
+        dk_factor = ldexpf(1.0f, -x);
+        dv_factor = ldexpf(1.0f, -kTop);
+    }
 
     Acc<T, DP> dk, dv;
 #pragma unroll
@@ -449,7 +557,7 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
         const float *stats = reinterpret_cast<const float *>(q_tile + 2 * TILE);
         // sees(q, key): key <= q + shift
         dkv_round<T, DP>(dk, dv, s, dp, kf, vf, q_next, q_next + TILE, q_tile, q_tile + TILE, stats,
-                         c, a.causal ? key - shift - t * 32 : -kFar, lane);
+                         c, ds_scale, a.causal ? key - shift - t * 32 : -kFar, lane);
         t = t + 1 < t0 + nt ? t + 1 : t0;
     }
     if (key < sp.k_all) {
@@ -463,14 +571,14 @@ __global__ __launch_bounds__(64 * kWaves) void attend_dkv_kernel(AttendArgs a)
             const int64_t rows = int64_t(a.k_tokens) * a.k_heads;
             float *sum = a.partial + (2 * part * rows + int64_t(kv_head) * a.k_tokens + sp.k0 +
                                       key) * a.dim;
-            store_cols<float, DP>(sum, dk, 1.0f, a.dim, half);
-            store_cols<float, DP>(sum + rows * a.dim, dv, 1.0f, a.dim, half);
+            store_cols<float, DP>(sum, dk, dk_factor, a.dim, half);
+            store_cols<float, DP>(sum + rows * a.dim, dv, dv_factor, a.dim, half);
             return;
         }
         T *dst = reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.dk, sp.k0 + key, kv_head)));
-        store_cols<T, DP>(dst, dk, a.scale, a.dim, half);
+        store_cols<T, DP>(dst, dk, a.scale * dk_factor, a.dim, half);
         dst = reinterpret_cast<T *>(const_cast<char *>(row_ptr<T>(a.dv, sp.k0 + key, kv_head)));
-        store_cols<T, DP>(dst, dv, 1.0f, a.dim, half);
+        store_cols<T, DP>(dst, dv, dv_factor, a.dim, half);
     }
 }
 
@@ -526,12 +634,17 @@ hipError_t launch_shape(AttendArgs a, hipStream_t s)
     const int64_t k_tiles = tiles_of(a.k_tokens, a.batch, kRows) * a.k_heads;
     const int64_t k_blocks = k_tiles * a.splits;
     const int64_t sum_blocks = tiles_of(a.k_tokens, a.batch, kSumRows) * a.k_heads;
-    if (sum_blocks > INT32_MAX || 4 * d_blocks > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
+    if (sum_blocks > INT32_MAX || q_blocks > INT32_MAX || k_blocks > INT32_MAX)
         return hipErrorInvalidValue;
-    a.fill_from = int(d_blocks);
+    a.tops_from = int(d_blocks);
+    const int64_t v_blocks =
+        kScaled<T> ? (tiles_of(a.k_tokens, a.batch, 32) * a.k_heads + 3) / 4 : 0;
+    if (4 * (d_blocks + v_blocks) > INT32_MAX)
+        return hipErrorInvalidValue;
+    a.fill_from = int(d_blocks + v_blocks);
     const int fill = fill_blocks((int64_t(a.q_tokens) * a.q_heads + 2 * int64_t(a.k_tokens) * a.k_heads) *
                                  a.dim * sizeof(T));
-    attend_delta_kernel<T, DP><<<uint32_t(d_blocks + fill), 256, 0, s>>>(a);
+    attend_delta_kernel<T, DP><<<uint32_t(a.fill_from + fill), 256, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k_blocks > 0) {
         attend_dkv_kernel<T, DP><<<uint32_t(k_blocks), 64 * kWaves, 0, s>>>(a);

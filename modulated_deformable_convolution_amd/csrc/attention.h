@@ -58,6 +58,9 @@ struct AttendArgs {
     Heads go, dq, dk, dv;  // backward
     float *lse;            // [q_heads][q_tokens]
     float2 *stats;         // backward: [q_heads][q_tokens], {lse * log2(e), sum of go * out}
+    // backward in fp16, at every 32nd row of a sequence: the largest of 32 rows
+    float2 *row_tops;      // [q_heads][q_tokens], {|go|, |sum of go * out|}
+    float *key_tops;       // [k_heads][k_tokens], |v|
     const int32_t *cu_q, *cu_k, *used_k;
     int32_t batch, q_tokens, k_tokens;
     int32_t q_heads, k_heads, dim, causal;
@@ -67,6 +70,7 @@ struct AttendArgs {
     int32_t splits;        // backward: workgroups that share a tile of keys
     int32_t fill;          // forward: kFillOut, kFillLse
     int32_t fill_from;     // first of the workgroups that fill (see outside_rows)
+    int32_t tops_from;     // backward in fp16: first of the workgroups that take key_tops
     float *partial;        // sums that several workgroups leave for one result
 };
 

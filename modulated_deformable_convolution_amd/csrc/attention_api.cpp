@@ -268,10 +268,19 @@ mdcn_status check_attend_view(View &v)
     return MDCN_OK;
 }
 
-// The backward's row statistics, up to the next 256 bytes.
+size_t up_256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The backward's row statistics, and the maxima that only fp16 has, up to the next 256 bytes.
 size_t stats_bytes(const AttendArgs &a)
 {
-    return (size_t(a.q_heads) * a.q_tokens * sizeof(float2) + 255) / 256 * 256;
+    return up_256(size_t(a.q_heads) * a.q_tokens * sizeof(float2));
+}
+
+size_t tops_bytes(mdcn_dtype dtype, const AttendArgs &a)
+{
+    return dtype == MDCN_F16
+               ? stats_bytes(a) + up_256(size_t(a.k_heads) * a.k_tokens * sizeof(float))
+               : 0;
 }
 
 }  // namespace
@@ -617,7 +626,7 @@ mdcn_status mdcn_attend_backward_workspace_bytes(const mdcn_attention *op, mdcn_
     if (st != MDCN_OK)
         return st;
     const int splits = mdcn::attend_backward_splits(a);
-    *bytes = stats_bytes(a) + 256;
+    *bytes = stats_bytes(a) + tops_bytes(dtype, a) + 256;
     if (splits > 1)
         *bytes += size_t(splits) * 2 * a.k_tokens * a.k_heads * a.dim * sizeof(float);
     return MDCN_OK;
@@ -698,7 +707,10 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
         a.dv = g[2].h;
         a.lse = const_cast<float *>(lse);
         a.stats = static_cast<float2 *>(align_up(workspace));
-        a.partial = reinterpret_cast<float *>(reinterpret_cast<char *>(a.stats) + stats_bytes(a));
+        char *const behind = reinterpret_cast<char *>(a.stats) + stats_bytes(a);
+        a.row_tops = reinterpret_cast<float2 *>(behind);
+        a.key_tops = reinterpret_cast<float *>(behind + stats_bytes(a));
+        a.partial = reinterpret_cast<float *>(behind + tops_bytes(dtype, a));
         a.splits = mdcn::attend_backward_splits(a);
         a.cu_q = cu_q;
         a.cu_k = cu_k;

@@ -85,3 +85,68 @@ def test_what_the_caller_gave_is_left_outside_the_sequences():
         own, got = A.attend(op, q, q[:, :1], q[:, 1:], ints(cq), ints(ck), lse=lse)
         assert got is lse and (lse[:, :10] == 5).all() and (lse[:, cq[1]:] == 5).all()
         assert (own[:10] == 0).all() and (own[cq[1]:] == 0).all()
+
+
+# ---------------------------------------------------------------- fp16 gradients
+
+def half_case(q_scale, k_scale, v_scale, go_scale, keys, seed=0):
+    rows, hq, hk, dim = 64, 2, 1, 64
+    t = [rand(n, h, dim, seed=seed + i, dtype=torch.float16, scale=s) for i, (n, h, s) in
+         enumerate(((rows, hq, q_scale), (keys, hk, k_scale), (keys, hk, v_scale),
+                    (rows, hq, go_scale)))]
+    op = A.mdcn_attention_create(hq, hk, dim, False)
+    want = R.attend(*t[:3], [0, rows], [0, keys], None, False, op.scale, torch.float16, t[3])
+    dev = [x.cuda() for x in t]
+    c = ints([0, rows]), ints([0, keys])
+    out, lse = A.attend(op, *dev[:3], *c)
+    return A.attend_backward(op, *dev[:3], out, lse, dev[3], *c), want
+
+
+def rounding_error(got, exact):
+    """The error in units of what rounding the exact values to fp16 leaves."""
+    last = (exact.to(torch.float16).double() - exact).norm()
+    return float((got.double().cpu() - exact).norm() / last)
+
+
+@pytest.mark.parametrize("name,scales", [
+    # few queries and many keys: p and p (go v - delta) lie far below fp16's normal numbers (6e-5),
+    # the gradients within them
+    ("q", (2.0 ** -6, 2.0 ** 6, 1.0, 2.0 ** -9)), ("q", (2.0 ** -8, 2.0 ** 8, 1.0, 2.0 ** -13)),
+    ("k", (2.0 ** 7, 2.0 ** -7, 1.0, 2.0 ** -4)), ("v", (1.0, 1.0, 1.0, 2.0 ** 5)),
+])
+def test_half_gradients_of_small_score_gradients(name, scales):
+    """As test_score_gradients_carry_two_roundings: two roundings of one size, sqrt(2) = 1.42
+    times one alone, and 0.08 for the rounding of out, wherever the factors lie."""
+    got, want = half_case(*scales, keys=16384 if name != "v" else 65536)
+    assert want[name][0].abs().median() > 2.0 ** -13
+    assert rounding_error(got[name], want[name][0]) < 1.5
+
+
+@pytest.mark.parametrize("name,scales,keys", [
+    # go v - delta passes 65504 where the sums' other factor is small
+    ("q", (2.0 ** 6, 2.0 ** -6, 2.0 ** 4, 2.0 ** 13), 300),
+    ("k", (2.0 ** -7, 2.0 ** 7, 2.0 ** 3, 2.0 ** 13), 300),
+    ("q", (2.0 ** 9, 2.0 ** -9, 2.0 ** 8, 2.0 ** 9), 300),
+])
+def test_half_gradients_of_large_score_gradients(name, scales, keys):
+    got, want = half_case(*scales, keys=keys)
+    assert want[name][0].abs().max() < 60000
+    assert rounding_error(got[name], want[name][0]) < 1.5
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gradients_of_rows_without_gradient_and_of_zeros(dt):
+    """All-zero gradients, zero values, single rows that are not zero."""
+    dtype = DTYPES[dt]
+    op, q, k, v, dq, dk, dv, cq, ck = attend_case(([200, 40], None, 4, 2, 64, True), dtype)
+    go = torch.zeros_like(q)
+    for rows in ([], [3], [0, 199, 239]):
+        for r in rows:
+            go[r] = rand(4, 64, seed=r, dtype=dtype)
+        ref = R.attend(q, k, v, cq, ck, None, True, op.scale, dtype, go)
+        out, lse = A.attend(op, dq, dk, dv, ints(cq), ints(ck))
+        g = A.attend_backward(op, dq, dk, dv, out, lse, go.cuda(), ints(cq), ints(ck))
+        for n in "qkv":
+            within(g[n], ref[n], "d" + n)
+        if not rows:
+            assert all((g[n] == 0).all() for n in "qkv")
