@@ -215,7 +215,7 @@ __global__ __launch_bounds__(64 * RW * KW, (waves_per_simd<T, DP, KW>())) void a
             l == 0.0f ? 0.0f : 1.0f / l, a.dim, half);
         if (half == 0)
             a.lse[int64_t(head) * a.q_tokens + sp.q0 + row] =
-                l == 0.0f ? -INFINITY : fmaf(sm.m, a.scale, logf(l));
+                l == 0.0f ? -INFINITY : row_lse<T>(sm.m, l, a.scale);
     }
 }
 

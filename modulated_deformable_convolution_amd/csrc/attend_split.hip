@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256) void attend_split_kernel(AttendArgs a)
                                 from_f32<T>(sum == 0.0f ? 0.0f : o / sum);
                         if (d == 0)
                             a.lse[int64_t(qh) * a.q_tokens + sp.q0 + qr] =
-                                sum == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(sum));
+                                sum == 0.0f ? -INFINITY : row_lse<T>(m, sum, a.scale);
                     } else {
                         slot[r * PART + 2 + d] = o;
                         if (d == 0) {
@@ -403,7 +403,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
                 from_f32<T>(total == 0.0f ? 0.0f : out / total);
             if (threadIdx.x == 0)
                 a.lse[int64_t(head) * a.q_tokens + token] =
-                    total == 0.0f ? -INFINITY : fmaf(top, a.scale, logf(total));
+                    total == 0.0f ? -INFINITY : row_lse<T>(top, total, a.scale);
         }
         return;
     }

@@ -395,6 +395,19 @@ constexpr float kRaise = 8.0f;
 // however small the scale is.
 __device__ __forceinline__ float raise_margin(float c) { return fminf(kRaise / c, 3.0e38f); }
 
+// fp16: exponentials are 2^7 e^(scale (s - m)), up to 2^15, where they are rounded for the
+// product with v, so that weights down to 2^-21 are normal numbers there: thousands of
+// keys of little weight may outweigh one whose value is small.  The sums have the factor
+// too, so only lse has to know of it.
+template <typename T> inline constexpr int kLift = 0;
+template <> inline constexpr int kLift<half_t> = 7;
+
+// log(sum of exponentials) of a row
+template <typename T> __device__ __forceinline__ float row_lse(float m, float l, float scale)
+{
+    return fmaf(m, scale, logf(kLift<T> ? l * (1.0f / (1 << kLift<T>)) : l));
+}
+
 // Softmax state of one query row (both halves of the wave hold the same
 // maximum; the sums are those of the half's own keys).
 template <typename T, int DP> struct Softmax {
@@ -439,7 +452,7 @@ template <typename T, int DP> struct Softmax {
             l *= f;
             m = up;
         }
-        return m == -INFINITY ? 0.0f : sizeof(T) == 4 ? m : m * c;
+        return m == -INFINITY ? 0.0f : sizeof(T) == 4 ? m : fmaf(m, c, float(-kLift<T>));
     }
 
     // Turns scores into e^(scale (s - m)) and adds them up.  16-bit types: one fma,
@@ -513,7 +526,7 @@ __device__ __attribute__((noinline)) void recompute(float16v *o, const uint4 *q,
         const float dp = g ? half_dot<T, DP>(g, vr, dim, half) : 0.0f;
         if (j > t->last)
             continue;
-        float w = exp2f(fmaf(s, t->c, g ? -t->m : -t->m * t->c));
+        float w = exp2f(fmaf(s, t->c, g ? -t->m : fmaf(-t->m, t->c, float(kLift<T>))));
         if (g)
             w *= dp - t->delta;
         const T *row = g ? kr : vr;

@@ -150,3 +150,30 @@ def test_gradients_of_rows_without_gradient_and_of_zeros(dt):
             within(g[n], ref[n], "d" + n)
         if not rows:
             assert all((g[n] == 0).all() for n in "qkv")
+
+
+# ---------------------------------------------------------------- small probabilities
+
+@pytest.mark.parametrize("sink", [0.0, 0.4, 1.0])
+@pytest.mark.parametrize("heads,rows,n", [(1, 1, 65536), (16, 600, 4096), (32, 1200, 4096)])
+@pytest.mark.parametrize("power", [19.3, 21.7, 23.2])
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_many_keys_of_little_weight(dt, power, heads, rows, n, sink):
+    """One key of weight 1 whose value is 0, and all others of 2^-power with the value 1.  Off by
+    the rounding of the weights, scaled by 2^7 in fp16 (half a step 2^-32 below its normal
+    numbers), that of the result, and fp32 sums over all keys."""
+    dtype = DTYPES[dt]
+    op = A.mdcn_attention_create(heads, heads, 8, False, scale=1.0)
+    q, k, v = torch.zeros(rows, heads, 8), torch.zeros(n, heads, 8), torch.ones(n, heads, 8)
+    q[..., 0] = 1.0
+    at = int(sink * (n - 1))
+    k[at, :, 0] = power * math.log(2.0)
+    v[at] = 0.0
+    q, k, v = (t.to(dtype).cuda() for t in (q, k, v))
+    out, lse = A.attend(op, q, k, v, ints([0, rows]), ints([0, n]))
+    score = float(k[at, 0, 0])
+    mass = (n - 1) * math.exp(-score)
+    want, least = mass / (1 + mass), 2.0 ** -32 if dtype == torch.float16 else 0.0
+    bound = want * (2 * R.unit(dtype) + 2 * n * R.E32) + n * least
+    assert float((out.double() - want).abs().max()) <= bound
+    assert float((lse.double() - score - math.log1p(mass)).abs().max()) <= n * R.E32
