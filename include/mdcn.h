@@ -408,6 +408,19 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
                                  const int32_t *used_k, void *grad_q, void *grad_k, void *grad_v,
                                  void *workspace, size_t workspace_bytes, void *stream);
 
+/* One line on the kernels that a call of these sizes runs, written NUL-terminated into
+ * buf[len].  Host only; errors as the calls'.
+ *   mdcn_describe_rotate: dims tokens, q heads, k heads, for tensors aligned to 16 bytes;
+ *   values of a vector, lanes of a head, rounds of heads of a wave, waves of a token,
+ *   workgroups of mdcn_norm_rotate_backward.
+ *   mdcn_describe_attend: dims batch, query tokens, key tokens; the split kernel's keys of a
+ *   unit and workgroups, or the tile kernel's queries of a workgroup and waves that share
+ *   their keys; backward: these for grad_q, and the workgroups that share a tile of keys. */
+mdcn_status mdcn_describe_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const int64_t dims[3],
+                                 char *buf, size_t len);
+mdcn_status mdcn_describe_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[3],
+                                 int32_t backward, char *buf, size_t len);
+
 /* ---- tracing: per-kernel device time, for profiling --------------------- */
 
 typedef struct mdcn_trace mdcn_trace;

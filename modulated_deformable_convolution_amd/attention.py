@@ -394,3 +394,24 @@ def attend_backward(op: Attention, q, k, v, out, lse, grad_out, cu_q, cu_k, used
     if st:
         _m._check(st, where)
     return {"q": dq, "k": dk, "v": dv}
+
+
+# ---------------------------------------------------------------- what a call runs
+
+def describe_rotate(op: Rotary, dtype, tokens: int, q_heads: int, k_heads: int) -> str:
+    """One line on the shape of rotate's and norm_rotate's kernels (mdcn_describe_rotate)."""
+    buf = ctypes.create_string_buffer(256)
+    _m._check(_m._lib.mdcn_describe_rotate(op.handle, _m.dtype_code(dtype),
+                                           (_i64 * 3)(tokens, q_heads, k_heads), buf, 256),
+              "describe_rotate")
+    return buf.value.decode()
+
+
+def describe_attend(op: Attention, dtype, batch: int, q_tokens: int, k_tokens: int,
+                    backward: bool = False) -> str:
+    """One line on attend's kernels, or attend_backward's (mdcn_describe_attend)."""
+    buf = ctypes.create_string_buffer(256)
+    _m._check(_m._lib.mdcn_describe_attend(op.handle, _m.dtype_code(dtype),
+                                           (_i64 * 3)(batch, q_tokens, k_tokens), int(backward),
+                                           buf, 256), "describe_attend")
+    return buf.value.decode()

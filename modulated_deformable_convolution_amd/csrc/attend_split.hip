@@ -492,14 +492,19 @@ size_t attend_split_bytes(mdcn_dtype dtype, int dim)
            sizeof(float);
 }
 
-hipError_t launch_attend_split(mdcn_dtype dtype, AttendArgs a, hipStream_t s)
+int attend_split_unit_shift(const AttendArgs &a)
 {
     // Units of a batch: at most (row tiles) x (key heads) x (units of all keys).
     const double tiles = double(a.q_tokens) * (a.q_heads / a.k_heads) / kTileRows + a.batch;
-    a.unit_shift = 0;
-    while (tiles * a.k_heads * (double(a.k_tokens >> (5 + a.unit_shift)) + 1) > 1e9 &&
-           a.unit_shift < 16)
-        ++a.unit_shift;
+    int shift = 0;
+    while (tiles * a.k_heads * (double(a.k_tokens >> (5 + shift)) + 1) > 1e9 && shift < 16)
+        ++shift;
+    return shift;
+}
+
+hipError_t launch_attend_split(mdcn_dtype dtype, AttendArgs a, hipStream_t s)
+{
+    a.unit_shift = attend_split_unit_shift(a);
     switch (dtype) {
     case MDCN_F32:
         return launch_dim<float>(a, s);

@@ -48,6 +48,12 @@ enum class RotaryKind { Rotate, NormRotate, NormRotateBackward };
 
 // Blocks of the backward, one row of `partial` each.
 int rotary_backward_blocks(int64_t tokens);
+// How a call is laid out: values of a vector, lanes of a head, rounds of heads that a wave
+// takes and waves that share a token's.
+struct RotaryShape {
+    int width, lanes, rounds, waves;
+};
+RotaryShape rotary_shape(RotaryKind kind, mdcn_dtype dtype, const RotaryArgs &a);
 hipError_t launch_rotary(RotaryKind kind, mdcn_dtype dtype, const RotaryArgs &a, hipStream_t s);
 // Sums partial's rows into the two gain gradients.
 hipError_t launch_gain_sum(mdcn_dtype dtype, const RotaryArgs &a, void *dq_gain, void *dk_gain,
@@ -87,6 +93,7 @@ bool attend_prefers_split(mdcn_dtype dtype, const AttendArgs &a);
 // Workgroups of the split kernel and the bytes of `partial` they need.
 int attend_split_workers(mdcn_dtype dtype, int dim);
 size_t attend_split_bytes(mdcn_dtype dtype, int dim);
+int attend_split_unit_shift(const AttendArgs &a);
 hipError_t launch_attend_split(mdcn_dtype dtype, AttendArgs a, hipStream_t s);
 // Workgroups that share the queries of a tile of keys; more than one need
 // splits * 2 * k_tokens * k_heads * dim floats of `partial`.

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <cmath>
+#include <cstdio>
 #include <new>
 #include <numeric>
 
@@ -719,6 +720,49 @@ mdcn_status mdcn_attend_backward(const mdcn_attention *op, mdcn_dtype dtype,
     } catch (...) {
         return MDCN_E_INTERNAL;
     }
+}
+
+mdcn_status mdcn_describe_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const int64_t dims[3],
+                                 char *buf, size_t len)
+{
+    if (!op || !dims || !buf || len == 0)
+        return MDCN_E_NULL;
+    RotaryArgs a = {};
+    const int64_t all[4] = {dims[0], dims[1], dims[2], dims[0]};
+    const int32_t position = 0;                  // only looked at for being there
+    const mdcn_status st = rotary_args(op, dtype, all, &position, &a);
+    if (st != MDCN_OK)
+        return st;
+    if (a.tokens == 0) {
+        std::snprintf(buf, len, "nothing to do");
+        return MDCN_OK;
+    }
+    const mdcn::RotaryShape s = mdcn::rotary_shape(RotaryKind::Rotate, dtype, a);
+    std::snprintf(buf, len, "width=%d lanes=%d rounds=%d waves_per_token=%d backward_blocks=%d",
+                  s.width, s.lanes, s.rounds, s.waves, mdcn::rotary_backward_blocks(a.tokens));
+    return MDCN_OK;
+}
+
+mdcn_status mdcn_describe_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[3],
+                                 int32_t backward, char *buf, size_t len)
+{
+    if (!buf || len == 0)
+        return MDCN_E_NULL;
+    AttendArgs a = {};
+    const mdcn_status st = attend_dims(op, dtype, dims, &a);
+    if (st != MDCN_OK)
+        return st;
+    const int waves = mdcn::attend_key_waves(dtype, a), rows = waves == 1 ? 128 : 64;
+    if (backward)
+        std::snprintf(buf, len, "rows=%d key_waves=%d parts=%d", rows, waves,
+                      mdcn::attend_backward_splits(a));
+    else if (mdcn::attend_prefers_split(dtype, a))
+        std::snprintf(buf, len, "split unit=%d workgroups=%d",
+                      32 << mdcn::attend_split_unit_shift(a),
+                      mdcn::attend_split_workers(dtype, a.dim));
+    else
+        std::snprintf(buf, len, "tile rows=%d key_waves=%d", rows, waves);
+    return MDCN_OK;
 }
 
 }  // extern "C"

@@ -509,6 +509,29 @@ int vector_width(const RotaryArgs &a, RotaryKind kind, size_t elem)
     return 1;
 }
 
+// Lanes of a head of `units` units.
+int lanes_of(int units)
+{
+    int group = 1;
+    while (group < units && group < 64)
+        group *= 2;
+    return group;
+}
+
+// Rounds of a wave and waves of a token.  A few tokens (a decoding step) are spread
+// over the chip by giving each wave fewer of a token's heads; enough tokens to fill it
+// take all of a token's heads in one wave, which computes the angles once.
+void share_token(const RotaryArgs &a, int group, int &per_wave, int &waves)
+{
+    const int slots = 64 / group;
+    const int rounds = (a.q_heads + a.k_heads + slots - 1) / slots;
+    const int64_t want = 4096;                     // waves that keep the chip busy
+    int split = int((want + a.tokens - 1) / a.tokens);
+    split = split < 1 ? 1 : split > rounds ? rounds : split;
+    per_wave = (rounds + split - 1) / split;
+    waves = (rounds + per_wave - 1) / per_wave;
+}
+
 template <typename T, int V, int U, bool ADJ, bool ALL>
 hipError_t launch_units(RotaryKind kind, const RotaryArgs &a, int group, int units, hipStream_t s)
 {
@@ -517,16 +540,8 @@ hipError_t launch_units(RotaryKind kind, const RotaryArgs &a, int group, int uni
             <<<rotary_backward_blocks(a.tokens), kThreads, 0, s>>>(a, group, units);
         return hipGetLastError();
     }
-    const int slots = 64 / group;
-    const int rounds = (a.q_heads + a.k_heads + slots - 1) / slots;
-    // A few tokens (a decoding step) are spread over the chip by giving each
-    // wave fewer of a token's heads; enough tokens to fill it take all of a
-    // token's heads in one wave, which computes the angles once.
-    const int64_t want = 4096;                     // waves that keep the chip busy
-    int split = int((want + a.tokens - 1) / a.tokens);
-    split = split < 1 ? 1 : split > rounds ? rounds : split;
-    const int per_wave = (rounds + split - 1) / split;
-    const int waves = (rounds + per_wave - 1) / per_wave;
+    int per_wave, waves;
+    share_token(a, group, per_wave, waves);
     const int64_t blocks = (a.tokens * waves + kWaves - 1) / kWaves;
     if (blocks > INT32_MAX)
         return hipErrorInvalidValue;
@@ -554,10 +569,7 @@ hipError_t launch_turns(RotaryKind kind, const RotaryArgs &a, int group, int uni
 template <typename T, int V>
 hipError_t launch_width(RotaryKind kind, const RotaryArgs &a, hipStream_t s)
 {
-    const int units = a.dim / (2 * V);
-    int group = 1;
-    while (group < units && group < 64)
-        group *= 2;
+    const int units = a.dim / (2 * V), group = lanes_of(units);
     if (units <= 64)
         return launch_turns<T, V, 1>(kind, a, group, units, s);
     if constexpr (V == 1)                           // up to 128 units of single pairs
@@ -583,6 +595,15 @@ hipError_t launch_type(RotaryKind kind, const RotaryArgs &a, hipStream_t s)
 }
 
 }  // namespace
+
+RotaryShape rotary_shape(RotaryKind kind, mdcn_dtype dtype, const RotaryArgs &a)
+{
+    RotaryShape s;
+    s.width = vector_width(a, kind, dtype == MDCN_F32 ? 4 : 2);
+    s.lanes = lanes_of(a.dim / (2 * s.width));
+    share_token(a, s.lanes, s.rounds, s.waves);
+    return s;
+}
 
 int rotary_backward_blocks(int64_t tokens)
 {

@@ -54,7 +54,8 @@ EXPORTED = [
     "mdcn_rotary_create", "mdcn_rotary_destroy", "mdcn_rotate", "mdcn_norm_rotate",
     "mdcn_norm_rotate_backward_workspace_bytes", "mdcn_norm_rotate_backward",
     "mdcn_attention_create", "mdcn_attention_destroy", "mdcn_attend_workspace_bytes",
-    "mdcn_attend", "mdcn_attend_filled", "mdcn_attend_backward_workspace_bytes", "mdcn_attend_backward",
+    "mdcn_attend", "mdcn_attend_filled", "mdcn_attend_backward_workspace_bytes",
+    "mdcn_attend_backward", "mdcn_describe_rotate", "mdcn_describe_attend",
 ]
 
 # bytes of the device array mdcn_forward_noalloc works in (include/mdcn.h)
@@ -129,6 +130,10 @@ def _bind(lib):
         "mdcn_attend_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
         "mdcn_attend": ([_vp, ctypes.c_int, _i64p] + [_vp] * 9 + [ctypes.c_size_t, _vp],
                         ctypes.c_int),
+        "mdcn_describe_rotate": ([_vp, ctypes.c_int, _i64p, ctypes.c_char_p, ctypes.c_size_t],
+                                 ctypes.c_int),
+        "mdcn_describe_attend": ([_vp, ctypes.c_int, _i64p, ctypes.c_int32, ctypes.c_char_p,
+                                  ctypes.c_size_t], ctypes.c_int),
         "mdcn_attend_filled": ([_vp, ctypes.c_int, _i64p] + [_vp] * 6 + [ctypes.c_int32] +
                                [_vp] * 3 + [ctypes.c_size_t, _vp], ctypes.c_int),
         "mdcn_attend_backward_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),

@@ -100,3 +100,18 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     with pytest.raises(mdcn.MdcnError) as e:
         A._check_current("attend", 1)
     assert e.value.status == mdcn.MDCN_E_DEVICE
+
+
+def test_descriptions():
+    op, rot = A.mdcn_attention_create(32, 8, 128, True), A.mdcn_rotary_create(128, [64])
+    assert A.describe_attend(op, torch.bfloat16, 4, 4096, 4096) == "tile rows=128 key_waves=1"
+    assert A.describe_attend(op, torch.bfloat16, 48, 48, 48 * 8192).startswith("split unit=32 ")
+    assert A.describe_rotate(rot, torch.float16, 1, 32, 8) == \
+        "width=8 lanes=8 rounds=1 waves_per_token=5 backward_blocks=1"
+    assert A.describe_rotate(rot, torch.float32, 0, 32, 8) == "nothing to do"
+    for call in (lambda: A.describe_attend(op, torch.float16, -1, 1, 1),
+                 lambda: A.describe_attend(op, torch.float64, 1, 1, 1),
+                 lambda: A.describe_rotate(rot, torch.float16, -1, 1, 1),
+                 lambda: A.describe_rotate(rot, torch.float16, 1, 0, 0)):
+        with pytest.raises(mdcn.MdcnError):
+            call()
