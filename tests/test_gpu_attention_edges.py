@@ -7,7 +7,7 @@ import torch
 import attention_reference as R
 from helpers import ensure_built
 from modulated_deformable_convolution_amd import attention as A
-from test_gpu_attention import DTYPES, attend_case, ints, rand, within
+from test_gpu_attention import DTYPES, attend_case, cu, ints, rand, within
 from test_gpu_rotary_edges import poison
 
 pytestmark = pytest.mark.gpu
@@ -177,3 +177,61 @@ def test_many_keys_of_little_weight(dt, power, heads, rows, n, sink):
     bound = want * (2 * R.unit(dtype) + 2 * n * R.E32) + n * least
     assert float((out.double() - want).abs().max()) <= bound
     assert float((lse.double() - score - math.log1p(mass)).abs().max()) <= n * R.E32
+
+
+# ---------------------------------------------------------------- layouts
+
+def laid_out(x, how):
+    """x [tokens, heads, dim] on the GPU in a layout of its own."""
+    n, h, d = x.shape
+    pad = 8
+    if how == "heads first":
+        return x.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+    if how == "wide rows":
+        w = torch.full((n, h + 3, d + pad), math.nan, dtype=x.dtype, device="cuda")
+        v = w[:, 1:h + 1, :d]
+    elif how == "interleaved":
+        w = torch.full((n, h, 3, d), math.nan, dtype=x.dtype, device="cuda")
+        v = w[:, :, 1]
+    elif how == "every other token":
+        w = torch.full((n, 2, h, d), math.nan, dtype=x.dtype, device="cuda")
+        v = w[:, 0]
+    else:                                                # heads first, in rows of their own
+        w = torch.full((h, n + 2, d + 2 * pad), math.nan, dtype=x.dtype, device="cuda")
+        v = w[:, :n, :d].transpose(0, 1)
+    v.copy_(x)
+    return v
+
+
+LAYOUTS = ["heads first", "wide rows", "interleaved", "every other token", "heads first, padded"]
+
+
+@pytest.mark.parametrize("turn", range(5))
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("case", [
+    (([150, 3, 40], [170, 60, 40], 4, 2, 96, True), None),
+    (([150, 3, 40], [170, 60, 40], 4, 2, 80, False), [170, 33, 0]),
+    (([600], [700], 2, 2, 120, True), None),                 # four waves to the keys
+    (([130, 65, 1, 100], [130, 75, 1, 100], 96, 24, 40, True), None),
+    (([2, 1], [2500, 1300], 8, 2, 96, True), [2500, 1000]),  # split kernel
+    (([1, 1], [2500, 1300], 8, 2, 120, True), [2001, 0]),
+], ids=str)
+def test_layouts(case, dt, turn):
+    """Queries, keys, values, outputs and gradients with strides of their own."""
+    (ql, kl, hq, hk, dim, causal), used = case
+    dtype = DTYPES[dt]
+    q, go = (rand(sum(ql), hq, dim, seed=s, dtype=dtype) for s in (1, 2))
+    k, v = (rand(sum(kl), hk, dim, seed=s, dtype=dtype) for s in (3, 4))
+    op = A.mdcn_attention_create(hq, hk, dim, causal)
+    cq, ck = cu(ql), cu(kl)
+    ref = R.attend(q, k, v, cq, ck, used, causal, op.scale, dtype, go)
+    how = LAYOUTS[turn:] + LAYOUTS[:turn]
+    d = [laid_out(x, h) for x, h in zip((q, k, v, torch.zeros_like(q), go), how)]
+    more = dict(used_k=None if used is None else ints(used))
+    out, lse = A.attend(op, *d[:3], ints(cq), ints(ck), out=d[3], **more)
+    assert out is d[3]
+    within(out, ref["out"], "out")
+    within(lse, ref["lse"], "lse")
+    g = A.attend_backward(op, *d[:3], out, lse, d[4], ints(cq), ints(ck), **more)
+    for n in "qkv":
+        within(g[n], ref[n], "d" + n)
