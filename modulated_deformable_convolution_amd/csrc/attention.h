@@ -63,7 +63,8 @@ struct AttendArgs {
     Heads q, k, v, out;    // out: output of the forward, input of the backward
     Heads go, dq, dk, dv;  // backward
     float *lse;            // [q_heads][q_tokens]
-    float2 *stats;         // backward: [q_heads][q_tokens], {lse * log2(e), sum of go * out}
+    // backward: [q_heads][q_tokens], {lse * log2(e) (fp16: 15 less), sum of go * out}
+    float2 *stats;
     // backward in fp16, at every 32nd row of a sequence: the largest of 32 rows
     float2 *row_tops;      // [q_heads][q_tokens], {|go|, |sum of go * out|}
     float *key_tops;       // [k_heads][k_tokens], |v|

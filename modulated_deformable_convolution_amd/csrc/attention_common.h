@@ -28,7 +28,6 @@
 namespace mdcn {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short short4v __attribute__((ext_vector_type(4)));
@@ -148,8 +147,10 @@ template <typename T, int DP, int ROWS, int WAVES> struct Stager {
         }
     }
 
-    // Offset of channels past dim: out of range whatever shift is added (a
-    // tile's offsets and shifts are below 2^30).
+    // Offset of channels past dim: out of range whatever shift is added.  A tile has at
+    // most 256 rows of 2^23 bytes (fp32: 64 of 2^24), so a row's offset and the size of a
+    // shift are at most 255 * 2^23 < 2^31: sums of this and a shift stay below 2^32 and
+    // at least 2^23 above the second tensor's rows.
     static constexpr uint32_t kOutside = 0x80000000u;
 };
 
