@@ -16,12 +16,12 @@
 // keys at 128 channels: 32 MFMAs of 32 cycles, 32 exponentials and ~150 other
 // vector instructions), two waves a SIMD, and by the card's power.  One MI355X,
 // bf16, 32 query and 8 key heads of 128: sequences of 4096 to 1 tokens, causal,
-// 222 us (840 TFLOP/s of the visible pairs), 4096 x 4096 full 282 us (980); zeros
-// instead of random values 16384 x 4096 1130 against 840, as a large matrix
-// product does (1660 against 1230).  Not kept, with no gain: the next
-// tile's scores computed among this one's exponentials, instruction by
-// instruction; wave priorities; eight waves of 256 queries (6% slower); heads
-// dealt over the XCDs otherwise.
+// 223 to 227 us among other work (830 TFLOP/s of the visible pairs), 250 in a row;
+// 4096 x 4096 full 283 us (970), 16384 x 4096 1035 (1063), with zeros in place of
+// random values 226 and 851, as a large matrix product does (769 against 608).  Not kept,
+// with no gain: the next tile's scores computed among this one's exponentials,
+// instruction by instruction; wave priorities; eight waves of 256 queries (6% slower);
+// heads dealt over the XCDs otherwise.
 #include "attention_common.h"
 
 namespace mdcn {

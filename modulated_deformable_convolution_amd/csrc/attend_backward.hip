@@ -14,8 +14,8 @@
 // every run, one rounding of each gradient.
 //
 // One MI355X, bf16, 16 query and 4 key heads of 128, 4096 x 4096 full: dk and dv
-// 377 us (730 TFLOP/s of its four products), dq 203 us (1020 of its three).
-// Sequences of 2048 to 1 tokens, causal: 13 + 90 + 13 + 66 us, where the
+// 320 us (860 TFLOP/s of its four products), dq 188 us (1100 of its three).
+// Sequences of 2048 to 1 tokens, causal: 14 + 90 + 13 + 67 us, where the
 // longest rows of tiles and the start of a workgroup (about 8 us) bound it: 592
 // workgroups cannot be spread evenly.
 #include "attention_common.h"

@@ -14,8 +14,8 @@
 // unscaled outputs in fp32) go to the workspace and a second kernel joins them.
 //
 // One MI355X, bf16, 32 query and 8 key heads of 128: 48 caches of 1 to 16384
-// tokens 268 us (1.6 GB, 6.0 TB/s; a copy's reads and writes reach 4.8) and 8 us
-// to join; one cache of 4097 tokens 9.8 us and 5 us, round trips to memory.
+// tokens 263 to 273 us (1.6 GB, 6.0 TB/s; a copy's reads and writes reach 4.8) and 8 us
+// to join; one cache of 4097 tokens 11 us and 5 us, round trips to memory.
 #include <algorithm>
 #include <cmath>
 

@@ -22,11 +22,11 @@
 // vector; V is the widest of 8, 4, 2, 1 that divides the pairs, the unturned
 // rest, and all strides and addresses.  Bound by memory: one read and one write
 // of each value (backward: two reads, one write), the next heads read while
-// these are turned.  One MI355X: 51201 tokens of 20 heads of 128 in bf16 100 us
-// (5.2 TB/s; a large copy reaches 4.8); norm and rotation of 16000 tokens of 40
-// heads 68 us (4.8 TB/s); 8193 tokens of 20 heads of 96 of which 36 pairs turn
-// (V = 4, 12 of 16 lanes) forward 19 us (3.3 TB/s), backward 31 us (3.0 TB/s)
-// and 4.5 us for the gains' sums.  With each lane's angles computed for itself
+// these are turned.  One MI355X: 51201 tokens of 20 heads of 128 in bf16 99 us
+// (5.3 TB/s; a large copy reaches 4.8), fp32 198 us (5.3); norm and rotation of 16000
+// tokens of 40 heads 68 us (4.8 TB/s), fp32 132 us (5.0); 8193 tokens of 20 heads of 96
+// of which 36 pairs turn (V = 4, 12 of 16 lanes) forward 20 us (3.1 TB/s), backward
+// 32 us (3.0 TB/s) and 4 us for the gains' sums.  With each lane's angles computed for itself
 // and no rounds read ahead the first took 150 us.
 #include "attention.h"
 #include "device_common.h"
