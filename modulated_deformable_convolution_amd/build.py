@@ -25,7 +25,7 @@ SOURCES = ["plan.cpp", "api.cpp", "prep.hip", "gather.hip", "gemm.hip", "depthwi
            "attention_api.cpp", "rotary.hip", "attend.hip", "attend_split.hip",
            "attend_backward.hip"]
 HEADERS = ["plan.h", "launch.h", "device_common.h", "mfma_common.h", "entry.h",
-           "attention.h", "attention_common.h"]
+           "attention.h", "attention_common.h", "views.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -10,6 +10,11 @@
 
 #include "mdcn.h"
 
+struct mdcn_attention {
+    int32_t q_heads, k_heads, dim, causal;
+    float scale;
+};
+
 namespace mdcn {
 
 constexpr int kMaxRotaryDim = 256;
