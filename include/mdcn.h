@@ -421,6 +421,140 @@ mdcn_status mdcn_describe_rotate(const mdcn_rotary *op, mdcn_dtype dtype, const 
 mdcn_status mdcn_describe_attend(const mdcn_attention *op, mdcn_dtype dtype, const int64_t dims[3],
                                  int32_t backward, char *buf, size_t len);
 
+/* ---- key/value caches in 4 bits, in pages --------------------------------- */
+
+/* A pool is device memory cut into pages; a page holds the keys and values of
+ * `page` consecutive tokens of one sequence, rounded to 4 bits.  A table,
+ * int32 [rows][width], lists the pages of each sequence in the order of its
+ * tokens, and used, int32 [rows], its tokens: token t of sequence b lies in page
+ * table[b][t / page].  Numbers outside [0, pages) (-1 by convention) are no page.
+ * Sequences may share pages.  The tables and lengths are read on the GPU only, and
+ * nothing that they hold leads to an access outside the pool.  The conventions of
+ * the attention operators hold. */
+
+typedef struct mdcn_cache mdcn_cache;
+
+/* Caches of k_heads key and value heads of dim channels (a multiple of 8, at most
+ * 128) in pages of `page` tokens (a power of two, 16 to 256).  The handle holds no
+ * device memory.  Errors: MDCN_E_NULL, MDCN_E_ATTR. */
+mdcn_status mdcn_cache_create(int32_t k_heads, int32_t dim, int32_t page, mdcn_cache **out);
+void mdcn_cache_destroy(mdcn_cache *op);
+
+/* Bytes of a page.  Values are rounded in blocks of 32 channels of one token and
+ * head (a head's last block may be shorter) to s * m * 2^e: a sign, one of the
+ * magnitudes m 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 to 7, the sign above them), and
+ * one exponent e for the block, held as the byte e + 127: the smallest exponent
+ * within the type's limits (fp32 and bf16 -120 to 125, fp16 -23 to 13) for which
+ * the largest magnitude of the block is at most 7 * 2^e.  Values are rounded to the
+ * nearest, ties to the even code; 6 * 2^e is the largest, infinities become that.
+ * A token whose key or value of a head holds a NaN is NaN in that head's key and
+ * value (its key's exponent bytes are 255, the rest as of zeros).
+ * With n = ceil(dim / 32) blocks a head, a page is [k_heads][page / 16] strips of 16 tokens:
+ *   keys    [4 groups g][16 tokens][n][4 bytes b]: channels 8 g + 2 b and the next of a block
+ *   values  [4 groups g][16 pairs r][n][4 tokens i]: token 4 g + i, channels 2 r and the next
+ *   keys' exponents   [16 tokens][n, or 4 if n is 3]
+ *   values' exponents [4 groups g][n][4 tokens i]
+ * the first channel of two in the lower half of a byte.  A pool is written and
+ * read in one dtype.  Errors: MDCN_E_NULL. */
+mdcn_status mdcn_cache_page_bytes(const mdcn_cache *op, int64_t *bytes);
+
+/* Rounds the new keys and values of `batch` packed sequences into their pages:
+ * sequence b's are tokens cu[b] .. cu[b + 1] - 1 of k and v, and become its last,
+ * ending with token used[b] - 1.
+ *   dims[0] batch, dims[1] tokens of k and v, dims[2] pages of the pool, dims[3] bytes
+ *   from one page to the next (a multiple of 16, as is the pool's address), dims[4] width
+ *   of the table, dims[5] entries from one row of the table to the next;
+ *   dims[6..9] token and head stride of k, v (multiples of 16 bytes, as are the pointers).
+ *   cu: int32 [batch + 1].
+ * Tokens for which the table has no page, and tokens of no sequence, are not stored.
+ * Tokens that several sequences put in one place of a shared page leave values of
+ * any of them there.  Errors: MDCN_E_NULL, MDCN_E_SHAPE, MDCN_E_DTYPE, MDCN_E_ALIAS,
+ * MDCN_E_DEVICE, MDCN_E_LAUNCH. */
+mdcn_status mdcn_cache_store(const mdcn_cache *op, mdcn_dtype dtype, const int64_t dims[10],
+                             const void *k, const void *v, const int32_t *table,
+                             const int32_t *used, const int32_t *cu, void *pool, void *stream);
+
+/* The opposite: the last tokens of each sequence, as the values the cache holds, to k
+ * and v.  Tokens for which the table has no page become zeros; tokens of no
+ * sequence are left as they are, or become zeros if `fill`. */
+mdcn_status mdcn_cache_load(const mdcn_cache *op, mdcn_dtype dtype, const int64_t dims[10],
+                            const void *pool, const int32_t *table, const int32_t *used,
+                            const int32_t *cu, int32_t fill, void *k, void *v, void *stream);
+
+/* mdcn_attend against such a cache: the queries of sequence b, tokens cu_q[b] ..
+ * cu_q[b + 1] - 1, attend to its used[b] tokens (at most width * page), those of the
+ * queries among them.  `att` and `op` agree in key heads and dim.
+ *   dims[0] batch, dims[1] query tokens, dims[2..5] as above, dims[6..9] token and head
+ *   stride of q, out.
+ * Tokens for which the table has no page do not exist.  What pages hold beyond the used
+ * tokens is never used.  fill, the row that sees no key, rows of no sequence and lse are as for
+ * mdcn_attend_filled.  Keys and values are exact in the products; queries are too (fp32
+ * ones as three bf16 parts: beyond 3.39e38 NaN), probabilities are rounded to the inputs' type
+ * (fp32: to three bf16 parts, 2^-24).  The same bits in every call.
+ * Errors as for mdcn_attend. */
+mdcn_status mdcn_cache_attend_workspace_bytes(const mdcn_attention *att, const mdcn_cache *op,
+                                              mdcn_dtype dtype, const int64_t dims[10],
+                                              size_t *bytes);
+mdcn_status mdcn_cache_attend(const mdcn_attention *att, const mdcn_cache *op, mdcn_dtype dtype,
+                              const int64_t dims[10], const void *q, const void *pool,
+                              const int32_t *table, const int32_t *used, const int32_t *cu_q,
+                              int32_t fill, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Pages of any content (these operators look at tables only) of pools [layers][pages]
+ * whose layers share one table.  owners, int32 [pages], counts the entries of the
+ * table that name a page, and whatever else holds it; a page whose count is not positive
+ * is free.  Results are new tables, lengths and counts, which may overlap no input. */
+
+/* New sequences from old ones: row i of the result goes on from row parents[i] of the
+ * table and gets room for new_tokens[i] more.
+ *   dims[0] layers, dims[1] pages, dims[2] bytes of a page, dims[3] bytes from one page to
+ *   the next, dims[4] from one layer to the next (multiples of 16, as is the pool's address),
+ *   dims[5] tokens of a page, dims[6] rows of the table, dims[7] rows of the result,
+ *   dims[8] width of both.
+ *   parents: int32 [rows of the result] or NULL (row i goes on from row i); outside the
+ *   table: a new, empty sequence.  new_tokens: int32 or NULL (none); below 0 counts as 0.
+ * Full pages are shared.  Of the rows with one parent the first one keeps a last page
+ * that is full in part; each other gets a copy of it in a page of its own, in every layer.
+ * Pages for the new tokens follow.  Old rows that nobody goes on from, and entries beyond
+ * their used tokens, give their pages up; those that nothing holds then are free, and the
+ * lowest free pages are taken, in the order of rows and tokens.
+ *   table_out [rows][width] (-1: no page), used_out = used + new tokens (of the parent),
+ *   owners_out: owners less the table's entries plus table_out's.
+ *   missing: int32 [1], 0, or how many pages there are too few in the pool and the
+ *   table's width; then nothing is copied, entries without a page are -1, and the inputs
+ *   still stand for what the pool holds.
+ * Without a copy to make the pool may be NULL if `layers` is 0.
+ * Errors: MDCN_E_NULL, MDCN_E_SHAPE, MDCN_E_ALIAS, MDCN_E_WORKSPACE, MDCN_E_DEVICE, MDCN_E_LAUNCH. */
+mdcn_status mdcn_pages_fork_workspace_bytes(const int64_t dims[9], size_t *bytes);
+mdcn_status mdcn_pages_fork(const int64_t dims[9], void *pool, const int32_t *table,
+                            const int32_t *used, const int32_t *owners, const int32_t *parents,
+                            const int32_t *new_tokens, int32_t *table_out, int32_t *used_out,
+                            int32_t *owners_out, int32_t *missing, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Moves the n pages that are held to the numbers 0 .. n - 1: pages from n on go to the
+ * free numbers below n, in ascending order, in every layer; the others stay.
+ *   dims[0..4] as above, dims[5] rows, dims[6] width of the table.
+ *   table_out: the table with the new numbers (-1 for entries that name no held page),
+ *   owners_out: the counts of the new numbers, moved: int32 [pages], the new number
+ *   of each page, -1 if it is free. */
+mdcn_status mdcn_pages_compact_workspace_bytes(const int64_t dims[7], size_t *bytes);
+mdcn_status mdcn_pages_compact(const int64_t dims[7], void *pool, const int32_t *table,
+                               const int32_t *owners, int32_t *table_out, int32_t *owners_out,
+                               int32_t *moved, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Copies page src[i] of one pool to page dst[i] of another, or of the same one, in every
+ * layer.  dims[0] layers, dims[1] count, dims[2] bytes of a page; dims[3] pages, dims[4]
+ * bytes from one page and dims[5] from one layer to the next of the source, dims[6..8] of the
+ * destination.  src, dst: int32 [count].  Pairs with a number outside its pool are
+ * passed over.  A page that several pairs name as destination, or one pair as source and
+ * another as destination, holds bytes of any of them.  The pools are one (same address
+ * and strides) or do not overlap.  Errors as mdcn_pages_fork. */
+mdcn_status mdcn_pages_copy(const int64_t dims[9], const void *src_pool, void *dst_pool,
+                            const int32_t *src, const int32_t *dst, void *stream);
+
 /* ---- tracing: per-kernel device time, for profiling --------------------- */
 
 typedef struct mdcn_trace mdcn_trace;

@@ -56,6 +56,10 @@ EXPORTED = [
     "mdcn_attention_create", "mdcn_attention_destroy", "mdcn_attend_workspace_bytes",
     "mdcn_attend", "mdcn_attend_filled", "mdcn_attend_backward_workspace_bytes",
     "mdcn_attend_backward", "mdcn_describe_rotate", "mdcn_describe_attend",
+    "mdcn_cache_create", "mdcn_cache_destroy", "mdcn_cache_page_bytes", "mdcn_cache_store",
+    "mdcn_cache_load", "mdcn_cache_attend_workspace_bytes", "mdcn_cache_attend",
+    "mdcn_pages_fork_workspace_bytes", "mdcn_pages_fork", "mdcn_pages_compact_workspace_bytes",
+    "mdcn_pages_compact", "mdcn_pages_copy",
 ]
 
 # bytes of the device array mdcn_forward_noalloc works in (include/mdcn.h)
@@ -139,6 +143,21 @@ def _bind(lib):
         "mdcn_attend_backward_workspace_bytes": ([_vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
         "mdcn_attend_backward": ([_vp, ctypes.c_int, _i64p] + [_vp] * 13 + [ctypes.c_size_t, _vp],
                                  ctypes.c_int),
+        "mdcn_cache_create": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                               ctypes.POINTER(_vp)], ctypes.c_int),
+        "mdcn_cache_destroy": ([_vp], None),
+        "mdcn_cache_page_bytes": ([_vp, _i64p], ctypes.c_int),
+        "mdcn_cache_store": ([_vp, ctypes.c_int, _i64p] + [_vp] * 7, ctypes.c_int),
+        "mdcn_cache_load": ([_vp, ctypes.c_int, _i64p] + [_vp] * 4 + [ctypes.c_int32] + [_vp] * 3,
+                            ctypes.c_int),
+        "mdcn_cache_attend_workspace_bytes": ([_vp, _vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
+        "mdcn_cache_attend": ([_vp, _vp, ctypes.c_int, _i64p] + [_vp] * 5 + [ctypes.c_int32] +
+                              [_vp] * 3 + [ctypes.c_size_t, _vp], ctypes.c_int),
+        "mdcn_pages_fork_workspace_bytes": ([_i64p, _szp], ctypes.c_int),
+        "mdcn_pages_fork": ([_i64p] + [_vp] * 11 + [ctypes.c_size_t, _vp], ctypes.c_int),
+        "mdcn_pages_compact_workspace_bytes": ([_i64p, _szp], ctypes.c_int),
+        "mdcn_pages_compact": ([_i64p] + [_vp] * 7 + [ctypes.c_size_t, _vp], ctypes.c_int),
+        "mdcn_pages_copy": ([_i64p] + [_vp] * 5, ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
