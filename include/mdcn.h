@@ -462,7 +462,7 @@ mdcn_status mdcn_cache_page_bytes(const mdcn_cache *op, int64_t *bytes);
  * sequence b's are tokens cu[b] .. cu[b + 1] - 1 of k and v, and become its last,
  * ending with token used[b] - 1.
  *   dims[0] batch, dims[1] tokens of k and v, dims[2] pages of the pool, dims[3] bytes
- *   from one page to the next (a multiple of 16, as is the pool's address), dims[4] width
+ *   from one page to the next (a multiple of 16 below 2^32; the pool's address too is one of 16), dims[4] width
  *   of the table, dims[5] entries from one row of the table to the next;
  *   dims[6..9] token and head stride of k, v (multiples of 16 bytes, as are the pointers).
  *   cu: int32 [batch + 1].

@@ -14,7 +14,8 @@ namespace {
 using namespace mdcn;
 
 constexpr int64_t kMaxRowTokens = int64_t(1) << 30;      // of a row of a table
-constexpr int64_t kMaxPageStride = int64_t(1) << 40;
+constexpr int64_t kMaxPageStride = int64_t(1) << 40;     // bytes
+constexpr int64_t kMaxCacheStride = (int64_t(1) << 32) - 16;
 constexpr int64_t kMaxEntries = (int64_t(1) << 31) - 1;  // of a table, and pages of a pool
 
 int64_t page_bytes_of(const mdcn_cache &op)
@@ -32,7 +33,7 @@ mdcn_status cache_dims(const mdcn_cache *op, mdcn_dtype dtype, const int64_t *di
     if (!valid_dtype(dtype))
         return MDCN_E_DTYPE;
     if (dims[0] < 0 || dims[0] > (1 << 24) || dims[1] < 0 || dims[1] > kMaxTokens || dims[2] < 0 ||
-        dims[2] > kMaxEntries || dims[3] < 0 || dims[3] > kMaxPageStride || dims[3] % 16 ||
+        dims[2] > kMaxEntries || dims[3] < 0 || dims[3] > kMaxCacheStride || dims[3] % 16 ||
         (dims[2] > 1 && dims[3] < page_bytes_of(*op)))
         return MDCN_E_SHAPE;
     if (dims[4] < 0 || dims[4] > kMaxRowTokens / op->page || dims[5] < 0 ||

@@ -29,6 +29,13 @@ namespace mdcn {
 namespace {
 
 constexpr int kTile = 32;                        // tokens
+
+// s_waitcnt lgkmcnt(0), nothing else
+constexpr int kWaitLds = 0xc07f;
+
+// Whole numbers that no kernel writes while this one runs, read through the scalar cache.
+typedef const int32_t __attribute__((address_space(4))) *scalar_ints;
+
 constexpr int kWaves = 4;
 
 __device__ __forceinline__ float4v mfma16(half8 a, half8 b, float4v c)
@@ -60,6 +67,19 @@ template <typename T> using Vec = typename Operand<T>::vec;
 template <typename T> struct Parts {
     Vec<T> p[Operand<T>::PARTS];
 
+    // Waits for the loads behind the values here: the compiler would at their first use,
+    // in the loop, in every round, and for the copies of the tiles to come with them.
+    __device__ __forceinline__ void settle()
+    {
+#pragma unroll
+        for (int i = 0; i < Operand<T>::PARTS; ++i) {
+            uint32_t w[4];
+            __builtin_memcpy(w, &p[i], 16);
+            asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+            __builtin_memcpy(&p[i], w, 16);
+        }
+    }
+
     __device__ __forceinline__ void set(const float (&v)[8])
     {
         typedef float f8 __attribute__((ext_vector_type(8)));
@@ -82,7 +102,7 @@ __device__ __forceinline__ float4v product(Vec<T> a, const Parts<T> &b, float4v 
     return c;
 }
 
-// What a lane reads of a strip.
+// What a lane reads of a strip, in LDS.
 template <int N> struct Raw {
     Words<N> k, v, ve;
     uint32_t ke;
@@ -91,7 +111,6 @@ template <int N> struct Raw {
     {
         constexpr Strip S{N};
         k = *reinterpret_cast<const Words<N> *>(strip + lane * 4 * N);
-        v = *reinterpret_cast<const Words<N> *>(strip + S.values() + lane * 4 * N);
         const char *e = strip + S.key_exps() + (lane & 15) * S.key_exp();
         if constexpr (N == 1)
             ke = *reinterpret_cast<const uint8_t *>(e);
@@ -99,7 +118,38 @@ template <int N> struct Raw {
             ke = *reinterpret_cast<const uint16_t *>(e);
         else
             ke = *reinterpret_cast<const uint32_t *>(e);
+        v = *reinterpret_cast<const Words<N> *>(strip + S.values() + lane * 4 * N);
         ve = *reinterpret_cast<const Words<N> *>(strip + S.value_exps() + (lane >> 4) * 4 * N);
+    }
+};
+
+// Waves a SIMD that the registers leave room for: a row tile of 16-bit queries with its sums
+// takes 48 of 128 of them, a second one or the three parts of fp32 as much again.
+template <typename T, int N, int R> constexpr int row_waves()
+{
+    return R > 1 ? 2 : sizeof(T) == 4 ? 3 : 4;
+}
+
+// A wave's ring of staged tiles (two strips each), copied there asynchronously: as many as
+// fit its share of the LDS, so that a compute unit has about 140 KB on their way.
+// COPIES instructions copy a tile.
+template <int N, int WAVES> struct Ring {
+    static constexpr int TILE = 2 * Strip{N}.bytes();
+    static constexpr int SHARE = 160 * 1024 / 4 / WAVES - 64;
+    static constexpr int DEPTH = SHARE / TILE < 8 ? SHARE / TILE : 8;
+    static constexpr int STEPS = (Strip{N}.bytes() + 1023) / 1024;
+    static constexpr int COPIES = 2 * STEPS;
+
+    // 16 bytes a lane; lanes past the strip's end are switched off (they would write LDS)
+    static __device__ __forceinline__ void load(uint32_t lds, const char *strip, int lane)
+    {
+        const v4i r = row_resource(strip, Strip{N}.bytes());
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const uint32_t off = uint32_t(i * 1024 + lane * 16);
+            if ((i + 1) * 1024 <= Strip{N}.bytes() || off < uint32_t(Strip{N}.bytes()))
+                dma_row16(__builtin_amdgcn_readfirstlane(lds + i * 1024), r, off);
+        }
     }
 };
 
@@ -183,6 +233,17 @@ template <int M> struct State {
         l = 0.0f;
     }
 
+    __device__ __forceinline__ void raise(float top, float c)
+    {
+        const float up = fmaxf(top, m);
+        const float f = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - up) * c);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            o[i] *= f;
+        l *= f;
+        m = up;
+    }
+
     __device__ __forceinline__ void merge(const State &x, float c)
     {
         const float up = fmaxf(m, x.m);
@@ -243,17 +304,22 @@ __device__ __forceinline__ Piece piece_of(const CacheArgs &a, int b)
     return p;
 }
 
+// Units of an item, a (key head, row tile) of a sequence: one for each 32 << unit_shift tokens,
+// after kItemCost for what an item costs whatever its length.
 struct Units {
     int tiles, keys, all;
 };
+
+constexpr int kItemCost = 10;
+// Tiles up to which one wave takes an item alone, without the others and their barriers.
+constexpr int kAlone = 3;
 
 template <int R> __device__ __forceinline__ Units units_of(const CacheArgs &a, const Piece &p)
 {
     Units u;
     const uint32_t rows = uint32_t(p.lq) * uint32_t(a.q_heads / a.k_heads);
     u.tiles = int((rows + 16 * R - 1) / (16 * R));
-    const int keys = kTile << a.unit_shift;
-    u.keys = p.lk > keys ? (p.lk + keys - 1) >> (5 + a.unit_shift) : 1;
+    u.keys = ((p.lk + (kTile << a.unit_shift) - 1) >> (5 + a.unit_shift)) + kItemCost;
     u.all = u.tiles * a.k_heads * u.keys;
     return u;
 }
@@ -357,13 +423,19 @@ __device__ __forceinline__ void join_waves(State<M> (&s)[R], float *lds, float c
 }
 
 template <typename T, int N, int R>
-__global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend_kernel(CacheArgs a)
+__global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kernel(CacheArgs a)
 {
     constexpr Strip S{N};
-    __shared__ __align__(16) float lds[2 * R * part_floats<N>()];
+    using ring = Ring<N, row_waves<T, N, R>()>;
+    constexpr int RING = ring::DEPTH * ring::TILE;
+    constexpr int JOIN = 2 * R * part_floats<N>() * 4;
+    __shared__ __align__(16) char smem[kWaves * RING > JOIN ? kWaves * RING : JOIN];
+    float *const lds = reinterpret_cast<float *>(smem);
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const char *const own = smem + wave * RING;
+    const uint32_t ring_lds = lds_address(own);
     const int col = lane & 15, grp = lane >> 4;
     const int shared = a.q_heads / a.k_heads;
     const float c = a.scale * kLog2e, margin = raise_margin(c);
@@ -394,10 +466,11 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
         join->last = -1;
     if (int(blockIdx.x) >= share.n)
         return;
+    __syncthreads();                             // another wave may write it below
     const int u_begin = share.begin(int(blockIdx.x)), u_end = share.begin(int(blockIdx.x) + 1);
     const int strip_shift = a.page_shift - 4;
 
-    int base = 0;
+    int base = 0, turn = 0;
     for (int b0 = 0; b0 < a.batch && base < u_end; b0 += 64) {
         if (b0 > 0)
             chunk.load(a, b0, lane);
@@ -414,7 +487,8 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
             const Units un = units_of<R>(a, pc);
             const int shift = pc.lk - pc.lq;
             const int to = min(u_end, s_end);
-            const int32_t *row_pages = a.table + int64_t(b0 + i) * a.table_stride;
+            const auto row_pages = reinterpret_cast<scalar_ints>(
+                reinterpret_cast<uintptr_t>(a.table + int64_t(b0 + i) * a.table_stride));
             const int held = (pc.lk + (1 << a.page_shift) - 1) >> a.page_shift;
             for (int u = max(u_begin, s_begin); u < to;) {
                 // item: a (key head, row tile) of this sequence; keys [n0, n1) of it, in units
@@ -425,6 +499,11 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
                 const int kv_head = item / un.tiles, tile = item % un.tiles;
                 if (kv_head >= a.k_heads)
                     return;                      // offsets that overlap beyond counting
+                const int t0 = max(n0 - kItemCost, 0) << a.unit_shift;
+                const int nt = (max(n1 - kItemCost, 0) << a.unit_shift) - t0;
+                const bool alone = nt <= kAlone;
+                if (alone && (turn++ & (kWaves - 1)) != wave)
+                    continue;
 
                 int last[R], token[R], head[R];
                 bool live[R];
@@ -458,6 +537,11 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
                         q[r][j].set(v);
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        q[r][j].settle();
                 const int first_row = int(uint32_t(tile) * R * 16 / uint32_t(shared));
                 const int last_row = min(int((uint32_t(tile) * R * 16 + R * 16 - 1) /
                                              uint32_t(shared)), pc.lq - 1);
@@ -465,93 +549,111 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
                 const int all_see = a.causal ? first_row + shift : pc.lk - 1;
                 const int any_sees = a.causal ? last_row + shift : pc.lk - 1;
 
-                const int t0 = n0 << a.unit_shift, nt = (n1 - n0) << a.unit_shift;
                 const int visible = any_sees < 0 ? 0 : any_sees / kTile + 1;
-                const int w0 = t0 + nt / kWaves * wave + min(nt % kWaves, wave);
-                const int w1 = min(t0 + nt / kWaves * (wave + 1) + min(nt % kWaves, wave + 1),
-                                   visible);
+                int w0 = t0, w1 = t0 + nt;
+                if (!alone) {
+                    w0 = t0 + nt / kWaves * wave + min(nt % kWaves, wave);
+                    w1 = t0 + nt / kWaves * (wave + 1) + min(nt % kWaves, wave + 1);
+                }
+                w1 = min(w1, visible);
 
                 State<2 * N> st[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     st[r].init();
 
-                // page numbers of 64 pages, one a lane
-                int pages_at = -64, pages = -1;
-                const int64_t head_off = int64_t(kv_head << strip_shift) * S.bytes();
-                auto strip = [&](int s, bool &there) -> const char * {
-                    const int p = s >> strip_shift;
-                    if (p >= pages_at + 64 || pages_at < 0) {
-                        pages_at = p & ~63;
-                        pages = pages_at + lane < held ? row_pages[pages_at + lane] : -1;
-                    }
-                    const int n = __builtin_amdgcn_readlane(pages, p & 63);
-                    there = n >= 0 && n < a.pages;
-                    return a.pool + (there ? n : 0) * a.page_stride + head_off +
-                           (s & ((1 << strip_shift) - 1)) * S.bytes();
+                // What strip s lies in: the page that the table names, or, if that is none, page 0.
+                const char *const heads = a.pool + int64_t(kv_head << strip_shift) * S.bytes();
+                auto page_of = [&](int s) { return row_pages[min(s >> strip_shift, held - 1)]; };
+                auto stage = [&](uint32_t to, int s, int n) {
+                    const uint32_t page = uint32_t(n) < uint32_t(a.pages) ? uint32_t(n) : 0u;
+                    ring::load(to, heads + uint64_t(page) * uint32_t(a.page_stride) +
+                                       (s & ((1 << strip_shift) - 1)) * S.bytes(), lane);
+                    return page == uint32_t(n) ? 0 : 1;
                 };
-                auto load = [&](Raw<N> (&x)[2], int t, int &missing) {
-                    bool there[2];
+                int missing = 0;                 // two bits a tile of the ring, the oldest first
+                int page0 = 0, page1 = 0;        // of the tile to be staged next
+                auto next_pages = [&](int t) {
+                    page0 = page_of(2 * t);
+                    page1 = page_of(2 * t + 1);
+                };
+                auto stage_tile = [&](int t, int slot) {
+                    const uint32_t to = ring_lds + uint32_t(slot) * ring::TILE;
+                    const int m0 = stage(to, 2 * t, page0);
+                    return m0 | stage(to + S.bytes(), 2 * t + 1, page1) << 1;
+                };
+                if (w0 < w1) {
+                    next_pages(w0);
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        x[s].load(strip(2 * t + s, there[s]), lane);
-                    missing = (there[0] ? 0 : 1) | (there[1] ? 0 : 2);
-                };
-                auto compute = [&](Raw<N> (&x)[2], int t, int missing) {
-                    const int tok = t * kTile + grp * 4;
-                    const bool cut = t * kTile + kTile - 1 > all_see || missing;
-                    if (cut) {
-                        // tokens that do not exist: whatever bytes there are, finite values
+                    for (int i = 0; i < ring::DEPTH; ++i)
+                        if (w0 + i < w1) {
+                            missing |= stage_tile(w0 + i, i) << (2 * i);
+                            next_pages(w0 + i + 1);
+                        }
+                }
+                int slot = 0;
+                for (int t = w0; t < w1; ++t) {
+                    if (t + ring::DEPTH <= w1)
+                        dma_wait<ring::COPIES *(ring::DEPTH - 1)>();
+                    else
+                        dma_wait<0>();
+                    Raw<N> x[2];
+                    x[0].load(own + slot * ring::TILE, lane);
+                    x[1].load(own + slot * ring::TILE + S.bytes(), lane);
+                    float4v sc[R][2] = {};
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            const Vec<T> k = key_operand<T, N>(x[s], j);
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                sc[r][s] = product<T>(k, q[r][j], sc[r][s]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);      // 16 registers of keys, not 32
+                    }
+                    // the slot is filled again once it has been read; a wait that the compiler
+                    // knows of, or it would wait for the page numbers too before it uses x
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_s_waitcnt(kWaitLds);
+                    asm volatile("" ::: "memory");
+                    const int gone = missing & 3;
+                    missing >>= 2;
+                    if (t + ring::DEPTH < w1) {
+                        missing |= stage_tile(t + ring::DEPTH, slot) << (2 * (ring::DEPTH - 1));
+                        next_pages(t + ring::DEPTH + 1);
+                    }
+                    slot = slot + 1 == ring::DEPTH ? 0 : slot + 1;
+
+                    if (t * kTile + kTile - 1 > all_see || gone) {
+                        asm volatile("");        // a branch, not selects in every round
+                        const int tok = t * kTile + grp * 4;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            const int left = (missing >> s & 1)
-                                                 ? 0
-                                                 : clamp_int(pc.lk - (tok + 16 * s), 0, 4);
-                            const uint32_t keep =
-                                left == 0 ? 0u : 0xffffffffu >> (32 - 8 * left);
+                            // tokens that do not exist: finite values, whatever bytes there are
+                            const int left =
+                                gone >> s & 1 ? 0 : clamp_int(pc.lk - (tok + 16 * s), 0, 4);
+                            const uint32_t keep = left == 0 ? 0u : 0xffffffffu >> (32 - 8 * left);
 #pragma unroll
                             for (int b = 0; b < N; ++b)
                                 x[s].ve.w[b] = (x[s].ve.w[b] & keep) | (0x7f7f7f7fu & ~keep);
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (tok + 16 * s + e > last[r] || (gone >> s & 1))
+                                        sc[r][s][e] = -INFINITY;
                         }
                     }
-                    Vec<T> k[2][N];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int j = 0; j < N; ++j)
-                            k[s][j] = key_operand<T, N>(x[s], j);
                     Parts<T> p[R];
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        float4v sc[2] = {};
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-#pragma unroll
-                            for (int j = 0; j < N; ++j)
-                                sc[s] = product<T>(k[s][j], q[r][j], sc[s]);
-                        if (cut) {
-#pragma unroll
-                            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    sc[s][e] = tok + 16 * s + e <= last[r] && !(missing >> s & 1)
-                                                   ? sc[s][e]
-                                                   : -INFINITY;
-                        }
-                        float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                                          fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-                        top = max_groups(top);
-                        if (__ballot(top > st[r].m + margin)) {
-                            const float up = fmaxf(top, st[r].m);
-                            const float f =
-                                up == -INFINITY ? 1.0f
-                                                : __builtin_amdgcn_exp2f((st[r].m - up) * c);
-#pragma unroll
-                            for (int o = 0; o < 2 * N; ++o)
-                                st[r].o[o] *= f;
-                            st[r].l *= f;
-                            st[r].m = up;
-                        }
+                        const float4v &s0 = sc[r][0], &s1 = sc[r][1];
+                        const float top = max_groups(
+                            fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
+                                  fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))));
+                        if (__ballot(top > st[r].m + margin))
+                            st[r].raise(top, c);
                         const float off = st[r].m == -INFINITY
                                               ? 0.0f
                                               : sizeof(T) == 4
@@ -560,9 +662,9 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
                         float e8[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float s = sc[e >> 2][e & 3];
-                            e8[e] = __builtin_amdgcn_exp2f(sizeof(T) == 4 ? (s - off) * c
-                                                                          : fmaf(s, c, -off));
+                            const float v = sc[r][e >> 2][e & 3];
+                            e8[e] = __builtin_amdgcn_exp2f(sizeof(T) == 4 ? (v - off) * c
+                                                                          : fmaf(v, c, -off));
                         }
                         st[r].l += ((e8[0] + e8[1]) + (e8[2] + e8[3])) +
                                    ((e8[4] + e8[5]) + (e8[6] + e8[7]));
@@ -577,25 +679,14 @@ __global__ __launch_bounds__(256, R == 1 ? 3 : R == 2 ? 2 : 1) void cache_attend
                             st[r].o[2 * b] = product<T>(even, p[r], st[r].o[2 * b]);
                             st[r].o[2 * b + 1] = product<T>(odd, p[r], st[r].o[2 * b + 1]);
                         }
-                    }
-                };
-                Raw<N> x[2], y[2];
-                int mx = 0, my = 0;
-                if (w0 < w1)
-                    load(x, w0, mx);
-                for (int t = w0; t < w1; t += 2) {
-                    if (t + 1 < w1)
-                        load(y, t + 1, my);
-                    compute(x, t, mx);
-                    if (t + 1 < w1) {
-                        if (t + 2 < w1)
-                            load(x, t + 2, mx);
-                        compute(y, t + 1, my);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
-
-                join_waves<R, 2 * N>(st, lds, c, wave, lane);
-                if (wave == 0) {
+                if (!alone) {
+                    __syncthreads();             // the rings become the waves' way to join
+                    join_waves<R, 2 * N>(st, lds, c, wave, lane);
+                }
+                if (alone || wave == 0) {
                     if (n0 == 0 && n1 == un.keys) {
 #pragma unroll
                         for (int r = 0; r < R; ++r)
@@ -707,10 +798,10 @@ template <typename T> hipError_t launch_blocks(const CacheArgs &a, hipStream_t s
 
 }  // namespace
 
-int cache_attend_workers(mdcn_dtype, const CacheArgs &a)
+int cache_attend_workers(mdcn_dtype dtype, const CacheArgs &a)
 {
     const int tiles = row_tiles(a);
-    return 256 * (tiles == 1 ? 3 : tiles == 2 ? 2 : 1);
+    return 256 * (tiles > 1 ? 2 : dtype == MDCN_F32 ? 3 : 4);
 }
 
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a)
@@ -727,7 +818,7 @@ hipError_t launch_cache_attend(mdcn_dtype dtype, CacheArgs a, void *workspace, h
     // units of a batch, at most (row tiles) x (key heads) x (units of all tokens)
     const double rows = double(a.tokens) * (a.q_heads / a.k_heads);
     const double tiles = rows / (16 * row_tiles(a)) + a.batch;
-    const double keys = double(a.width) * (1 << a.page_shift) / kTile;
+    const double keys = double(a.width) * (1 << a.page_shift) / kTile + kItemCost;
     a.unit_shift = 0;
     while (tiles * a.k_heads * (keys / (1 << a.unit_shift) + 1) > 1e9 && a.unit_shift < 20)
         ++a.unit_shift;
