@@ -23,9 +23,11 @@ LIBRARY = os.path.join(PKG, "libmdcn.so")
 SOURCES = ["plan.cpp", "api.cpp", "prep.hip", "gather.hip", "gemm.hip", "depthwise.hip",
            "fused.hip", "window.hip", "direct.hip", "backward.hip", "noalloc.hip",
            "attention_api.cpp", "rotary.hip", "attend.hip", "attend_split.hip",
-           "attend_backward.hip", "cache_api.cpp", "cache_store.hip", "cache_attend.hip", "pages.hip"]
+           "attend_backward.hip", "cache_api.cpp", "cache_store.hip", "cache_attend.hip",
+           "cache_attend_tile.hip", "pages.hip"]
 HEADERS = ["plan.h", "launch.h", "device_common.h", "mfma_common.h", "entry.h",
-           "attention.h", "attention_common.h", "views.h", "cache.h", "cache_common.h"]
+           "attention.h", "attention_common.h", "views.h", "cache.h", "cache_common.h",
+           "cache_attend.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

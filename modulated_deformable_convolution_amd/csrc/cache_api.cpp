@@ -126,6 +126,8 @@ mdcn_status attend_args(const mdcn_attention *att, const mdcn_cache *op, mdcn_dt
         return st;
     if (att->k_heads != op->k_heads || att->dim != op->dim)
         return MDCN_E_ATTR;
+    if (dims[1] > kMaxEntries / (att->q_heads / att->k_heads))   // rows of a key head
+        return MDCN_E_SHAPE;
     a->q_heads = att->q_heads;
     a->causal = att->causal;
     a->scale = att->scale;

@@ -1,0 +1,485 @@
+// cache_attend.h -- pieces of the attention kernels on 4-bit caches (gfx950).
+//
+// out = softmax(scale q k^T) v with one pass over the used tokens.  Scores are computed as
+// S^T = K Q^T on 16x16x32 MFMA tiles, 16 rows (queries times the heads that share a key head)
+// a tile: lane 16 g + c then holds row c's scores of tokens 4 g .. 4 g + 3 of a strip, which,
+// rounded, are the operand of O^T = V^T P^T without any exchange, as the order of an
+// instruction's k index is free as long as both operands share it.  The strips are laid out
+// so that a lane's fp4 words of keys and values are the other operands once converted.
+//
+// Keys, values and scales are exact in 16 bits; the conversion takes 2^e from a float's
+// exponent bits and ignores the others, so an exponent byte needs one shift.
+// Values of one byte are two channels of one token (one exponent); two converted tokens
+// are regrouped by channel with two permutes.  fp32 queries and probabilities are
+// split into three bf16 parts (products with fp4 values are exact in fp32): 2^-24, at a
+// sixth of the time of fp32 MFMA.
+#pragma once
+
+#include "cache_common.h"
+
+namespace mdcn {
+
+// s_waitcnt lgkmcnt(0), nothing else
+constexpr int kWaitLds = 0xc07f;
+
+// Whole numbers that no kernel writes while this one runs, read through the scalar cache.
+typedef const int32_t __attribute__((address_space(4))) *scalar_ints;
+
+constexpr int kWaves = 4;                        // of a workgroup
+
+__device__ __forceinline__ float4v mfma16(half8 a, half8 b, float4v c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float4v mfma16(bf16x8 a, bf16x8 b, float4v c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// The 16-bit operands that stand for a value of T: itself, or three bf16 parts.
+template <typename T> struct Operand {
+    typedef T type;
+    typedef T vec __attribute__((ext_vector_type(8)));
+    static constexpr int PARTS = 1;
+};
+template <> struct Operand<float> {
+    typedef bf16_t type;
+    typedef bf16x8 vec;
+    static constexpr int PARTS = 3;
+};
+
+template <typename T> using Vec = typename Operand<T>::vec;
+
+// v[0..7] as operands.  16-bit types: rounded to nearest even (queries are exact); fp32:
+// each part is the rounded rest.
+template <typename T> struct Parts {
+    Vec<T> p[Operand<T>::PARTS];
+
+    // Waits for the loads behind the values here: the compiler would at their first use,
+    // in the loop, in every round, and for the copies of the tiles to come with them.
+    __device__ __forceinline__ void settle()
+    {
+#pragma unroll
+        for (int i = 0; i < Operand<T>::PARTS; ++i) {
+            uint32_t w[4];
+            __builtin_memcpy(w, &p[i], 16);
+            asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+            __builtin_memcpy(&p[i], w, 16);
+        }
+    }
+
+    __device__ __forceinline__ void set(const float (&v)[8])
+    {
+        typedef float f8 __attribute__((ext_vector_type(8)));
+        f8 x = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+#pragma unroll
+        for (int i = 0; i < Operand<T>::PARTS; ++i) {
+            p[i] = __builtin_convertvector(x, Vec<T>);
+            if (i + 1 < Operand<T>::PARTS)
+                x -= __builtin_convertvector(p[i], f8);
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ float4v product(Vec<T> a, const Parts<T> &b, float4v c)
+{
+#pragma unroll
+    for (int i = Operand<T>::PARTS - 1; i >= 0; --i)
+        c = mfma16(a, b.p[i], c);
+    return c;
+}
+
+// What a lane reads of a strip.
+template <int N> struct Raw {
+    Words<N> k, v, ve;
+    uint32_t ke;
+
+    __device__ __forceinline__ void load(const char *strip, int lane)
+    {
+        constexpr Strip S{N};
+        k = *reinterpret_cast<const Words<N> *>(strip + lane * 4 * N);
+        const char *e = strip + S.key_exps() + (lane & 15) * S.key_exp();
+        if constexpr (N == 1)
+            ke = *reinterpret_cast<const uint8_t *>(e);
+        else if constexpr (N == 2)
+            ke = *reinterpret_cast<const uint16_t *>(e);
+        else
+            ke = *reinterpret_cast<const uint32_t *>(e);
+        v = *reinterpret_cast<const Words<N> *>(strip + S.values() + lane * 4 * N);
+        ve = *reinterpret_cast<const Words<N> *>(strip + S.value_exps() + (lane >> 4) * 4 * N);
+    }
+};
+
+// Byte i of w where a float has its exponent, other bits of no meaning around it.
+__device__ __forceinline__ uint32_t exponent_at(uint32_t w, int i)
+{
+    return i < 3 ? w << (23 - 8 * i) : w >> 1;
+}
+
+template <typename T> __device__ __forceinline__ Vec<T> as_vec(const uint32_t (&w)[4])
+{
+    Vec<T> v;
+    __builtin_memcpy(&v, w, 16);
+    return v;
+}
+
+// Keys of block j of a strip: 8 channels of the lane's token.
+template <typename T, int N>
+__device__ __forceinline__ Vec<T> key_operand(const Raw<N> &r, int j)
+{
+    using E = typename Operand<T>::type;
+    const uint32_t e = exponent_at(r.ke, j);
+    const uint32_t w[4] = {fp4_pair<E, 0>(r.k.w[j], e), fp4_pair<E, 1>(r.k.w[j], e),
+                           fp4_pair<E, 2>(r.k.w[j], e), fp4_pair<E, 3>(r.k.w[j], e)};
+    return as_vec<T>(w);
+}
+
+// Values of block b of a strip: 4 tokens of the lane's two channels, half of an operand each.
+template <typename T, int N>
+__device__ __forceinline__ void value_halves(const Raw<N> &x, int b, uint32_t (&even)[2],
+                                             uint32_t (&odd)[2])
+{
+    using E = typename Operand<T>::type;
+    const uint32_t w = x.v.w[b], e = x.ve.w[b];
+    const uint32_t t[4] = {fp4_pair<E, 0>(w, exponent_at(e, 0)), fp4_pair<E, 1>(w, exponent_at(e, 1)),
+                           fp4_pair<E, 2>(w, exponent_at(e, 2)),
+                           fp4_pair<E, 3>(w, exponent_at(e, 3))};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        even[i] = __builtin_amdgcn_perm(t[2 * i + 1], t[2 * i], 0x05040100u);
+        odd[i] = __builtin_amdgcn_perm(t[2 * i + 1], t[2 * i], 0x07060302u);
+    }
+}
+
+// Tokens of a strip that do not exist get exponents of finite values, whatever bytes there
+// are; `left` of the lane's four tokens exist.
+template <int N> __device__ __forceinline__ void settle_values(Raw<N> &x, int left)
+{
+    const uint32_t keep = left <= 0 ? 0u : left >= 4 ? ~0u : 0xffffffffu >> (32 - 8 * left);
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+        x.ve.w[b] = (x.ve.w[b] & keep) | (0x7f7f7f7fu & ~keep);
+}
+
+// The largest of the four lanes that hold one row.
+__device__ __forceinline__ float max_groups(float v)
+{
+    uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    return max_halves(v);
+}
+
+__device__ __forceinline__ float sum_groups(float v)
+{
+    uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    u = __float_as_uint(v);
+    const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// One row tile's maxima, sums (the lane's own tokens only) and M tiles of outputs.
+template <int M> struct State {
+    float4v o[M];
+    float m, l;
+
+    __device__ __forceinline__ void init()
+    {
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            o[i] = (float4v){};
+        m = -INFINITY;
+        l = 0.0f;
+    }
+
+    __device__ __forceinline__ void raise(float top, float c)
+    {
+        const float up = fmaxf(top, m);
+        const float f = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - up) * c);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            o[i] *= f;
+        l *= f;
+        m = up;
+    }
+
+    __device__ __forceinline__ void merge(const State &x, float c)
+    {
+        const float up = fmaxf(m, x.m);
+        const float f = m == up ? 1.0f : __builtin_amdgcn_exp2f((m - up) * c);
+        const float g = x.m == up ? 1.0f : __builtin_amdgcn_exp2f((x.m - up) * c);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[i][j] = fmaf(x.o[i][j], g, o[i][j] * f);
+        l = fmaf(x.l, g, l * f);
+        m = up;
+    }
+};
+
+// Scores of NS strips, -infinity where hidden, to probabilities, which are added up and
+// rounded to operands of two strips each.
+template <typename T, int M, int NS>
+__device__ __forceinline__ void softmax(State<M> &st, const float4v (&sc)[NS],
+                                        Parts<T> (&p)[NS / 2], float c, float margin)
+{
+    float top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+        top = fmaxf(top, fmaxf(fmaxf(sc[s][0], sc[s][1]), fmaxf(sc[s][2], sc[s][3])));
+    top = max_groups(top);
+    if (__ballot(top > st.m + margin))
+        st.raise(top, c);
+    const float off = st.m == -INFINITY ? 0.0f
+                      : sizeof(T) == 4  ? st.m
+                                        : fmaf(st.m, c, float(-kLift<T>));
+#pragma unroll
+    for (int i = 0; i < NS / 2; ++i) {
+        float e8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = sc[2 * i + (e >> 2)][e & 3];
+            e8[e] = __builtin_amdgcn_exp2f(sizeof(T) == 4 ? (v - off) * c : fmaf(v, c, -off));
+        }
+        st.l += ((e8[0] + e8[1]) + (e8[2] + e8[3])) + ((e8[4] + e8[5]) + (e8[6] + e8[7]));
+        p[i].set(e8);
+    }
+}
+
+// Outputs of blocks b0 .. b0 + M / 2 - 1 of a finished row, and its lse.
+template <typename T, int M>
+__device__ __forceinline__ void finish(const CacheArgs &a, const State<M> &s, int token, int head,
+                                       int b0, int group, bool live)
+{
+    const float sum = sum_groups(s.l);
+    if (!live)
+        return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    char *row = const_cast<char *>(row_ptr<T>(a.out, token, head));
+#pragma unroll
+    for (int b = 0; b < M / 2; ++b) {
+        const int ch = (b0 + b) * 32 + group * 8;
+        if (ch < a.dim) {
+            struct alignas(16) {
+                T e[8];
+            } v;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float o = s.o[2 * b + (i & 1)][i >> 1];
+                v.e[i] = from_f32<T>(sum == 0.0f ? 0.0f : sizeof(T) == 4 ? o / sum : o * inv);
+            }
+            __builtin_memcpy(__builtin_assume_aligned(row + ch * sizeof(T), 16), &v, sizeof(v));
+        }
+    }
+    if (b0 == 0 && group == 0)
+        a.lse[int64_t(head) * a.tokens + token] =
+            sum == 0.0f ? -INFINITY : row_lse<T>(s.m, sum, a.scale);
+}
+
+// ---- the batch -------------------------------------------------------------
+
+struct Piece {
+    int q0, lq, lk;                              // first query, queries, tokens of the cache
+};
+
+__device__ __forceinline__ Piece piece_of(const CacheArgs &a, int b)
+{
+    Piece p;
+    p.q0 = clamp_int(a.cu[b], 0, a.tokens);
+    p.lq = clamp_int(a.cu[b + 1], p.q0, a.tokens) - p.q0;
+    p.lk = a.pages ? clamp_int(a.used[b], 0, a.width << a.page_shift) : 0;
+    return p;
+}
+
+// The rows of row tile `index` of a (sequence, key head), one a lane of 16.
+template <typename T, int N> struct RowTile {
+    Parts<T> q[N];
+    int token, head, last;                       // last token that the row sees
+    bool live;
+
+    __device__ __forceinline__ void load(const CacheArgs &a, const Piece &pc, int kv_head,
+                                         uint32_t index, int lane)
+    {
+        const uint32_t shared = uint32_t(a.q_heads / a.k_heads);
+        const uint32_t packed = index * 16 + (lane & 15);
+        const int row = int(packed / shared);
+        live = row < pc.lq;
+        token = pc.q0 + row;
+        head = kv_head * int(shared) + int(packed % shared);
+        last = !live ? -1 : a.causal ? row + pc.lk - pc.lq : pc.lk - 1;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int ch = j * 32 + (lane >> 4) * 8;
+            float v[8] = {};
+            if (live && ch < a.dim) {
+                struct alignas(16) {
+                    T e[8];
+                } x;
+                const char *p = row_ptr<T>(a.q, token, head) + ch * sizeof(T);
+                __builtin_memcpy(&x, __builtin_assume_aligned(p, 16), sizeof(x));
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = to_f32(x.e[e]);
+            }
+            q[j].set(v);
+        }
+    }
+};
+
+// What row tiles first .. first + n - 1 see: all their rows the tokens up to `all`, none those
+// past `any`.
+struct Sight {
+    int all, any;
+
+    __device__ __forceinline__ Sight(const CacheArgs &a, const Piece &pc, uint32_t first, uint32_t n)
+    {
+        const uint32_t shared = uint32_t(a.q_heads / a.k_heads);
+        const int low = int(first * 16 / shared), high = int(((first + n) * 16 - 1) / shared);
+        all = a.causal ? low + pc.lk - pc.lq : pc.lk - 1;
+        any = low >= pc.lq ? -1 : a.causal ? min(high, pc.lq - 1) + pc.lk - pc.lq : pc.lk - 1;
+    }
+};
+
+// Fills rows of no sequence: the workgroups past `workers`.
+template <typename T> __device__ __forceinline__ void fill_rows(const CacheArgs &a)
+{
+    const int part = int(blockIdx.x) - a.workers, parts = int(gridDim.x) - a.workers;
+    if (a.fill & kFillOut)
+        zero_outside<T>(a.out, a.cu, a.batch, a.tokens, a.q_heads, a.dim, part, parts);
+    if (a.fill & kFillLse)
+        outside_rows(a.cu, a.batch, a.tokens, a.q_heads, part, parts, [&](int token, int h) {
+            a.lse[int64_t(h) * a.tokens + token] = -INFINITY;
+        });
+}
+
+// `n` workgroups, enough units for all waves of each; workgroup i has units
+// [units * i / n, units * (i + 1) / n).
+struct Share {
+    int units, n, each, rest;
+
+    __device__ __forceinline__ Share(int units_, int workers) : units(units_)
+    {
+        n = min((units + kWaves - 1) / kWaves, workers);
+        each = n > 0 ? units / n : 0;
+        rest = units - each * n;
+    }
+
+    __device__ __forceinline__ int begin(int i) const { return i * each + i * rest / n; }
+
+    // the workgroup that has unit u
+    __device__ __forceinline__ int owner(int u) const
+    {
+        int i = min(int(float(u) * (float(n) / float(units))), n - 1);   // off by one at most
+        while (i + 1 < n && begin(i + 1) <= u)
+            ++i;
+        while (i > 0 && begin(i) > u)
+            --i;
+        return i;
+    }
+};
+
+// What the second kernel is to join: the item that begins in a workgroup's range
+// and does not end there.
+struct Join {
+    int q0, lq, head, tile;
+    int last;                                    // workgroup of its last part, -1: nothing
+    int pad[3];
+};
+
+// A part in the workspace: registers as they are, [row tile][2 n + m and l][lane].
+template <int N> constexpr int part_floats() { return (8 * N + 2) * 64; }
+
+template <int M>
+__device__ __forceinline__ void put_state(float *p, const State<M> &s, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        reinterpret_cast<float4v *>(p)[i * 64 + lane] = s.o[i];
+    p[M * 256 + lane] = s.m;
+    p[M * 256 + 64 + lane] = s.l;
+}
+
+template <int M>
+__device__ __forceinline__ void get_state(State<M> &s, const float *p, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        s.o[i] = reinterpret_cast<const float4v *>(p)[i * 64 + lane];
+    s.m = p[M * 256 + lane];
+    s.l = p[M * 256 + 64 + lane];
+}
+
+// Joins the four waves' states into wave 0's.
+template <int R, int M>
+__device__ __forceinline__ void join_waves(State<M> (&s)[R], float *lds, float c, int wave, int lane)
+{
+    constexpr int FLOATS = (4 * M + 2) * 64;
+#pragma unroll
+    for (int half = 2; half >= 1; half /= 2) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                put_state(lds + ((wave - half) * R + r) * FLOATS, s[r], lane);
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                State<M> x;
+                get_state(x, lds + (wave * R + r) * FLOATS, lane);
+                s[r].merge(x, c);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// One workgroup per (workgroup of the first kernel, row tile and block of channels): joins
+// the parts of the item of ROWS row tiles that began there.  Its waves take every fourth part.
+template <typename T, int N, int ROWS>
+__global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
+{
+    __shared__ __align__(16) float lds[2 * part_floats<1>()];
+    const Join j = reinterpret_cast<const Join *>(a.joins)[blockIdx.x];
+    if (j.last < 0)
+        return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int r = int(blockIdx.y) / N, b = int(blockIdx.y) % N;
+    const float c = a.scale * kLog2e;
+    const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
+
+    State<2> st[1];
+    st[0].init();
+    for (int i = first + wave; i <= end; i += kWaves) {
+        const float *p = a.partial + ((int64_t(i) * 2 + (i == first ? 1 : 0)) * ROWS + r) *
+                                         part_floats<N>();
+        State<2> x;
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+            x.o[o] = reinterpret_cast<const float4v *>(p)[(2 * b + o) * 64 + lane];
+        x.m = p[2 * N * 256 + lane];
+        x.l = p[2 * N * 256 + 64 + lane];
+        st[0].merge(x, c);
+    }
+    join_waves<1, 2>(st, lds, c, wave, lane);
+    if (wave == 0) {
+        const uint32_t shared = uint32_t(a.q_heads / a.k_heads);
+        const uint32_t packed = (uint32_t(j.tile) * ROWS + r) * 16 + (lane & 15);
+        const int row = int(packed / shared);
+        finish<T, 2>(a, st[0], j.q0 + row, j.head * int(shared) + int(packed % shared), b, lane >> 4,
+                     row < j.lq);
+    }
+}
+
+// The kernel for many rows: 16 * kWaves * R of one key head a workgroup.
+constexpr int tile_row_tiles(bool f32) { return kWaves * (f32 ? 1 : 2); }
+constexpr int kTileWorkers = 512;
+hipError_t launch_cache_tile(mdcn_dtype dtype, const CacheArgs &a, hipStream_t s);
+
+}  // namespace mdcn

@@ -189,6 +189,11 @@ ATTEND = [
     (2, 1, 56, 16, [20, 33], [25, 40], True),          # more queries than tokens
     (2, 2, 32, 16, [3] * 66 + [100, 0, 9], [1] * 66 + [2, 1, 0], True),
     (64, 1, 128, 16, [130], [1], True),
+    (8, 2, 128, 16, [500, 33, 0, 64], [300, 33, 5, 1], True),
+    (4, 4, 64, 32, [700, 129], [200, 129], True),
+    (12, 2, 96, 64, [257, 1000], [100, 64], False),
+    (6, 1, 32, 16, [30, 200], [60, 150], True),        # more queries than tokens
+    (2, 1, 80, 128, [1500], [400], True),
 ]
 
 
