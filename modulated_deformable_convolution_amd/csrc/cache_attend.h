@@ -251,13 +251,45 @@ __device__ __forceinline__ void softmax(State<M> &st, const float4v (&sc)[NS],
     }
 }
 
+// ---- the batch -------------------------------------------------------------
+
+struct Piece {
+    int q0, lq, lk;                              // first query, queries, tokens of the cache
+};
+
+__device__ __forceinline__ Piece piece_of(const CacheArgs &a, int b)
+{
+    Piece p;
+    p.q0 = clamp_int(a.cu[b], 0, a.tokens);
+    p.lq = clamp_int(a.cu[b + 1], p.q0, a.tokens) - p.q0;
+    p.lk = a.pages ? clamp_int(a.used[b], 0, a.width << a.page_shift) : 0;
+    return p;
+}
+
+// Row c of row tile `index` of a (sequence, key head), c = lane % 16.
+struct Row16 {
+    int row, token, head;
+    bool live;
+
+    __device__ __forceinline__ Row16(const CacheArgs &a, int q0, int lq, int kv_head, uint32_t index,
+                                     int lane)
+    {
+        const uint32_t shared = uint32_t(a.q_heads / a.k_heads), packed = index * 16 + (lane & 15);
+        row = int(packed / shared);
+        live = row < lq;
+        token = q0 + row;
+        head = kv_head * int(shared) + int(packed % shared);
+    }
+};
+
 // Outputs of blocks b0 .. b0 + M / 2 - 1 of a finished row, and its lse.
 template <typename T, int M>
-__device__ __forceinline__ void finish(const CacheArgs &a, const State<M> &s, int token, int head,
-                                       int b0, int group, bool live)
+__device__ __forceinline__ void finish(const CacheArgs &a, const State<M> &s, const Row16 &at,
+                                       int b0, int lane)
 {
+    const int token = at.token, head = at.head, group = lane >> 4;
     const float sum = sum_groups(s.l);
-    if (!live)
+    if (!at.live)
         return;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     char *row = const_cast<char *>(row_ptr<T>(a.out, token, head));
@@ -281,46 +313,25 @@ __device__ __forceinline__ void finish(const CacheArgs &a, const State<M> &s, in
             sum == 0.0f ? -INFINITY : row_lse<T>(s.m, sum, a.scale);
 }
 
-// ---- the batch -------------------------------------------------------------
-
-struct Piece {
-    int q0, lq, lk;                              // first query, queries, tokens of the cache
-};
-
-__device__ __forceinline__ Piece piece_of(const CacheArgs &a, int b)
-{
-    Piece p;
-    p.q0 = clamp_int(a.cu[b], 0, a.tokens);
-    p.lq = clamp_int(a.cu[b + 1], p.q0, a.tokens) - p.q0;
-    p.lk = a.pages ? clamp_int(a.used[b], 0, a.width << a.page_shift) : 0;
-    return p;
-}
-
-// The rows of row tile `index` of a (sequence, key head), one a lane of 16.
+// The queries of a row tile, and the last token that each row sees.
 template <typename T, int N> struct RowTile {
     Parts<T> q[N];
-    int token, head, last;                       // last token that the row sees
-    bool live;
+    int last;
 
     __device__ __forceinline__ void load(const CacheArgs &a, const Piece &pc, int kv_head,
                                          uint32_t index, int lane)
     {
-        const uint32_t shared = uint32_t(a.q_heads / a.k_heads);
-        const uint32_t packed = index * 16 + (lane & 15);
-        const int row = int(packed / shared);
-        live = row < pc.lq;
-        token = pc.q0 + row;
-        head = kv_head * int(shared) + int(packed % shared);
-        last = !live ? -1 : a.causal ? row + pc.lk - pc.lq : pc.lk - 1;
+        const Row16 r(a, pc.q0, pc.lq, kv_head, index, lane);
+        last = !r.live ? -1 : a.causal ? r.row + pc.lk - pc.lq : pc.lk - 1;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int ch = j * 32 + (lane >> 4) * 8;
             float v[8] = {};
-            if (live && ch < a.dim) {
+            if (r.live && ch < a.dim) {
                 struct alignas(16) {
                     T e[8];
                 } x;
-                const char *p = row_ptr<T>(a.q, token, head) + ch * sizeof(T);
+                const char *p = row_ptr<T>(a.q, r.token, r.head) + ch * sizeof(T);
                 __builtin_memcpy(&x, __builtin_assume_aligned(p, 16), sizeof(x));
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -412,69 +423,6 @@ __device__ __forceinline__ void get_state(State<M> &s, const float *p, int lane)
         s.o[i] = reinterpret_cast<const float4v *>(p)[i * 64 + lane];
     s.m = p[M * 256 + lane];
     s.l = p[M * 256 + 64 + lane];
-}
-
-// Joins the four waves' states into wave 0's.
-template <int R, int M>
-__device__ __forceinline__ void join_waves(State<M> (&s)[R], float *lds, float c, int wave, int lane)
-{
-    constexpr int FLOATS = (4 * M + 2) * 64;
-#pragma unroll
-    for (int half = 2; half >= 1; half /= 2) {
-        if (wave >= half && wave < 2 * half) {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                put_state(lds + ((wave - half) * R + r) * FLOATS, s[r], lane);
-        }
-        __syncthreads();
-        if (wave < half) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                State<M> x;
-                get_state(x, lds + (wave * R + r) * FLOATS, lane);
-                s[r].merge(x, c);
-            }
-        }
-        __syncthreads();
-    }
-}
-
-// One workgroup per (workgroup of the first kernel, row tile and block of channels): joins
-// the parts of the item of ROWS row tiles that began there.  Its waves take every fourth part.
-template <typename T, int N, int ROWS>
-__global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
-{
-    __shared__ __align__(16) float lds[2 * part_floats<1>()];
-    const Join j = reinterpret_cast<const Join *>(a.joins)[blockIdx.x];
-    if (j.last < 0)
-        return;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const int r = int(blockIdx.y) / N, b = int(blockIdx.y) % N;
-    const float c = a.scale * kLog2e;
-    const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
-
-    State<2> st[1];
-    st[0].init();
-    for (int i = first + wave; i <= end; i += kWaves) {
-        const float *p = a.partial + ((int64_t(i) * 2 + (i == first ? 1 : 0)) * ROWS + r) *
-                                         part_floats<N>();
-        State<2> x;
-#pragma unroll
-        for (int o = 0; o < 2; ++o)
-            x.o[o] = reinterpret_cast<const float4v *>(p)[(2 * b + o) * 64 + lane];
-        x.m = p[2 * N * 256 + lane];
-        x.l = p[2 * N * 256 + 64 + lane];
-        st[0].merge(x, c);
-    }
-    join_waves<1, 2>(st, lds, c, wave, lane);
-    if (wave == 0) {
-        const uint32_t shared = uint32_t(a.q_heads / a.k_heads);
-        const uint32_t packed = (uint32_t(j.tile) * ROWS + r) * 16 + (lane & 15);
-        const int row = int(packed / shared);
-        finish<T, 2>(a, st[0], j.q0 + row, j.head * int(shared) + int(packed % shared), b, lane >> 4,
-                     row < j.lq);
-    }
 }
 
 // The kernel for many rows: 16 * kWaves * R of one key head a workgroup.

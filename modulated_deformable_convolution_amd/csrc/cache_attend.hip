@@ -83,6 +83,31 @@ template <int R> struct Chunk {
     }
 };
 
+// Joins the four waves' states into wave 0's.
+template <int R, int M>
+__device__ __forceinline__ void join_waves(State<M> (&s)[R], float *lds, float c, int wave, int lane)
+{
+    constexpr int FLOATS = (4 * M + 2) * 64;
+#pragma unroll
+    for (int half = 2; half >= 1; half /= 2) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                put_state(lds + ((wave - half) * R + r) * FLOATS, s[r], lane);
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                State<M> x;
+                get_state(x, lds + (wave * R + r) * FLOATS, lane);
+                s[r].merge(x, c);
+            }
+        }
+        __syncthreads();
+    }
+}
+
 template <typename T, int N, int R>
 __global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kernel(CacheArgs a)
 {
@@ -286,7 +311,9 @@ __global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kern
                     if (n0 == 0 && n1 == un.keys) {
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            finish<T, 2 * N>(a, st[r], rows[r].token, rows[r].head, 0, grp, rows[r].live);
+                            finish<T, 2 * N>(
+                                a, st[r],
+                                Row16(a, pc.q0, pc.lq, kv_head, uint32_t(tile) * R + r, lane), 0, lane);
                     } else {
                         float *slot = a.partial + (int64_t(blockIdx.x) * 2 + (n0 == 0 ? 1 : 0)) *
                                                       (R * part_floats<N>());
@@ -302,6 +329,39 @@ __global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kern
         }
         base += __builtin_amdgcn_readlane(chunk.upto, 63);
     }
+}
+
+// One workgroup per (workgroup of the first kernel, row tile and block of channels): joins
+// the parts of the item of ROWS row tiles that began there.  Its waves take every fourth part.
+template <typename T, int N, int ROWS>
+__global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
+{
+    __shared__ __align__(16) float lds[2 * part_floats<1>()];
+    const Join j = reinterpret_cast<const Join *>(a.joins)[blockIdx.x];
+    if (j.last < 0)
+        return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int r = int(blockIdx.y) / N, b = int(blockIdx.y) % N;
+    const float c = a.scale * kLog2e;
+    const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
+
+    State<2> st[1];
+    st[0].init();
+    for (int i = first + wave; i <= end; i += kWaves) {
+        const float *p = a.partial + ((int64_t(i) * 2 + (i == first ? 1 : 0)) * ROWS + r) *
+                                         part_floats<N>();
+        State<2> x;
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+            x.o[o] = reinterpret_cast<const float4v *>(p)[(2 * b + o) * 64 + lane];
+        x.m = p[2 * N * 256 + lane];
+        x.l = p[2 * N * 256 + 64 + lane];
+        st[0].merge(x, c);
+    }
+    join_waves<1, 2>(st, lds, c, wave, lane);
+    if (wave == 0)
+        finish<T, 2>(a, st[0], Row16(a, j.q0, j.lq, j.head, uint32_t(j.tile) * ROWS + r, lane), b, lane);
 }
 
 // Row tiles of an item: the split kernel takes one or two, the tile kernel (a row tile or

@@ -283,7 +283,7 @@ template <typename T, int N, int R> __global__ __launch_bounds__(256, 2) void ca
                 if (n0 == 0 && n1 == all) {
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        finish<T, 2 * N>(a, st[r], rows[r].token, rows[r].head, 0, grp, rows[r].live);
+                        finish<T, 2 * N>(a, st[r], Row16(a, pc.q0, pc.lq, kv_head, first + r, lane), 0, lane);
                 } else {
                     float *slot = a.partial + ((int64_t(blockIdx.x) * 2 + (n0 == 0 ? 1 : 0)) * kWaves +
                                                wave) * (R * part_floats<N>());
@@ -299,6 +299,36 @@ template <typename T, int N, int R> __global__ __launch_bounds__(256, 2) void ca
     }
 }
 
+// One wave per (workgroup of the first kernel, row tile): joins the parts of the item that
+// began there, the next part's registers on their way.
+template <typename T, int N, int ROWS>
+__global__ __launch_bounds__(256) void cache_tile_join_kernel(CacheArgs a)
+{
+    const Join j = reinterpret_cast<const Join *>(a.joins)[blockIdx.x];
+    if (j.last < 0)
+        return;
+    const int lane = threadIdx.x & 63;
+    const int r = int(blockIdx.y) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const float c = a.scale * kLog2e;
+    const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
+    auto part = [&](int i) {
+        return a.partial +
+               ((int64_t(i) * 2 + (i == first ? 1 : 0)) * ROWS + r) * part_floats<N>();
+    };
+    State<2 * N> st, x;
+    get_state(st, part(first), lane);
+    if (first < end)
+        get_state(x, part(first + 1), lane);
+    for (int i = first + 1; i <= end; ++i) {
+        State<2 * N> y;
+        if (i < end)
+            get_state(y, part(i + 1), lane);
+        st.merge(x, c);
+        x = y;
+    }
+    finish<T, 2 * N>(a, st, Row16(a, j.q0, j.lq, j.head, uint32_t(j.tile) * ROWS + r, lane), 0, lane);
+}
+
 template <typename T, int N> hipError_t launch(const CacheArgs &a, hipStream_t s)
 {
     constexpr int ROWS = tile_row_tiles(sizeof(T) == 4), R = ROWS / kWaves;
@@ -308,7 +338,7 @@ template <typename T, int N> hipError_t launch(const CacheArgs &a, hipStream_t s
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.workers == 0)
         return e;
-    cache_join_kernel<T, N, ROWS><<<dim3(uint32_t(a.workers), ROWS * N), 256, 0, s>>>(a);
+    cache_tile_join_kernel<T, N, ROWS><<<dim3(uint32_t(a.workers), R), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -301,23 +301,146 @@ __device__ void fork_take(const PagesArgs &a, const ForkState &f, const Team &t)
     }
 }
 
+// Rows, pages and entries up to which one workgroup does all steps, with what they count in
+// LDS: 32 rows of a table of 126 pages and a pool of 1300 take 6 us, 512 rows of 20 pages 10;
+// as steps of their own kernels, which go through memory each time, 26 and 33 us.
+constexpr int kSmallRows = 2048, kSmallPages = 16384, kSmallEntries = 65536;
+
+struct ForkLds {
+    int counts[kSmallPages];
+    uint16_t list[kSmallPages];                  // the free pages that are taken
+    int first[kSmallRows];
+    int4 rows[kSmallRows];                       // parent, held (own copy: bit 31), wants, fresh
+    int sums[kWavesOfChunk];
+    unsigned long long excess;
+};
+
 __global__ __launch_bounds__(kChunk) void fork_kernel(PagesArgs a, ForkState f)
 {
-    __shared__ int lds[kWavesOfChunk];
-    const Team t = team();
-    fork_init(a, f, t);
+    __shared__ ForkLds l;
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        l.excess = 0;
+    for (int p = tid; p < a.pool.pages; p += kChunk)
+        l.counts[p] = a.owners[p];
+    for (int r = tid; r < a.rows_in; r += kChunk)
+        l.first[r] = INT32_MAX;
     __syncthreads();
-    fork_first(a, f, t);
+
+    constexpr int EACH = kSmallRows / kChunk;    // rows of a thread: tid, tid + kChunk
+    ForkRow rows[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int i = tid + k * kChunk;
+        if (i < a.rows_out) {
+            rows[k] = fork_row(a, i);
+            if (rows[k].parent >= 0)
+                atomicMin(&l.first[rows[k].parent], i);
+        }
+    }
     __syncthreads();
-    fork_share(a, f, t);
+    int fresh = 0, copies = 0, all;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int i = tid + k * kChunk;
+        if (k * kChunk >= a.rows_out)
+            break;
+        int source = -1, n = 0;
+        if (i < a.rows_out) {
+            ForkRow &r = rows[k];
+            if (r.parent >= 0 && r.used % a.page != 0 && l.first[r.parent] != i)
+                source = a.table[r.parent * a.width + r.held - 1];
+            r.own = is_page(a, source);
+            n = (r.own ? 1 : 0) + max(0, r.wants - r.held);
+            if (r.excess)
+                atomicAdd(&l.excess, (unsigned long long)r.excess);
+            a.used_out[i] = int(min(int64_t(r.used) + r.new_tokens, int64_t(a.width) * a.page));
+        }
+        const int upto = group_scan(n, l.sums, all);
+        if (i < a.rows_out)
+            l.rows[i] = make_int4(rows[k].parent, rows[k].held | (rows[k].own ? 1 << 31 : 0),
+                                  rows[k].wants, fresh + upto - n);
+        fresh += all;
+        const int own = i < a.rows_out && rows[k].own ? 1 : 0;
+        const int made = group_scan(own, l.sums, all);
+        if (own) {
+            f.src[copies + made - 1] = source;
+            f.copies[i] = copies + made - 1;
+        }
+        copies += all;
+    }
     __syncthreads();
-    fork_count(a, f, t, lds);
+
+    // shared entries, and what they change in the counts
+    const int entries = max(a.rows_in, a.rows_out) * a.width;
+    constexpr int AT_ONCE = 4;
+    for (int e0 = tid; e0 < entries; e0 += AT_ONCE * kChunk) {
+        int old[AT_ONCE], now[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int e = e0 + k * kChunk;
+            old[k] = now[k] = -1;
+            if (e < entries) {
+                const int i = int(uint32_t(e) / uint32_t(a.width)), j = e - i * a.width;
+                if (i < a.rows_in)
+                    old[k] = a.table[e];
+                if (i < a.rows_out) {
+                    const int4 r = l.rows[i];
+                    if (j < (r.y & INT32_MAX) - (r.y < 0 ? 1 : 0))
+                        now[k] = a.table[r.x * a.width + j];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int e = e0 + k * kChunk;
+            if (!is_page(a, now[k]))
+                now[k] = -1;
+            if (e < a.rows_out * a.width)
+                a.table_out[e] = now[k];
+            if (old[k] != now[k]) {
+                if (is_page(a, old[k]))
+                    atomicAdd(&l.counts[old[k]], -1);
+                if (now[k] >= 0)
+                    atomicAdd(&l.counts[now[k]], 1);
+            }
+        }
+    }
     __syncthreads();
-    fork_scan(a, f, lds);
+
+    // the lowest free pages: each thread looks at as many pages, one after the other
+    const int each = (a.pool.pages + kChunk - 1) / kChunk;
+    const int p0 = min(tid * each, a.pool.pages), p1 = min(p0 + each, a.pool.pages);
+    int mine = 0;
+    for (int p = p0; p < p1; ++p)
+        mine += l.counts[p] <= 0 ? 1 : 0;
+    int free;
+    int rank = group_scan(mine, l.sums, free) - mine;
+    const int take = min(fresh, free);
+    for (int p = p0; p < p1 && rank < take; ++p)
+        if (l.counts[p] <= 0) {
+            l.list[rank++] = uint16_t(p);
+            l.counts[p] = 1;
+        }
     __syncthreads();
-    fork_list(a, f, t, lds);
-    __syncthreads();
-    fork_take(a, f, t);
+    for (int p = tid; p < a.pool.pages; p += kChunk)
+        a.owners_out[p] = l.counts[p];
+    const int lane = tid & 63;
+    for (int i = tid >> 6; i < a.rows_out; i += kWavesOfChunk) {
+        const int4 r = l.rows[i];
+        const int held = r.y & INT32_MAX, own = r.y < 0 ? 1 : 0;
+        for (int k = lane; k < own + max(0, r.z - held); k += 64) {
+            const int p = r.w + k < take ? l.list[r.w + k] : -1;
+            a.table_out[i * a.width + held - own + k] = p;
+            if (own && k == 0)
+                f.dst[f.copies[i]] = p;
+        }
+    }
+    if (tid == 0) {
+        const unsigned long long missing = l.excess + max(0, fresh - free);
+        a.missing[0] = missing < INT32_MAX ? int(missing) : INT32_MAX;
+        f.totals[0] = missing ? 0 : copies;
+    }
 }
 
 template <int STEP> __global__ __launch_bounds__(kChunk) void fork_step_kernel(PagesArgs a, ForkState f)
@@ -339,9 +462,6 @@ template <int STEP> __global__ __launch_bounds__(kChunk) void fork_step_kernel(P
     if (STEP == 6)
         fork_take(a, f, t);
 }
-
-// Entries and pages up to which one workgroup does the bookkeeping.
-constexpr int64_t kSmallEntries = 65536, kSmallPages = 65536;
 
 int step_blocks(int64_t n) { return int(std::clamp<int64_t>((n + kChunk - 1) / kChunk, 1, 512)); }
 
@@ -436,19 +556,63 @@ __device__ void compact_table(const PagesArgs &a, const Team &t)
     }
 }
 
+struct CompactLds {
+    int counts[kSmallPages];
+    int moved[kSmallPages];
+    int sums[kWavesOfChunk];
+    int below;
+};
+
 __global__ __launch_bounds__(kChunk) void compact_kernel(PagesArgs a, CompactState f)
 {
-    __shared__ int lds[kWavesOfChunk];
-    const Team t = team();
-    compact_count(a, f, t, lds);
+    __shared__ CompactLds l;
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        l.below = 0;
+    for (int p = tid; p < a.pool.pages; p += kChunk)
+        l.counts[p] = a.owners[p];
     __syncthreads();
-    compact_scan(a, f, lds);
+    const int each = (a.pool.pages + kChunk - 1) / kChunk;
+    const int p0 = min(tid * each, a.pool.pages), p1 = min(p0 + each, a.pool.pages);
+    int mine = 0, held;
+    for (int p = p0; p < p1; ++p)
+        mine += l.counts[p] > 0 ? 1 : 0;
+    const int before = group_scan(mine, l.sums, held) - mine;
+    // held pages that stay, below the number of all
+    mine = 0;
+    for (int p = p0; p < min(p1, held); ++p)
+        mine += l.counts[p] > 0 ? 1 : 0;
+    if (mine)
+        atomicAdd(&l.below, mine);
     __syncthreads();
-    compact_list(a, f, t, lds);
+    const int stay = l.below, moves = held - stay;
+    int rank = before;
+    for (int p = p0; p < p1; ++p) {
+        const bool there = l.counts[p] > 0;
+        l.moved[p] = there && p < held ? p : -1;
+        if (p < held && !there)
+            f.dst[p - rank] = p;
+        if (p >= held && there)
+            f.src[rank - stay] = p;
+        rank += there ? 1 : 0;
+    }
     __syncthreads();
-    compact_number(a, f, t);
+    for (int k = tid; k < moves; k += kChunk) {
+        const int s = f.src[k], d = f.dst[k];
+        l.moved[s] = d;
+        l.counts[d] = l.counts[s];
+    }
     __syncthreads();
-    compact_table(a, t);
+    for (int p = tid; p < a.pool.pages; p += kChunk) {
+        a.moved[p] = l.moved[p];
+        a.owners_out[p] = p < held ? l.counts[p] : 0;
+    }
+    for (int e = tid; e < a.rows_in * a.width; e += kChunk) {
+        const int p = a.table[e];
+        a.table_out[e] = is_page(a, p) ? l.moved[p] : -1;
+    }
+    if (tid == 0)
+        f.totals[0] = moves;
 }
 
 template <int STEP>
@@ -501,7 +665,8 @@ hipError_t launch_pages_fork(const PagesArgs &a, void *workspace, hipStream_t s)
     f.free = cut.take(a.pool.pages);
     f.totals = cut.take(2);
     const int64_t entries = int64_t(std::max(a.rows_in, a.rows_out)) * a.width;
-    if (entries <= kSmallEntries && a.pool.pages <= kSmallPages) {
+    if (entries <= kSmallEntries && a.pool.pages <= kSmallPages &&
+        std::max(a.rows_in, a.rows_out) <= kSmallRows) {
         fork_kernel<<<1, kChunk, 0, s>>>(a, f);
     } else {
         const int rows = step_blocks(std::max(a.rows_in, a.rows_out));
