@@ -125,21 +125,24 @@ def load(op: Cache, pool, table, used, cu, tokens: int, dtype, k=None, v=None, s
     where = "load"
     _device_tensors(where, pool, table, used, cu)
     stream, ctx = _stream_of(stream, pool)
-    fill = int(k is None or v is None)
-    with ctx or _NO_CONTEXT:
-        if k is None:
-            k = torch.empty((tokens, op.k_heads, op.dim), dtype=dtype, device=pool.device)
-        if v is None:
-            v = torch.empty((tokens, op.k_heads, op.dim), dtype=dtype, device=pool.device)
-    if k.dtype != dtype:
-        _fail(where, "k must be of the dtype asked for")
-    _device_tensors(where, k, v)
-    key = (_sig(pool), _sig(k), _sig(v), _sig(table), _sig(used), _sig(cu), tokens)
+    key = (_sig(pool), _sig(table), _sig(used), _sig(cu), tokens, dtype,
+           None if k is None else _sig(k), None if v is None else _sig(v))
     call = op.calls.get(key)
-    if call is None:
-        call = _remember(op.calls, key, _cache_dims(
-            op, where, pool, table, used, cu, k, tokens,
-            (("k", k, op.k_heads), ("v", v, op.k_heads))))
+    with ctx or _NO_CONTEXT:
+        if call is None:
+            like = _like((tokens, op.k_heads, op.dim), dtype, pool.device)
+            views = [_new(like) if t is None else t for t in (k, v)]
+            _device_tensors(where, *views)
+            if views[0].dtype != dtype:
+                _fail(where, "k must be of the dtype asked for")
+            call = _remember(op.calls, key, _cache_dims(
+                op, where, pool, table, used, cu, views[0], tokens,
+                (("k", views[0], op.k_heads), ("v", views[1], op.k_heads))) + (like,))
+        fill = int(k is None or v is None)
+        if k is None:
+            k = _new(call[2])
+        if v is None:
+            v = _new(call[2])
     st = _m._lib.mdcn_cache_load(op.handle, call[0], call[1], pool.data_ptr(), table.data_ptr(),
                                  used.data_ptr(), cu.data_ptr(), fill, k.data_ptr(), v.data_ptr(),
                                  stream)

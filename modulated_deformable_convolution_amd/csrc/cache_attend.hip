@@ -8,6 +8,7 @@
 // registers, and are joined in LDS; a (sequence, head, tile) that several workgroups share
 // goes to the workspace in parts that a second kernel joins.
 #include <algorithm>
+#include <cmath>
 
 #include "cache_attend.h"
 
@@ -346,18 +347,28 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
     const float c = a.scale * kLog2e;
     const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
 
+    constexpr int AT_ONCE = 4;                   // parts whose loads are on their way together
     State<2> st[1];
     st[0].init();
-    for (int i = first + wave; i <= end; i += kWaves) {
-        const float *p = a.partial + ((int64_t(i) * 2 + (i == first ? 1 : 0)) * ROWS + r) *
-                                         part_floats<N>();
-        State<2> x;
+    for (int i0 = first + wave; i0 <= end; i0 += kWaves * AT_ONCE) {
+        State<2> x[AT_ONCE];
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
-            x.o[o] = reinterpret_cast<const float4v *>(p)[(2 * b + o) * 64 + lane];
-        x.m = p[2 * N * 256 + lane];
-        x.l = p[2 * N * 256 + 64 + lane];
-        st[0].merge(x, c);
+        for (int n = 0; n < AT_ONCE; ++n) {
+            const int i = i0 + n * kWaves;
+            x[n].init();
+            if (i <= end) {
+                const float *p = a.partial + ((int64_t(i) * 2 + (i == first ? 1 : 0)) * ROWS + r) *
+                                                 part_floats<N>();
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+                    x[n].o[o] = reinterpret_cast<const float4v *>(p)[(2 * b + o) * 64 + lane];
+                x[n].m = p[2 * N * 256 + lane];
+                x[n].l = p[2 * N * 256 + 64 + lane];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < AT_ONCE; ++n)
+            st[0].merge(x[n], c);
     }
     join_waves<1, 2>(st, lds, c, wave, lane);
     if (wave == 0)
@@ -405,10 +416,21 @@ template <typename T> hipError_t launch_blocks(const CacheArgs &a, int tiles, hi
 
 }  // namespace
 
+// Units of a batch, at most: (row tiles) x (key heads) x (units of all tokens).
+static double most_units(const CacheArgs &a, int tiles, int shift)
+{
+    const int tokens = (tiles > 2 ? 64 : kTile) << shift;
+    const double rows = double(a.tokens) * (a.q_heads / a.k_heads);
+    const double keys = double(a.width) * (1 << a.page_shift) / tokens;
+    return (rows / (16 * tiles) + a.batch) * a.k_heads * (keys + kItemCost + 1);
+}
+
 int cache_attend_workers(mdcn_dtype dtype, const CacheArgs &a)
 {
     const int tiles = row_tiles(dtype, a);
-    return tiles > 2 ? kTileWorkers : 256 * (tiles == 2 ? 2 : dtype == MDCN_F32 ? 3 : 4);
+    const int most = tiles > 2 ? kTileWorkers : 256 * (tiles == 2 ? 2 : dtype == MDCN_F32 ? 3 : 4);
+    // no more than a small batch has work for
+    return int(std::min<double>(most, std::ceil(most_units(a, tiles, 0) / kWaves)));
 }
 
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a)
@@ -420,17 +442,13 @@ size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a)
 
 hipError_t launch_cache_attend(mdcn_dtype dtype, CacheArgs a, void *workspace, hipStream_t s)
 {
-    const int tiles = row_tiles(dtype, a), tokens = tiles > 2 ? 64 : kTile;
+    const int tiles = row_tiles(dtype, a);
     a.workers = a.batch ? cache_attend_workers(dtype, a) : 0;    // none: rows to fill only
     a.joins = static_cast<int4 *>(workspace);
     a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                           size_t(a.workers) * sizeof(Join));
-    // units of a batch, at most (row tiles) x (key heads) x (units of all tokens)
-    const double rows = double(a.tokens) * (a.q_heads / a.k_heads);
-    const double items = (rows / (16 * tiles) + a.batch) * a.k_heads;
-    const double keys = double(a.width) * (1 << a.page_shift) / tokens;
     a.unit_shift = 0;
-    while (items * (keys / (1 << a.unit_shift) + kItemCost + 1) > 1e9 && a.unit_shift < 20)
+    while (most_units(a, tiles, a.unit_shift) > 1e9 && a.unit_shift < 20)
         ++a.unit_shift;
     if (tiles > 2)
         return launch_cache_tile(dtype, a, s);

@@ -11,26 +11,50 @@ template <int N> struct Words {
     uint32_t w[N];
 };
 
-// The sequence of a batch that token t of a packed tensor belongs to, by its offsets `cu`,
-// or -1; every lane of the wave must call it with the same t.
-__device__ __forceinline__ int wave_find(const int32_t *cu, int batch, int t, int lane)
-{
-    int lo = 0, n = batch;                       // cu[lo] <= t if any is
-    while (n > 64) {
-        const int step = (n + 63) / 64;
-        const int i = lane * step;
-        const int below = __popcll(__ballot(i < n && cu[lo + i] <= t));
-        if (below == 0)
-            return -1;
-        lo += (below - 1) * step;
-        n = min(step, n - (below - 1) * step);
+// Finds the sequences of a packed tensor's tokens.  The offsets and lengths of 64 sequences
+// are held one a lane: in a batch of no more than that a token costs no load.
+struct Finder {
+    int begin, end, used;
+
+    __device__ __forceinline__ Finder(const CacheArgs &a, int lane)
+    {
+        begin = INT32_MAX;
+        end = used = 0;
+        if (a.batch <= 64 && lane < a.batch) {
+            begin = a.cu[lane];
+            end = a.cu[lane + 1];
+            used = a.used[lane];
+        }
     }
-    const int below = __popcll(__ballot(lane < n && cu[lo + lane] <= t));
-    if (below == 0)
-        return -1;
-    const int b = lo + below - 1;
-    return t < cu[b + 1] ? b : -1;
-}
+
+    // The sequence that token t belongs to, or -1, and the token's place in it; every lane
+    // of the wave must call it with the same t.
+    __device__ __forceinline__ int find(const CacheArgs &a, int t, int lane, int64_t &at) const
+    {
+        if (a.batch <= 64) {
+            const uint64_t below = __ballot(begin <= t);
+            if (below == 0)
+                return -1;
+            // (offsets that do not grow leave gaps: the last sequence that begins before t)
+            const int b = 63 - __builtin_clzll(below);
+            const int last = __builtin_amdgcn_readlane(end, b);
+            at = int64_t(__builtin_amdgcn_readlane(used, b)) - min(last, a.tokens) + t;
+            return t < last ? b : -1;
+        }
+        int lo = 0, n = a.batch;
+        while (n > 0) {                          // 64 offsets at a time, evenly spread
+            const int step = (n + 63) / 64, i = lane * step;
+            const int below = __popcll(__ballot(i < n && a.cu[lo + i] <= t));
+            if (below == 0)
+                return -1;
+            lo += (below - 1) * step;
+            n = step == 1 ? 0 : min(step, n - (below - 1) * step);
+        }
+        const int last = a.cu[lo + 1];
+        at = int64_t(a.used[lo]) - min(last, a.tokens) + t;
+        return t < last ? lo : -1;
+    }
+};
 
 // Where a token lies: its strip's first byte, head 0, or null; and its place there.
 struct Place {

@@ -11,6 +11,9 @@
 // One lane takes 8 channels of one token's key and value (16 bytes in 16-bit types);
 // the block's maximum comes from the 4 lanes beside it, the NaN flag from all lanes
 // of the head.  Its 8 key codes are one dword of the strip, its 8 value codes four bytes.
+// A few tokens are bound by the round trips to offsets, table and values (48 tokens of 8 heads
+// of 128 in bf16 3.4 us), many by memory (7144 tokens of 8 heads of 80 in fp32 14 us each way,
+// 3 TB/s; waves of four times as many rows took 15.5).
 #include "cache_common.h"
 
 namespace mdcn {
@@ -75,14 +78,14 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[8], int &exponent)
 template <int N> struct Task {
     static constexpr int LANES = 4 * N;              // of a row
     static constexpr int ROWS = 64 / LANES;          // of a wave
-    int64_t row;
     int token, head, part;
     bool live;
 
-    __device__ __forceinline__ Task(const CacheArgs &a, int lane, int wave)
+    __device__ __forceinline__ Task(const CacheArgs &a, int lane)
     {
         const int r = lane / LANES;
-        row = (int64_t(blockIdx.x) * 4 + wave) * ROWS + r;
+        const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+        const int64_t row = (int64_t(blockIdx.x) * 4 + wave) * ROWS + r;
         live = r < ROWS && row < int64_t(a.tokens) * a.k_heads;
         token = live ? int(row / a.k_heads) : 0;
         head = live ? int(row - int64_t(token) * a.k_heads) : 0;
@@ -92,16 +95,17 @@ template <int N> struct Task {
     // The token's place, found for the tokens of the wave one after the other.
     __device__ __forceinline__ Place find(const CacheArgs &a, int lane, bool &inside) const
     {
+        const Finder f(a, lane);
         Place p = {nullptr, 0};
         inside = false;
         uint64_t todo = __ballot(live);
         while (todo) {
             const int t = __builtin_amdgcn_readlane(token, __builtin_ctzll(todo));
-            const int b = wave_find(a.cu, a.batch, t, lane);
+            int64_t at = 0;
+            const int b = f.find(a, t, lane, at);
             if (b >= 0) {
-                const int end = min(a.cu[b + 1], a.tokens);
-                const Place q = place_of(a, b, int64_t(a.used[b]) - end + t, Strip{N}.bytes());
-                if (token == t) {
+                const Place q = place_of(a, b, at, Strip{N}.bytes());
+                if (live && token == t) {
                     p = q;
                     inside = true;
                 }
@@ -117,27 +121,25 @@ template <int N> struct Task {
 template <typename T, int N> __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs a)
 {
     constexpr Strip S{N};
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Task<N> t(a, lane, wave);
-    bool inside;
-    const Place p = t.find(a, lane, inside);
+    const int lane = threadIdx.x & 63;
+    const Task<N> t(a, lane);
     const int ch = t.part * 8;
     Eight<T> k = {}, v = {};
-    if (p.strip && ch < a.dim) {
+    if (t.live && ch < a.dim) {                      // on their way while the place is found
         k.load(row_ptr<T>(a.k, t.token, t.head) + ch * sizeof(T));
         v.load(row_ptr<T>(a.v, t.token, t.head) + ch * sizeof(T));
     }
+    bool inside;
+    const Place p = t.find(a, lane, inside);
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         nan |= k.v[i] != k.v[i] || v.v[i] != v.v[i];
     const uint64_t bad = __ballot(nan);
     const int first = lane / Task<N>::LANES * Task<N>::LANES;
-    const uint64_t row_bad = bad >> first & (~0ull >> (64 - Task<N>::LANES));
-    if (row_bad) {
-        k = {};
-        v = {};
-    }
+    const bool row_bad = bad >> first & (~0ull >> (64 - Task<N>::LANES));
+    if (row_bad)
+        k = v = {};
     int ke, ve;
     const uint32_t kw = encode<T>(k.v, ke), vw = encode<T>(v.v, ve);
     if (!p.strip)
@@ -154,7 +156,7 @@ template <typename T, int N> __global__ __launch_bounds__(256) void cache_store_
     }
 }
 
-template <typename T> __device__ __forceinline__ void decode(float (&x)[8], uint32_t w, int exponent)
+__device__ __forceinline__ void decode(float (&x)[8], uint32_t w, int exponent)
 {
     typedef float f2 __attribute__((ext_vector_type(2)));
     const float scale = __uint_as_float(uint32_t(exponent) << 23);
@@ -170,8 +172,8 @@ template <typename T> __device__ __forceinline__ void decode(float (&x)[8], uint
 template <typename T, int N> __global__ __launch_bounds__(256) void cache_load_kernel(CacheArgs a)
 {
     constexpr Strip S{N};
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Task<N> t(a, lane, wave);
+    const int lane = threadIdx.x & 63;
+    const Task<N> t(a, lane);
     bool inside;
     const Place p = t.find(a, lane, inside);
     const int ch = t.part * 8;
@@ -179,22 +181,18 @@ template <typename T, int N> __global__ __launch_bounds__(256) void cache_load_k
         return;
     Eight<T> k = {}, v = {};
     if (p.strip) {
-        const int blk = t.part >> 2, g = t.part & 3;
+        const int blk = t.part >> 2, g = t.part & 3, i = p.token;
         const uint32_t kw =
-            *reinterpret_cast<const uint32_t *>(p.strip + ((g * 16 + p.token) * N + blk) * 4);
-        const char *vp =
-            p.strip + S.values() + (((p.token >> 2) * 16 + g * 4) * N + blk) * 4 + (p.token & 3);
+            *reinterpret_cast<const uint32_t *>(p.strip + ((g * 16 + i) * N + blk) * 4);
+        const char *vp = p.strip + S.values() + (((i >> 2) * 16 + g * 4) * N + blk) * 4 + (i & 3);
         uint32_t vw = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            vw |= uint32_t(uint8_t(vp[i * N * 4])) << (8 * i);
-        const int ke = uint8_t(p.strip[S.key_exps() + p.token * S.key_exp() + blk]);
-        const int ve = ke == kNanExp
-                           ? kNanExp
-                           : uint8_t(p.strip[S.value_exps() + ((p.token >> 2) * N + blk) * 4 +
-                                             (p.token & 3)]);
-        decode<T>(k.v, kw, ke);
-        decode<T>(v.v, vw, ve);
+        for (int c = 0; c < 4; ++c)
+            vw |= uint32_t(uint8_t(vp[c * N * 4])) << (8 * c);
+        const int ke = uint8_t(p.strip[S.key_exps() + i * S.key_exp() + blk]);
+        const int ve = uint8_t(p.strip[S.value_exps() + ((i >> 2) * N + blk) * 4 + (i & 3)]);
+        decode(k.v, kw, ke);
+        decode(v.v, vw, ke == kNanExp ? kNanExp : ve);
     }
     k.store(const_cast<char *>(row_ptr<T>(a.k, t.token, t.head)) + ch * sizeof(T));
     v.store(const_cast<char *>(row_ptr<T>(a.v, t.token, t.head)) + ch * sizeof(T));

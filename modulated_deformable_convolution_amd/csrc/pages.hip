@@ -60,17 +60,26 @@ size_t up_16(size_t n) { return (n + 15) / 16 * 16; }
 
 // ---- copies ----------------------------------------------------------------
 
-constexpr int kSegment = 16384;                  // bytes of a workgroup's turn
+constexpr int kSegment = 16384;                  // most bytes of a workgroup's turn
 
-// Page src[i] to dst[i] in every layer, i < count (or *counter, if there is one).  Four
-// 16-byte loads of each thread are in flight together.
+__host__ __device__ __forceinline__ int segments_of(int page_bytes)
+{
+    return (page_bytes + kSegment - 1) / kSegment;
+}
+
+// Page src[i] to dst[i] in every layer, i < count (or *counter, if there is one); the
+// segments of a page are alike.  Past the caches, a turn a workgroup: 601 pages of 34 KB in 12
+// layers 92 us (5.5 TB/s read and written; a large copy 4.9), through the caches or with
+// 4096 workgroups of several turns 102, both 106.
 __global__ __launch_bounds__(256) void copy_pages_kernel(PoolView from, PoolView to,
                                                          const int32_t *src, const int32_t *dst,
                                                          int count, const int32_t *counter)
 {
+    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
     if (counter)
         count = min(count, *counter);
-    const int segments = (from.page_bytes + kSegment - 1) / kSegment;
+    const int segments = segments_of(from.page_bytes);
+    const int size = (from.page_bytes / 16 + segments - 1) / segments * 16;
     const int64_t turns = int64_t(count) * from.layers * segments;
     for (int64_t t = blockIdx.x; t < turns; t += gridDim.x) {
         const int64_t pair = t / segments;
@@ -79,22 +88,22 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(PoolView from, PoolView
         const int s = src[i], d = dst[i];
         if (s < 0 || s >= from.pages || d < 0 || d >= to.pages)
             continue;
-        const char *p = from.data + layer * from.layer_stride + s * from.page_stride +
-                        int64_t(seg) * kSegment;
-        char *q = to.data + layer * to.layer_stride + d * to.page_stride + int64_t(seg) * kSegment;
-        const int bytes = min(kSegment, from.page_bytes - seg * kSegment);
-        uint4 v[4];
+        const int64_t begin = int64_t(seg) * size;
+        const char *p = from.data + layer * from.layer_stride + s * from.page_stride + begin;
+        char *q = to.data + layer * to.layer_stride + d * to.page_stride + begin;
+        const int bytes = int(min(int64_t(size), from.page_bytes - begin));
+        v4u v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int at = (k * 256 + int(threadIdx.x)) * 16;
             if (at < bytes)
-                v[k] = *reinterpret_cast<const uint4 *>(p + at);
+                v[k] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(p + at));
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int at = (k * 256 + int(threadIdx.x)) * 16;
             if (at < bytes)
-                *reinterpret_cast<uint4 *>(q + at) = v[k];
+                __builtin_nontemporal_store(v[k], reinterpret_cast<v4u *>(q + at));
         }
     }
 }
@@ -102,11 +111,10 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(PoolView from, PoolView
 hipError_t launch_copies(const PoolView &from, const PoolView &to, const int32_t *src,
                          const int32_t *dst, int count, const int32_t *counter, hipStream_t s)
 {
-    const int64_t turns = int64_t(count) * from.layers *
-                          ((from.page_bytes + kSegment - 1) / kSegment);
+    const int64_t turns = int64_t(count) * from.layers * segments_of(from.page_bytes);
     if (turns == 0)
         return hipSuccess;
-    const int blocks = int(std::min<int64_t>(turns, 4096));
+    const int blocks = int(std::min<int64_t>(turns, 65536));
     copy_pages_kernel<<<blocks, 256, 0, s>>>(from, to, src, dst, count, counter);
     return hipGetLastError();
 }
