@@ -501,6 +501,13 @@ mdcn_status mdcn_cache_attend(const mdcn_attention *att, const mdcn_cache *op, m
                               int32_t fill, void *out, float *lse, void *workspace,
                               size_t workspace_bytes, void *stream);
 
+/* One line on the kernels that a call of these sizes runs, as mdcn_describe_attend: the
+ * kernel for few rows ("split") or for many ("tile"), the rows of a workgroup, workgroups and
+ * tokens of a unit. */
+mdcn_status mdcn_describe_cache_attend(const mdcn_attention *att, const mdcn_cache *op,
+                                       mdcn_dtype dtype, const int64_t dims[10], char *buf,
+                                       size_t len);
+
 /* Pages of any content (these operators look at tables only) of pools [layers][pages]
  * whose layers share one table.  owners, int32 [pages], counts the entries of the
  * table that name a page, and whatever else holds it; a page whose count is not positive
@@ -518,7 +525,7 @@ mdcn_status mdcn_cache_attend(const mdcn_attention *att, const mdcn_cache *op, m
  * that is full in part; each other gets a copy of it in a page of its own, in every layer.
  * Pages for the new tokens follow.  Old rows that nobody goes on from, and entries beyond
  * their used tokens, give their pages up; those that nothing holds then are free, and the
- * lowest free pages are taken, in the order of rows and tokens.
+ * lowest free pages are taken, in the order of rows and tokens; their count becomes 1.
  *   table_out [rows][width] (-1: no page), used_out = used + new tokens (of the parent),
  *   owners_out: owners less the table's entries plus table_out's.
  *   missing: int32 [1], 0, or how many pages there are too few in the pool and the

@@ -192,6 +192,15 @@ def attend(att: _a.Attention, op: Cache, q, pool, table, used, cu_q, out=None, l
     return out, lse
 
 
+def describe_attend(att: _a.Attention, op: Cache, dtype, batch: int, q_tokens: int, width: int) -> str:
+    """One line on attend's kernels for these sizes (mdcn_describe_cache_attend)."""
+    buf = ctypes.create_string_buffer(256)
+    dims = (_i64 * 10)(batch, q_tokens, 1, op.page_bytes, width, width, 0, 0, 0, 0)
+    _m._check(_m._lib.mdcn_describe_cache_attend(att.handle, op.handle, _m.dtype_code(dtype), dims, buf,
+                                                 256), "describe_attend")
+    return buf.value.decode()
+
+
 # ---------------------------------------------------------------- pages
 
 def _pool_dims(where, name, pool, like):
@@ -227,7 +236,7 @@ def fork_pages(pool, table, used, owners, page: int, parents=None, new_tokens=No
     _device_tensors(where, table, used, owners, *(() if pool is None else (pool,)),
                     *(() if parents is None else (parents,)),
                     *(() if new_tokens is None else (new_tokens,)))
-    lib = _m._lib
+    lib = _m._lib or _m.library()
     key = (where, None if pool is None else _sig(pool), _sig(table), _sig(used), _sig(owners), page,
            None if parents is None else _sig(parents),
            None if new_tokens is None else _sig(new_tokens))
@@ -279,7 +288,7 @@ def compact_pages(pool, table, owners, table_out=None, owners_out=None, moved=No
     the new numbers; moved int32 [pages]: the new number of each page, -1 if it is free."""
     where = "compact_pages"
     _device_tensors(where, pool, table, owners)
-    lib = _m._lib
+    lib = _m._lib or _m.library()
     key = (where, _sig(pool), _sig(table), _sig(owners))
     call = _page_calls.get(key)
     if call is None:
@@ -331,7 +340,7 @@ def copy_pages(src_pool, dst_pool, src, dst, stream=None):
         call = _remember(_page_calls, key, (_i64 * 9)(a[0], src.shape[0], a[2], a[1], a[3], a[4], b[1],
                                                       b[3], b[4]))
     stream, _ = _stream_of(stream, src)
-    st = _m._lib.mdcn_pages_copy(call, src_pool.data_ptr(), dst_pool.data_ptr(), src.data_ptr(),
-                                 dst.data_ptr(), stream)
+    st = (_m._lib or _m.library()).mdcn_pages_copy(call, src_pool.data_ptr(), dst_pool.data_ptr(),
+                                                   src.data_ptr(), dst.data_ptr(), stream)
     if st:
         _m._check(st, where)

@@ -69,8 +69,12 @@ struct CacheArgs {
 hipError_t launch_cache_store(mdcn_dtype dtype, const CacheArgs &a, hipStream_t s);
 hipError_t launch_cache_load(mdcn_dtype dtype, const CacheArgs &a, hipStream_t s);
 
-// The attention kernel's workgroups for a batch of these sizes, and its workspace.
-int cache_attend_workers(mdcn_dtype dtype, const CacheArgs &a);
+// How a batch of these sizes is attended to: rows of a workgroup (more than 32: the tile
+// kernel), workgroups, tokens of a unit of their work; and the workspace.
+struct CacheShape {
+    int rows, workers, unit;
+};
+CacheShape cache_attend_shape(mdcn_dtype dtype, const CacheArgs &a);
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a);
 hipError_t launch_cache_attend(mdcn_dtype dtype, CacheArgs a, void *workspace, hipStream_t s);
 

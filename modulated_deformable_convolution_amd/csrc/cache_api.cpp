@@ -2,6 +2,7 @@
 // pages (include/mdcn.h): validation on the host, launches on the caller's stream.
 #include <hip/hip_runtime_api.h>
 
+#include <cstdio>
 #include <new>
 
 #include "cache.h"
@@ -326,6 +327,22 @@ mdcn_status mdcn_cache_attend(const mdcn_attention *att, const mdcn_cache *op, m
     } catch (...) {
         return MDCN_E_INTERNAL;
     }
+}
+
+mdcn_status mdcn_describe_cache_attend(const mdcn_attention *att, const mdcn_cache *op,
+                                       mdcn_dtype dtype, const int64_t dims[10], char *buf,
+                                       size_t len)
+{
+    if (!buf || len == 0)
+        return MDCN_E_NULL;
+    CacheArgs a = {};
+    const mdcn_status st = attend_args(att, op, dtype, dims, &a);
+    if (st != MDCN_OK)
+        return st;
+    const mdcn::CacheShape c = mdcn::cache_attend_shape(dtype, a);
+    std::snprintf(buf, len, "%s rows=%d workgroups=%d unit=%d", c.rows > 32 ? "tile" : "split",
+                  c.rows, c.workers, c.unit);
+    return MDCN_OK;
 }
 
 mdcn_status mdcn_pages_fork_workspace_bytes(const int64_t dims[9], size_t *bytes)

@@ -425,31 +425,35 @@ static double most_units(const CacheArgs &a, int tiles, int shift)
     return (rows / (16 * tiles) + a.batch) * a.k_heads * (keys + kItemCost + 1);
 }
 
-int cache_attend_workers(mdcn_dtype dtype, const CacheArgs &a)
+CacheShape cache_attend_shape(mdcn_dtype dtype, const CacheArgs &a)
 {
     const int tiles = row_tiles(dtype, a);
     const int most = tiles > 2 ? kTileWorkers : 256 * (tiles == 2 ? 2 : dtype == MDCN_F32 ? 3 : 4);
-    // no more than a small batch has work for
-    return int(std::min<double>(most, std::ceil(most_units(a, tiles, 0) / kWaves)));
+    int shift = 0;
+    while (most_units(a, tiles, shift) > 1e9 && shift < 20)
+        ++shift;
+    // no more workgroups than a small batch has work for; none: rows to fill only
+    const int workers =
+        int(std::min<double>(most, std::ceil(most_units(a, tiles, shift) / kWaves)));
+    return CacheShape{16 * tiles, a.batch ? workers : 0, (tiles > 2 ? 64 : kTile) << shift};
 }
 
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a)
 {
-    const size_t part =
-        size_t(row_tiles(dtype, a)) * (8 * cache_blocks(a.dim) + 2) * 64 * sizeof(float);
-    return size_t(cache_attend_workers(dtype, a)) * (2 * part + sizeof(Join));
+    const CacheShape c = cache_attend_shape(dtype, a);
+    const size_t part = size_t(c.rows / 16) * (8 * cache_blocks(a.dim) + 2) * 64 * sizeof(float);
+    return size_t(c.workers) * (2 * part + sizeof(Join));
 }
 
 hipError_t launch_cache_attend(mdcn_dtype dtype, CacheArgs a, void *workspace, hipStream_t s)
 {
-    const int tiles = row_tiles(dtype, a);
-    a.workers = a.batch ? cache_attend_workers(dtype, a) : 0;    // none: rows to fill only
+    const CacheShape shape = cache_attend_shape(dtype, a);
+    const int tiles = shape.rows / 16;
+    a.workers = shape.workers;
+    a.unit_shift = __builtin_ctz(unsigned(shape.unit / (tiles > 2 ? 64 : kTile)));
     a.joins = static_cast<int4 *>(workspace);
     a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                           size_t(a.workers) * sizeof(Join));
-    a.unit_shift = 0;
-    while (most_units(a, tiles, a.unit_shift) > 1e9 && a.unit_shift < 20)
-        ++a.unit_shift;
     if (tiles > 2)
         return launch_cache_tile(dtype, a, s);
     switch (dtype) {

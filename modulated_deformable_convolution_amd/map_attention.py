@@ -7,14 +7,15 @@ of different sizes are packed as tokens, projected, normed and turned by their
 row and column, and attended in full, each map by itself; its backward pass
 gives the gradients of the tokens, the projection and the gains.  Decoder runs a
 causal layer over growing sequences, one token of each at a time, against a
-key/value cache.  The projections are plain torch products; everything else is
-the library's kernels.
+key/value cache; BeamDecoder the same against a cache in 4 bits, in pages that
+sequences share, and forks them as beam search does.  The projections are plain
+torch products; everything else is the library's kernels.
 """
 from __future__ import annotations
 
 import torch
 
-from . import attention, mdcn
+from . import attention, cache, mdcn
 
 
 def _normal(gen, shape, dtype, scale):
@@ -117,6 +118,43 @@ class Decoder(_Layer):
                                 self.cache_ends, used_k=self.used)[0].flatten(1)
 
 
+class BeamDecoder(_Layer):
+    """A causal layer whose keys and values lie in `pages` pages of a 4-bit cache; each
+    sequence has room for `room` tokens."""
+
+    def __init__(self, channels, q_heads, k_heads, dim, pages, room, page=16, dtype=torch.float16, seed=0):
+        super().__init__(channels, q_heads, k_heads, dim, [dim // 2], True, 10000.0, dtype, seed)
+        self.cache = cache.mdcn_cache_create(k_heads, dim, page)
+        self.pool = torch.empty((pages, self.cache.page_bytes), dtype=torch.uint8, device="cuda")
+        self.table = torch.empty((0, -(-room // page)), dtype=torch.int32, device="cuda")
+        self.used = torch.empty(0, dtype=torch.int32, device="cuda")
+        self.owners = torch.zeros(pages, dtype=torch.int32, device="cuda")
+
+    def forward(self, tokens, lengths, parents):
+        """The next lengths[i] tokens (packed; a list) of sequence i, which goes on from sequence
+        parents[i] of the last call, -1: a new one.  Sequences that nobody goes on from give
+        their pages up."""
+        new = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        state = cache.fork_pages(self.pool, self.table, self.used, self.owners, self.cache.page,
+                                 torch.tensor(parents, dtype=torch.int32, device="cuda"), new)
+        if int(state[3]):
+            raise ValueError("%d pages too few" % int(state[3]))
+        self.table, self.used, self.owners = state[:3]
+        ends = torch.tensor([0] + lengths).cumsum(0).to("cuda", torch.int32)
+        steps = torch.cat([torch.arange(n) for n in lengths]).to("cuda", torch.int32)
+        positions = torch.repeat_interleave(self.used - new, new) + steps
+        q, k, v = self.project(tokens)
+        q, k = attention.rotate(self.rotary, q, k, positions[None])
+        cache.store(self.cache, self.pool, k, v, self.table, self.used, ends)
+        return cache.attend(self.attention, self.cache, q, self.pool, self.table, self.used,
+                            ends)[0].flatten(1)
+
+    def compact(self):
+        """Moves the pages in use to the front of the pool; how many there are."""
+        self.table, self.owners, _ = cache.compact_pages(self.pool, self.table, self.owners)
+        return int((self.owners > 0).sum())
+
+
 def main():
     gen = torch.Generator().manual_seed(0)
     channels, sizes = 64, [(40, 40), (24, 24), (7, 5)]
@@ -140,6 +178,12 @@ def main():
         y = decoder.step(tokens[20 + 2 * i:22 + 2 * i])
     print("decoded 4 tokens of 2 sequences: used %s, outputs %s" % (decoder.used.tolist(),
                                                                     tuple(y.shape)))
+    beams = BeamDecoder(channels, 8, 2, 64, pages=24, room=64)
+    beams.forward(tokens[:24], [17, 7], [-1, -1])
+    for parents in ([0, 0, 1, 1], [1, 0, 3, 2], [0, 0, 0, 2]):
+        y = beams.forward(tokens[20:24], [1] * 4, parents)
+    print("decoded 3 tokens of 4 beams: used %s in %d pages, outputs %s" %
+          (beams.used.tolist(), beams.compact(), tuple(y.shape)))
 
 
 if __name__ == "__main__":

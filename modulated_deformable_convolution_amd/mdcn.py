@@ -58,6 +58,7 @@ EXPORTED = [
     "mdcn_attend_backward", "mdcn_describe_rotate", "mdcn_describe_attend",
     "mdcn_cache_create", "mdcn_cache_destroy", "mdcn_cache_page_bytes", "mdcn_cache_store",
     "mdcn_cache_load", "mdcn_cache_attend_workspace_bytes", "mdcn_cache_attend",
+    "mdcn_describe_cache_attend",
     "mdcn_pages_fork_workspace_bytes", "mdcn_pages_fork", "mdcn_pages_compact_workspace_bytes",
     "mdcn_pages_compact", "mdcn_pages_copy",
 ]
@@ -153,6 +154,8 @@ def _bind(lib):
         "mdcn_cache_attend_workspace_bytes": ([_vp, _vp, ctypes.c_int, _i64p, _szp], ctypes.c_int),
         "mdcn_cache_attend": ([_vp, _vp, ctypes.c_int, _i64p] + [_vp] * 5 + [ctypes.c_int32] +
                               [_vp] * 3 + [ctypes.c_size_t, _vp], ctypes.c_int),
+        "mdcn_describe_cache_attend": ([_vp, _vp, ctypes.c_int, _i64p, ctypes.c_char_p,
+                                        ctypes.c_size_t], ctypes.c_int),
         "mdcn_pages_fork_workspace_bytes": ([_i64p, _szp], ctypes.c_int),
         "mdcn_pages_fork": ([_i64p] + [_vp] * 11 + [ctypes.c_size_t, _vp], ctypes.c_int),
         "mdcn_pages_compact_workspace_bytes": ([_i64p, _szp], ctypes.c_int),
