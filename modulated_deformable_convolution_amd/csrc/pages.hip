@@ -319,6 +319,7 @@ struct ForkLds {
     uint16_t list[kSmallPages];                  // the free pages that are taken
     int first[kSmallRows];
     int4 rows[kSmallRows];                       // parent, held (own copy: bit 31), wants, fresh
+    int copies[kSmallRows];                      // which of the copies a row's is
     int sums[kWavesOfChunk];
     unsigned long long excess;
 };
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(kChunk) void fork_kernel(PagesArgs a, ForkState f)
         const int made = group_scan(own, l.sums, all);
         if (own) {
             f.src[copies + made - 1] = source;
-            f.copies[i] = copies + made - 1;
+            l.copies[i] = copies + made - 1;
         }
         copies += all;
     }
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(kChunk) void fork_kernel(PagesArgs a, ForkState f)
             const int p = r.w + k < take ? l.list[r.w + k] : -1;
             a.table_out[i * a.width + held - own + k] = p;
             if (own && k == 0)
-                f.dst[f.copies[i]] = p;
+                f.dst[l.copies[i]] = p;
         }
     }
     if (tid == 0) {
