@@ -19,7 +19,9 @@ namespace {
 constexpr int kTile = 32;                        // tokens
 
 // Waves a SIMD that the registers leave room for: a row tile of 16-bit queries with its sums
-// takes 48 of 128 of them, a second one or the three parts of fp32 as much again.
+// takes 48 of 128 of them, a second one or the three parts of fp32 as much again.  More
+// workgroups than run together, of less work each, were slower (98 us for 1536 and 2048
+// against 92 for 1024 in the case below).
 template <typename T, int N, int R> constexpr int row_waves()
 {
     return R > 1 ? 2 : sizeof(T) == 4 ? 3 : 4;
@@ -54,8 +56,11 @@ struct Units {
     int tiles, keys, all;
 };
 
+// Measured: 48 caches of 1 to 16384 tokens, 32/8 heads of 128 in bf16, with 0 / 10 / 20: 112, 99
+// and 103 us.
 constexpr int kItemCost = 10;
 // Tiles up to which one wave takes an item alone, without the others and their barriers.
+// With 0 / 3 / 8 these caches take 100, 99 and 103 us, 400 of 1 to 200 tokens 42, 39 and 33.
 constexpr int kAlone = 3;
 
 template <int R> __device__ __forceinline__ Units units_of(const CacheArgs &a, const Piece &p)
@@ -375,12 +380,18 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
         finish<T, 2>(a, st[0], Row16(a, j.q0, j.lq, j.head, uint32_t(j.tile) * ROWS + r, lane), b, lane);
 }
 
-// Row tiles of an item: the split kernel takes one or two, the tile kernel (a row tile or
-// two a wave) more, by what an average sequence has rows for.
+// Row tiles of an item, by the rows of an average sequence: one (fp32: of up to 64 rows) or
+// two in the split kernel, which reads keys and values again for each item, kWaves or twice
+// as many in the tile kernel.  Measured in us, 16 sequences of 4096 tokens (fp32: 2048), 32 query
+// and 8 key heads of 128, with one row tile / two / the tile kernel:
+//   rows   16          20          32          48          64          128
+//   bf16   32 36 64    42 38 64    41 38 64    53 49 69    61 50 70    99 70 76
+//   fp32   25 39 43    32 41 47    33 42 48    43 53 50    49 52 52    79 68 76
 int row_tiles(mdcn_dtype dtype, const CacheArgs &a)
 {
+    const bool f32 = dtype == MDCN_F32;
     const double rows = a.batch ? double(a.tokens) / a.batch * (a.q_heads / a.k_heads) : 0;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : tile_row_tiles(dtype == MDCN_F32);
+    return rows <= (f32 ? 64 : 16) ? 1 : rows <= 128 && !f32 ? 2 : tile_row_tiles(f32);
 }
 
 template <typename T, int N, int R> hipError_t launch(const CacheArgs &a, hipStream_t s)
@@ -397,7 +408,10 @@ template <typename T, int N, int R> hipError_t launch(const CacheArgs &a, hipStr
 
 template <typename T, int N> hipError_t launch_rows(const CacheArgs &a, int tiles, hipStream_t s)
 {
-    return tiles == 1 ? launch<T, N, 1>(a, s) : launch<T, N, 2>(a, s);
+    if constexpr (sizeof(T) == 2)
+        if (tiles == 2)
+            return launch<T, N, 2>(a, s);
+    return launch<T, N, 1>(a, s);
 }
 
 template <typename T> hipError_t launch_blocks(const CacheArgs &a, int tiles, hipStream_t s)

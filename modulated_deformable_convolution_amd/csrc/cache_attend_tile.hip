@@ -14,7 +14,9 @@ namespace mdcn {
 namespace {
 
 constexpr int kRound = 64;                       // tokens
-constexpr int kItemCost = 3;                     // units that an item costs beside its tokens'
+// Units that an item costs beside its tokens': with 0 / 3 / 8, six pieces of 2048 to 1 queries
+// behind 8192 to 1 tokens, 32/8 heads of 128 in bf16, took 356, 315 and 325 us.
+constexpr int kItemCost = 3;
 
 // Units of the items of one (sequence, key head), item i being rows 16 kWaves R i and on:
 // what they see grows evenly under a causal mask, so the units before an item are a

@@ -310,9 +310,9 @@ __device__ void fork_take(const PagesArgs &a, const ForkState &f, const Team &t)
 }
 
 // Rows, pages and entries up to which one workgroup does all steps, with what they count in
-// LDS: 32 rows of a table of 126 pages and a pool of 1300 take 6 us, 512 rows of 20 pages 10;
-// as steps of their own kernels, which go through memory each time, 26 and 33 us.
-constexpr int kSmallRows = 2048, kSmallPages = 16384, kSmallEntries = 65536;
+// LDS.  Forking 32 rows of 33 pages took 9 us that way and 21 as steps of their own kernels,
+// 512 rows of 20 pages 21 and 23; compacting 512 pages 8 and 13, 4096 11 and 16, 16000 30 and 20.
+constexpr int kSmallRows = 2048, kSmallPages = 8192, kSmallEntries = 32768;
 
 struct ForkLds {
     int counts[kSmallPages];
