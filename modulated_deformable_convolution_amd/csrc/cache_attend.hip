@@ -7,6 +7,13 @@
 // range's tokens each, copy their strips to LDS asynchronously and convert them in
 // registers, and are joined in LDS; a (sequence, head, tile) that several workgroups share
 // goes to the workspace in parts that a second kernel joins.
+//
+// One MI355X, 32 query and 8 key heads of 128, pages of 16: 48 caches of 1 to 16384 tokens in
+// bf16 82 to 85 us (384 MB; 430 past the L2s with the parts, 5.2 TB/s; strips alone read in this order
+// reach 5.9) and 5 to join.  Taking the conversions, the exponentials or both away leaves that time
+// as it is, pages that stay in the L2s halve it: memory bounds it.  Older waves are served
+// first and end after half of the time; shares to match, priorities or smaller shares gained
+// nothing.  One cache of 4097 tokens in fp16: 8.4 us and 5, round trips to memory.
 #include <algorithm>
 #include <cmath>
 
