@@ -476,7 +476,7 @@ mdcn_status mdcn_cache_store(const mdcn_cache *op, mdcn_dtype dtype, const int64
 
 /* The opposite: the last tokens of each sequence, as the values the cache holds, to k
  * and v.  Tokens for which the table has no page become zeros; tokens of no
- * sequence are left as they are, or become zeros if `fill`. */
+ * sequence are left as they are, or become zeros in k if fill & 1, in v if fill & 2. */
 mdcn_status mdcn_cache_load(const mdcn_cache *op, mdcn_dtype dtype, const int64_t dims[10],
                             const void *pool, const int32_t *table, const int32_t *used,
                             const int32_t *cu, int32_t fill, void *k, void *v, void *stream);

@@ -138,7 +138,7 @@ def load(op: Cache, pool, table, used, cu, tokens: int, dtype, k=None, v=None, s
             call = _remember(op.calls, key, _cache_dims(
                 op, where, pool, table, used, cu, views[0], tokens,
                 (("k", views[0], op.k_heads), ("v", views[1], op.k_heads))) + (like,))
-        fill = int(k is None or v is None)
+        fill = (1 if k is None else 0) | (2 if v is None else 0)
         if k is None:
             k = _new(call[2])
         if v is None:

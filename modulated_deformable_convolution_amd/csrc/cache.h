@@ -55,7 +55,7 @@ struct CacheArgs {
     int32_t k_heads, dim;
     int32_t page_shift;        // a page is 1 << page_shift tokens
     Heads k, v;                // store: inputs, load: outputs
-    int32_t fill;
+    int32_t fill;              // load: 1 k, 2 v; attention: kFillOut, kFillLse
     // attention
     Heads q, out;
     float *lse;

@@ -106,13 +106,13 @@ mdcn_status move_tokens(const mdcn_cache *op, mdcn_dtype dtype, const int64_t *d
     }
     if (load && share_values(views[0], views[1]))
         return MDCN_E_ALIAS;
-    if (a.tokens == 0 || (a.batch == 0 && !(load && fill)))
+    if (a.tokens == 0 || (a.batch == 0 && !(load && (fill & 3))))
         return MDCN_OK;
     if ((st = mdcn::check_device()) != MDCN_OK)
         return st;
     a.k = views[0].h;
     a.v = views[1].h;
-    a.fill = fill != 0;
+    a.fill = fill & 3;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return launched(load ? launch_cache_load(dtype, a, s) : launch_cache_store(dtype, a, s));
 }
@@ -480,7 +480,7 @@ mdcn_status mdcn_pages_copy(const int64_t dims[9], const void *src_pool, void *d
             return MDCN_E_NULL;
         const size_t list = size_t(dims[1]) * 4;
         const bool one = from.data == to.data && from.page_stride == to.page_stride &&
-                         from.layer_stride == to.layer_stride;
+                         (from.layers <= 1 || from.layer_stride == to.layer_stride);
         const Block all[] = {{one ? nullptr : from.data, pool_bytes(from), false},
                              {to.data, pool_bytes(to), true},
                              {src, list, false},

@@ -179,6 +179,7 @@ template <typename T, int N> __global__ __launch_bounds__(256) void cache_load_k
     const int ch = t.part * 8;
     if (!t.live || ch >= a.dim || !(inside || a.fill))
         return;
+    const bool put_k = inside || (a.fill & 1), put_v = inside || (a.fill & 2);
     Eight<T> k = {}, v = {};
     if (p.strip) {
         const int blk = t.part >> 2, g = t.part & 3, i = p.token;
@@ -194,8 +195,10 @@ template <typename T, int N> __global__ __launch_bounds__(256) void cache_load_k
         decode(k.v, kw, ke);
         decode(v.v, vw, ke == kNanExp ? kNanExp : ve);
     }
-    k.store(const_cast<char *>(row_ptr<T>(a.k, t.token, t.head)) + ch * sizeof(T));
-    v.store(const_cast<char *>(row_ptr<T>(a.v, t.token, t.head)) + ch * sizeof(T));
+    if (put_k)
+        k.store(const_cast<char *>(row_ptr<T>(a.k, t.token, t.head)) + ch * sizeof(T));
+    if (put_v)
+        v.store(const_cast<char *>(row_ptr<T>(a.v, t.token, t.head)) + ch * sizeof(T));
 }
 
 template <typename T, int N> hipError_t launch(const CacheArgs &a, bool load, hipStream_t s)

@@ -382,7 +382,7 @@ __global__ __launch_bounds__(kChunk) void fork_kernel(PagesArgs a, ForkState f)
 
     // shared entries, and what they change in the counts
     const int entries = max(a.rows_in, a.rows_out) * a.width;
-    constexpr int AT_ONCE = 4;
+    constexpr int AT_ONCE = 8;
     for (int e0 = tid; e0 < entries; e0 += AT_ONCE * kChunk) {
         int old[AT_ONCE], now[AT_ONCE];
 #pragma unroll
@@ -434,11 +434,11 @@ __global__ __launch_bounds__(kChunk) void fork_kernel(PagesArgs a, ForkState f)
     __syncthreads();
     for (int p = tid; p < a.pool.pages; p += kChunk)
         a.owners_out[p] = l.counts[p];
-    const int lane = tid & 63;
-    for (int i = tid >> 6; i < a.rows_out; i += kWavesOfChunk) {
+    constexpr int LANES = 16;                    // of a row: few have more pages to take
+    for (int i = tid / LANES; i < a.rows_out; i += kChunk / LANES) {
         const int4 r = l.rows[i];
         const int held = r.y & INT32_MAX, own = r.y < 0 ? 1 : 0;
-        for (int k = lane; k < own + max(0, r.z - held); k += 64) {
+        for (int k = tid % LANES; k < own + max(0, r.z - held); k += LANES) {
             const int p = r.w + k < take ? l.list[r.w + k] : -1;
             a.table_out[i * a.width + held - own + k] = p;
             if (own && k == 0)

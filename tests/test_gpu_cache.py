@@ -146,8 +146,14 @@ def test_tokens_without_a_page_and_of_no_sequence():
     torch.testing.assert_close(torch.stack((gk, gv)).cpu().double(), want, rtol=0, atol=0)
     k0, v0 = (torch.full((40, heads, dim), 3.0, device="cuda") for _ in range(2))
     K.load(op, there, *args, 40, torch.float32, k=k0, v=v0)
-    want[:, :2] = want[:, 36:] = 3.0
-    torch.testing.assert_close(torch.stack((k0, v0)).cpu().double(), want, rtol=0, atol=0)
+    given = want.clone()
+    given[:, :2] = given[:, 36:] = 3.0
+    torch.testing.assert_close(torch.stack((k0, v0)).cpu().double(), given, rtol=0, atol=0)
+    k0.fill_(3.0)                                     # one given, the other allocated
+    k1, v1 = K.load(op, there, *args, 40, torch.float32, k=k0)
+    assert k1 is k0
+    torch.testing.assert_close(k0.cpu().double(), given[0], rtol=0, atol=0)
+    torch.testing.assert_close(v1.cpu().double(), want[1], rtol=0, atol=0)
 
 
 # ---------------------------------------------------------------- attention
@@ -396,3 +402,8 @@ def test_copy(layers, count, size):
     want = a[:, :25].clone()
     want[:, 5:7] = want[:, 3:5]
     assert torch.equal(pool.cpu(), want)
+    flat = a[0].cuda()                                # and to pages past those of a part of it
+    K.copy_pages(flat[:5], flat, ints([2, 4]), ints([29, 9]))
+    want = a[0].clone()
+    want[29], want[9] = a[0][2], a[0][4]
+    assert torch.equal(flat.cpu(), want)
