@@ -19,13 +19,15 @@ MdcnError on bad arguments.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
 from . import attention as _a
 from . import mdcn as _m
-from .attention import (_NO_CONTEXT, _check_ints, _check_lse, _check_view, _device_tensors, _fail,
-                        _like, _new, _remember, _sig, _stream_of, _strides, _workspace_bytes)
+from .attention import (_NO_CONTEXT, _check_current, _check_ints, _check_lse, _check_view,
+                        _device_tensors, _fail, _like, _new, _remember, _sig, _stream_of, _strides,
+                        _workspace_bytes)
 from .mdcn import MDCN_E_ATTR
 
 _i64 = ctypes.c_int64
@@ -58,6 +60,9 @@ def mdcn_cache_create(k_heads: int, dim: int, page: int) -> Cache:
 
 
 # ---------------------------------------------------------------- checks
+#
+# What a call's checks depend on is its key: shapes, strides, types and devices.  A key that
+# passed them before needs only the current device looked at.
 
 def _check_bytes(where, name, pool, like, dims):
     if pool.dtype != torch.uint8 or pool.device != like.device or pool.dim() not in dims:
@@ -103,10 +108,12 @@ def store(op: Cache, pool, k, v, table, used, cu, stream=None):
     int32 [rows + 1]) into their pages: sequence b's become its last tokens, up to
     used[b] - 1."""
     where = "store"
-    _device_tensors(where, k, v, pool, table, used, cu)
     key = (_sig(pool), _sig(k), _sig(v), _sig(table), _sig(used), _sig(cu))
     call = op.calls.get(key)
-    if call is None:
+    if call is not None:
+        _check_current(where, k.get_device())
+    else:
+        _device_tensors(where, k, v, pool, table, used, cu)
         call = _remember(op.calls, key, _cache_dims(
             op, where, pool, table, used, cu, k, k.shape[0],
             (("k", k, op.k_heads), ("v", v, op.k_heads))))
@@ -123,11 +130,14 @@ def load(op: Cache, pool, table, used, cu, tokens: int, dtype, k=None, v=None, s
     them: (k, v), [tokens, k_heads, dim].  Tokens without a page are zeros, and so are those of
     no sequence, but in a k or v that the caller gives they are left as they are."""
     where = "load"
-    _device_tensors(where, pool, table, used, cu)
-    stream, ctx = _stream_of(stream, pool)
     key = (_sig(pool), _sig(table), _sig(used), _sig(cu), tokens, dtype,
            None if k is None else _sig(k), None if v is None else _sig(v))
     call = op.calls.get(key)
+    if call is not None:
+        _check_current(where, pool.get_device())
+    else:
+        _device_tensors(where, pool, table, used, cu)
+    stream, ctx = _stream_of(stream, pool)
     with ctx or _NO_CONTEXT:
         if call is None:
             like = _like((tokens, op.k_heads, op.dim), dtype, pool.device)
@@ -156,15 +166,19 @@ def attend(att: _a.Attention, op: Cache, q, pool, table, used, cu_q, out=None, l
     """attention.attend against the cache: the queries of sequence b (q [q_tokens, q_heads, dim],
     cu_q int32 [rows + 1]) attend to its used[b] tokens.  Returns (out, lse)."""
     where = "attend"
-    _device_tensors(where, q, pool, table, used, cu_q)
     lib = _m._lib
+    key = (att.q_heads, att.k_heads, att.dim, _sig(q), None if out is None else _sig(out),
+           _sig(pool), _sig(table), _sig(used), _sig(cu_q))
+    call = op.calls.get(key)
+    if call is not None:
+        _check_current(where, q.get_device())
+    else:
+        _device_tensors(where, q, pool, table, used, cu_q)
     stream, ctx = _stream_of(stream, q)
     fill = (1 if out is None else 0) | (2 if lse is None else 0)
     with ctx or _NO_CONTEXT:
         if out is None:
             out = torch.empty_like(q)
-        key = (att.q_heads, att.k_heads, att.dim, _sig(q), _sig(out), _sig(pool), _sig(table), _sig(used), _sig(cu_q))
-        call = op.calls.get(key)
         if call is None:
             if att.k_heads != op.k_heads or att.dim != op.dim:
                 _fail(where, "attention and cache must agree in key heads and dim", MDCN_E_ATTR)
@@ -219,10 +233,34 @@ def _contiguous_ints(where, name, t, like, shape):
         _fail(where, "%s must be contiguous" % name)
 
 
-def _page_workspace(where, function, dims, like):
-    n = ctypes.c_size_t()
-    _m._check(function(dims, ctypes.byref(n)), where)
-    return _like((n.value,), torch.uint8, like.device)
+class _Results:
+    """The results of a page operator and its workspace.  Where the caller gives none of them they
+    are parts of one allocation (2 us a call less than five)."""
+
+    def __init__(self, where, function, dims, like, names, shapes):
+        n = ctypes.c_size_t()
+        _m._check(function(dims, ctypes.byref(n)), where)
+        self.where, self.names, self.shapes = where, names, shapes
+        self.sizes = [-(-math.prod(s) // 4) * 4 for s in shapes] + [-(-n.value // 4)]
+        self.all = _like((sum(self.sizes),), torch.int32, like.device)
+        self.exact = [size == math.prod(s) and len(s) == 1 for size, s in zip(self.sizes, shapes)]
+
+    def make(self, given, workspace, like):
+        """(the results, the workspace)"""
+        parts = None
+        if workspace is None or any(t is None for t in given):
+            parts = _new(self.all).split_with_sizes(self.sizes)
+        results = []
+        for i, t in enumerate(given):
+            shape = self.shapes[i]
+            if t is not None:
+                _contiguous_ints(self.where, self.names[i], t, like, shape)
+            elif self.exact[i]:
+                t = parts[i]
+            else:
+                t = parts[i].as_strided(shape, (shape[-1], 1)[-len(shape):])
+            results.append(t)
+        return results, parts[-1] if workspace is None else workspace
 
 
 def fork_pages(pool, table, used, owners, page: int, parents=None, new_tokens=None, table_out=None,
@@ -233,15 +271,16 @@ def fork_pages(pool, table, used, owners, page: int, parents=None, new_tokens=No
     up.  Returns (table, used, owners, missing): missing int32 [1] is 0, or how many pages there
     are too few, and then nothing was copied and the old table still holds."""
     where = "fork_pages"
-    _device_tensors(where, table, used, owners, *(() if pool is None else (pool,)),
-                    *(() if parents is None else (parents,)),
-                    *(() if new_tokens is None else (new_tokens,)))
     lib = _m._lib or _m.library()
     key = (where, None if pool is None else _sig(pool), _sig(table), _sig(used), _sig(owners), page,
            None if parents is None else _sig(parents),
            None if new_tokens is None else _sig(new_tokens))
     call = _page_calls.get(key)
-    if call is None:
+    if call is not None:
+        _check_current(where, table.get_device())
+    else:
+        _device_tensors(where, table, used, owners,
+                        *(t for t in (pool, parents, new_tokens) if t is not None))
         if table.dim() != 2 or owners.dim() != 1:
             _fail(where, "table must be [rows, width], owners [pages]")
         rows, width = table.shape
@@ -258,20 +297,12 @@ def fork_pages(pool, table, used, owners, page: int, parents=None, new_tokens=No
                 _contiguous_ints(where, name, t, table, (out_rows,))
         dims = (_i64 * 9)(*dims, page, rows, out_rows, width)
         call = _remember(_page_calls, key, (
-            dims, _page_workspace(where, lib.mdcn_pages_fork_workspace_bytes, dims, table),
-            tuple(_like(shape, torch.int32, table.device)
-                  for shape in ((out_rows, width), (out_rows,), tuple(owners.shape), (1,)))))
+            dims, _Results(where, lib.mdcn_pages_fork_workspace_bytes, dims, table,
+                           ("table_out", "used_out", "owners_out", "missing"),
+                           ((out_rows, width), (out_rows,), tuple(owners.shape), (1,)))))
     stream, ctx = _stream_of(stream, table)
-    results = [table_out, used_out, owners_out, missing]
     with ctx or _NO_CONTEXT:
-        for i, (t, like) in enumerate(zip(results, call[2])):
-            if t is None:
-                results[i] = _new(like)
-            else:
-                _contiguous_ints(where, ("table_out", "used_out", "owners_out", "missing")[i], t, table,
-                                 tuple(like.shape))
-        if workspace is None:
-            workspace = _new(call[1])
+        results, workspace = call[1].make((table_out, used_out, owners_out, missing), workspace, table)
     st = lib.mdcn_pages_fork(
         call[0], None if pool is None else pool.data_ptr(), table.data_ptr(), used.data_ptr(),
         owners.data_ptr(), None if parents is None else parents.data_ptr(),
@@ -287,11 +318,13 @@ def compact_pages(pool, table, owners, table_out=None, owners_out=None, moved=No
     """Moves the n held pages to the numbers 0 .. n - 1.  Returns (table, owners, moved) with
     the new numbers; moved int32 [pages]: the new number of each page, -1 if it is free."""
     where = "compact_pages"
-    _device_tensors(where, pool, table, owners)
     lib = _m._lib or _m.library()
     key = (where, _sig(pool), _sig(table), _sig(owners))
     call = _page_calls.get(key)
-    if call is None:
+    if call is not None:
+        _check_current(where, table.get_device())
+    else:
+        _device_tensors(where, pool, table, owners)
         if table.dim() != 2:
             _fail(where, "table must be [rows, width]")
         _contiguous_ints(where, "table", table, table, tuple(table.shape))
@@ -299,19 +332,12 @@ def compact_pages(pool, table, owners, table_out=None, owners_out=None, moved=No
         _contiguous_ints(where, "owners", owners, table, (dims[1],))
         dims = (_i64 * 7)(*dims, *table.shape)
         call = _remember(_page_calls, key, (
-            dims, _page_workspace(where, lib.mdcn_pages_compact_workspace_bytes, dims, table),
-            tuple(_like(tuple(t.shape), torch.int32, table.device) for t in (table, owners, owners))))
+            dims, _Results(where, lib.mdcn_pages_compact_workspace_bytes, dims, table,
+                           ("table_out", "owners_out", "moved"),
+                           (tuple(table.shape), tuple(owners.shape), tuple(owners.shape)))))
     stream, ctx = _stream_of(stream, table)
-    results = [table_out, owners_out, moved]
     with ctx or _NO_CONTEXT:
-        for i, (t, like) in enumerate(zip(results, call[2])):
-            if t is None:
-                results[i] = _new(like)
-            else:
-                _contiguous_ints(where, ("table_out", "owners_out", "moved")[i], t, table,
-                                 tuple(like.shape))
-        if workspace is None:
-            workspace = _new(call[1])
+        results, workspace = call[1].make((table_out, owners_out, moved), workspace, table)
     st = lib.mdcn_pages_compact(
         call[0], pool.data_ptr(), table.data_ptr(), owners.data_ptr(),
         *(t.data_ptr() for t in results), workspace.data_ptr(),
@@ -325,10 +351,12 @@ def copy_pages(src_pool, dst_pool, src, dst, stream=None):
     """Copies page src[i] of one pool to page dst[i] of another, or of the same one, in every
     layer.  Pairs with a number outside its pool are passed over."""
     where = "copy_pages"
-    _device_tensors(where, src_pool, dst_pool, src, dst)
     key = (where, _sig(src_pool), _sig(dst_pool), _sig(src), _sig(dst))
     call = _page_calls.get(key)
-    if call is None:
+    if call is not None:
+        _check_current(where, src.get_device())
+    else:
+        _device_tensors(where, src_pool, dst_pool, src, dst)
         if src.dim() != 1:
             _fail(where, "src and dst must be lists of pages")
         _contiguous_ints(where, "src", src, src, tuple(src.shape))

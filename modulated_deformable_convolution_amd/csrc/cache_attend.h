@@ -12,7 +12,7 @@
 // Values of one byte are two channels of one token (one exponent); two converted tokens
 // are regrouped by channel with two permutes.  fp32 queries and probabilities are
 // split into three bf16 parts (products with fp4 values are exact in fp32): 2^-24, at a
-// sixth of the time of fp32 MFMA.
+// fifth of the time of fp32 MFMA.
 #pragma once
 
 #include "cache_common.h"
