@@ -407,3 +407,28 @@ def test_copy(layers, count, size):
     want = a[0].clone()
     want[29], want[9] = a[0][2], a[0][4]
     assert torch.equal(flat.cpu(), want)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_many_queries_pass_over_missing_pages_and_hidden_nans(dt):
+    hq, hk, dim, page, dtype, new = 4, 2, 40, 16, DTYPES[dt], 90
+    gen = torch.Generator().manual_seed(21)
+    op, pool = filled(gen, hk, dim, page, 12, dtype)
+    there, n = pool.cuda(), 170
+    table = torch.tensor([[0, 1, -1, 3, 12, 5, 6, -9, 8, 9, 10]], dtype=torch.int32)
+    bad = normal(gen, 1, hk, dim, dtype=dtype)        # token 150 is a NaN in head 0
+    bad[0, 0, 17] = math.nan
+    K.store(op, there, bad.cuda(), bad.cuda(), table.cuda(), ints([151]), ints([0, 1]))
+    att = A.mdcn_attention_create(hq, hk, dim, True)
+    assert K.describe_attend(att, op, dtype, 1, new, 11).startswith("tile")
+    q = normal(gen, new, hq, dim, dtype=dtype)
+    out, lse = K.attend(att, op, q.cuda(), there, table.cuda(), ints([n]), ints([0, new]))
+    k, v, held = C.tokens(there.cpu(), hk, dim, page, table, 0, range(n))
+    out, lse = out.cpu(), lse.cpu()
+    for i in range(new):
+        see = held & (torch.arange(n) <= n - new + i)
+        r = R.attend(q[i:i + 1], k[see], v[see], [0, 1], [0, int(see.sum())], None, False, att.scale, dtype)
+        within(out[i:i + 1], r["out"], "out %d" % i)
+        nan = [n - new + i >= 150] * 2 + [False] * 2
+        assert lse[:, i].isnan().tolist() == nan
+        within(lse[2:, i:i + 1], [x[2:] for x in r["lse"]], "lse %d" % i)
