@@ -181,6 +181,7 @@ __device__ void fork_first(const PagesArgs &a, const ForkState &f, const Team &t
 {
     for (int i = t.tid; i < a.rows_out; i += t.n) {
         const ForkRow r = fork_row(a, i);
+        a.used_out[i] = int(min(int64_t(r.used) + r.new_tokens, int64_t(a.width) * a.page));
         if (r.parent >= 0)
             atomicMin(f.first + r.parent, i);
     }
@@ -202,8 +203,6 @@ __device__ void fork_share(const PagesArgs &a, const ForkState &f, const Team &t
             if (!is_page(a, now))
                 now = -1;
             a.table_out[e] = now;
-            if (j == 0)
-                a.used_out[i] = int(min(int64_t(r.used) + r.new_tokens, int64_t(a.width) * a.page));
         }
         if (old != now) {
             if (is_page(a, old))
