@@ -529,8 +529,8 @@ mdcn_status mdcn_describe_cache_attend(const mdcn_attention *att, const mdcn_cac
  *   table_out [rows][width] (-1: no page), used_out = used + new tokens (of the parent),
  *   owners_out: owners less the table's entries plus table_out's.
  *   missing: int32 [1], 0, or how many pages there are too few in the pool and the
- *   table's width; then nothing is copied, entries without a page are -1, and the inputs
- *   still stand for what the pool holds.
+ *   table's width (2^31 - 1 if more); then nothing is copied, entries without a page are
+ *   -1, and the inputs still stand for what the pool holds.
  * Without a copy to make the pool may be NULL if `layers` is 0.
  * Errors: MDCN_E_NULL, MDCN_E_SHAPE, MDCN_E_ALIAS, MDCN_E_WORKSPACE, MDCN_E_DEVICE, MDCN_E_LAUNCH. */
 mdcn_status mdcn_pages_fork_workspace_bytes(const int64_t dims[9], size_t *bytes);

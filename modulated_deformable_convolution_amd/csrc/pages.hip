@@ -135,7 +135,7 @@ struct ForkRow {
     int parent;            // -1: none
     int used, held, wants; // tokens and pages of the parent, pages of the result (used and
                            // new tokens count in 32 bits: a row holds 2^30 tokens at most)
-    int excess;            // pages that the table has no room for
+    int excess;            // pages that the table has no room for (never more than new ones)
     int new_tokens;
     bool own;              // the last page held is a copy
 };
@@ -151,7 +151,7 @@ __device__ __forceinline__ ForkRow fork_row(const PagesArgs &a, int i)
     r.held = int((uint32_t(r.used) + a.page - 1) / uint32_t(a.page));
     const uint32_t all = (uint32_t(r.used) + uint32_t(r.new_tokens) + a.page - 1) / uint32_t(a.page);
     r.wants = int(min(all, uint32_t(a.width)));
-    r.excess = int(all) - r.wants;
+    r.excess = int(all - uint32_t(r.wants));
     r.own = false;
     return r;
 }
@@ -227,16 +227,20 @@ __device__ void fork_count(const PagesArgs &a, const ForkState &f, const Team &t
 // One workgroup: what comes before each row and each chunk.
 __device__ void fork_scan(const PagesArgs &a, const ForkState &f, int *lds)
 {
+    __shared__ unsigned long long excess;        // of a few rows may pass 32 bits
     int fresh = 0, copies = 0, free = 0, all;
-    int64_t excess = 0;
+    if (threadIdx.x == 0)
+        excess = 0;
+    __syncthreads();
     for (int i0 = 0; i0 < a.rows_out; i0 += kChunk) {
         const int i = i0 + int(threadIdx.x);
-        int n = 0, own = 0, over = 0;
+        int n = 0, own = 0;
         if (i < a.rows_out) {
             const ForkRow r = fork_row(a, i);
             own = copies_last(a, f, r, i) ? 1 : 0;
             n = own + max(0, r.wants - r.held);
-            over = r.excess;
+            if (r.excess)
+                atomicAdd(&excess, (unsigned long long)r.excess);
         }
         const int upto = group_scan(n, lds, all);
         if (i < a.rows_out)
@@ -246,8 +250,6 @@ __device__ void fork_scan(const PagesArgs &a, const ForkState &f, int *lds)
         if (i < a.rows_out)
             f.copies[i] = copies + made - own;
         copies += all;
-        group_scan(over, lds, all);
-        excess += all;
     }
     const int chunks = (a.pool.pages + kChunk - 1) / kChunk;
     for (int c0 = 0; c0 < chunks; c0 += kChunk) {
@@ -258,9 +260,10 @@ __device__ void fork_scan(const PagesArgs &a, const ForkState &f, int *lds)
             f.chunk[c] = free + upto - n;
         free += all;
     }
+    __syncthreads();
     if (threadIdx.x == 0) {
-        const int64_t missing = max(0, fresh - free) + excess;
-        a.missing[0] = int(min(missing, int64_t(INT32_MAX)));
+        const unsigned long long missing = excess + max(0, fresh - free);
+        a.missing[0] = missing < INT32_MAX ? int(missing) : INT32_MAX;
         f.totals[0] = missing ? 0 : copies;
         f.totals[1] = min(fresh, free);
     }
