@@ -26,17 +26,20 @@ constexpr int kItemCost = 3;
 
 // Units of the items of one (sequence, key head), item i being rows 16 kWaves R i and on:
 // what they see grows evenly under a causal mask, so the units before an item are a
-// quadratic of its index.  In 64-bit floating point: the inner sum is exact, so every workgroup
+// quadratic of its index, counted from the first item that sees a token at all: with more queries
+// than tokens the earlier ones are `blind`.  So there are never more units than the host
+// allows for (most_units).  In 64-bit floating point: the inner sum is exact, so every workgroup
 // comes to the same whole numbers, however the operations are fused, and they grow with the index.
 template <int R> struct Ladder {
     static constexpr int ROWS = 16 * kWaves * R;
     double first, step, per;
-    int tiles;
+    int tiles, blind;
 
     __device__ __forceinline__ Ladder(const CacheArgs &a, const Piece &pc)
     {
         const int shared = a.q_heads / a.k_heads;
         tiles = int((uint32_t(pc.lq) * uint32_t(shared) + ROWS - 1) / ROWS);
+        blind = a.causal ? int(uint32_t(max(pc.lq - pc.lk, 0)) * uint32_t(shared) / ROWS) : 0;
         step = a.causal ? double(ROWS) : 0.0;
         first = double(a.causal ? max(pc.lk - pc.lq, 0) : pc.lk) * shared + step;
         per = 1.0 / (2.0 * shared * double(kRound << a.unit_shift));
@@ -44,7 +47,8 @@ template <int R> struct Ladder {
 
     __device__ __forceinline__ int before(int i) const
     {
-        return kItemCost * i + int(double(i) * (2.0 * first + double(i - 1) * step) * per);
+        const int n = max(i - blind, 0);
+        return kItemCost * i + int(double(n) * (2.0 * first + double(n - 1) * step) * per);
     }
 
     __device__ __forceinline__ int item_of(int unit) const
