@@ -491,7 +491,8 @@ mdcn_status mdcn_cache_load(const mdcn_cache *op, mdcn_dtype dtype, const int64_
  * mdcn_attend_filled.  Keys and values are exact in the products; queries are too (fp32
  * ones as three bf16 parts: beyond 3.39e38 NaN), probabilities are rounded to the inputs' type
  * (fp32: to three bf16 parts, 2^-24).  The same bits in every call.
- * Errors as for mdcn_attend. */
+ * Errors as for mdcn_attend; MDCN_E_SHAPE also for batches of more than about 1.5 * 10^8 items
+ * of work (up to 16 to 128 rows of one sequence and key head each), which are counted in 31 bits. */
 mdcn_status mdcn_cache_attend_workspace_bytes(const mdcn_attention *att, const mdcn_cache *op,
                                               mdcn_dtype dtype, const int64_t dims[10],
                                               size_t *bytes);

@@ -75,6 +75,8 @@ struct CacheShape {
     int rows, workers, unit;
 };
 CacheShape cache_attend_shape(mdcn_dtype dtype, const CacheArgs &a);
+// Whether the kernels can count the batch's work in 31 bits.
+bool cache_attend_countable(mdcn_dtype dtype, const CacheArgs &a);
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a);
 hipError_t launch_cache_attend(mdcn_dtype dtype, CacheArgs a, void *workspace, hipStream_t s);
 

@@ -132,7 +132,7 @@ mdcn_status attend_args(const mdcn_attention *att, const mdcn_cache *op, mdcn_dt
     a->q_heads = att->q_heads;
     a->causal = att->causal;
     a->scale = att->scale;
-    return MDCN_OK;
+    return cache_attend_countable(dtype, *a) ? MDCN_OK : MDCN_E_SHAPE;
 }
 
 // ---- pages -----------------------------------------------------------------

@@ -437,13 +437,14 @@ template <typename T> hipError_t launch_blocks(const CacheArgs &a, int tiles, hi
 
 }  // namespace
 
-// Units of a batch, at most: (row tiles) x (key heads) x (units of all tokens).
-static double most_units(const CacheArgs &a, int tiles, int shift)
+// Units of a batch with queries in `sequences` sequences, at most: (row tiles) x (key heads) x
+// (units of all tokens).
+static double most_units(const CacheArgs &a, int tiles, int shift, int sequences)
 {
     const int tokens = (tiles > 2 ? 64 : kTile) << shift;
     const double rows = double(a.tokens) * (a.q_heads / a.k_heads);
     const double keys = double(a.width) * (1 << a.page_shift) / tokens;
-    return (rows / (16 * tiles) + a.batch) * a.k_heads * (keys + kItemCost + 1);
+    return (rows / (16 * tiles) + sequences) * a.k_heads * (keys + kItemCost + 1);
 }
 
 CacheShape cache_attend_shape(mdcn_dtype dtype, const CacheArgs &a)
@@ -451,12 +452,21 @@ CacheShape cache_attend_shape(mdcn_dtype dtype, const CacheArgs &a)
     const int tiles = row_tiles(dtype, a);
     const int most = tiles > 2 ? kTileWorkers : 256 * (tiles == 2 ? 2 : dtype == MDCN_F32 ? 3 : 4);
     int shift = 0;
-    while (most_units(a, tiles, shift) > 1e9 && shift < 20)
+    while (most_units(a, tiles, shift, a.batch) > 1e9 && shift < 20)
         ++shift;
     // no more workgroups than a small batch has work for; none: rows to fill only
     const int workers =
-        int(std::min<double>(most, std::ceil(most_units(a, tiles, shift) / kWaves)));
+        int(std::min<double>(most, std::ceil(most_units(a, tiles, shift, a.batch) / kWaves)));
     return CacheShape{16 * tiles, a.batch ? workers : 0, (tiles > 2 ? 64 : kTile) << shift};
+}
+
+// What an item costs does not shrink with longer units: enough items pass any count.
+bool cache_attend_countable(mdcn_dtype dtype, const CacheArgs &a)
+{
+    const CacheShape c = cache_attend_shape(dtype, a);
+    const int tiles = c.rows / 16;
+    const int shift = __builtin_ctz(unsigned(c.unit / (tiles > 2 ? 64 : kTile)));
+    return most_units(a, tiles, shift, std::min(a.batch, a.tokens)) <= 2e9;
 }
 
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a)
