@@ -282,35 +282,31 @@ struct Row16 {
     }
 };
 
-// Outputs of blocks b0 .. b0 + M / 2 - 1 of a finished row, and its lse.
-template <typename T, int M>
-__device__ __forceinline__ void finish(const CacheArgs &a, const State<M> &s, const Row16 &at,
-                                       int b0, int lane)
+// Channels 32 j + 8 (lane / 16) and on of the lane's row.
+template <typename T>
+__device__ __forceinline__ Parts<T> query_of(const CacheArgs &a, const Row16 &r, int j, int lane)
 {
-    const int token = at.token, head = at.head, group = lane >> 4;
-    const float sum = sum_groups(s.l);
-    if (!at.live)
-        return;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    char *row = const_cast<char *>(row_ptr<T>(a.out, token, head));
+    const int ch = j * 32 + (lane >> 4) * 8;
+    float v[8] = {};
+    if (r.live && ch < a.dim) {
+        struct alignas(16) {
+            T e[8];
+        } x;
+        const char *p = row_ptr<T>(a.q, r.token, r.head) + ch * sizeof(T);
+        __builtin_memcpy(&x, __builtin_assume_aligned(p, 16), sizeof(x));
 #pragma unroll
-    for (int b = 0; b < M / 2; ++b) {
-        const int ch = (b0 + b) * 32 + group * 8;
-        if (ch < a.dim) {
-            struct alignas(16) {
-                T e[8];
-            } v;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = s.o[2 * b + (i & 1)][i >> 1];
-                v.e[i] = from_f32<T>(sum == 0.0f ? 0.0f : sizeof(T) == 4 ? o / sum : o * inv);
-            }
-            __builtin_memcpy(__builtin_assume_aligned(row + ch * sizeof(T), 16), &v, sizeof(v));
-        }
+        for (int e = 0; e < 8; ++e)
+            v[e] = to_f32(x.e[e]);
     }
-    if (b0 == 0 && group == 0)
-        a.lse[int64_t(head) * a.tokens + token] =
-            sum == 0.0f ? -INFINITY : row_lse<T>(s.m, sum, a.scale);
+    Parts<T> q;
+    q.set(v);
+    return q;
+}
+
+// The last token that a row sees.
+__device__ __forceinline__ int last_of(const CacheArgs &a, const Piece &pc, const Row16 &r)
+{
+    return !r.live ? -1 : a.causal ? r.row + pc.lk - pc.lq : pc.lk - 1;
 }
 
 // The queries of a row tile, and the last token that each row sees.
@@ -322,23 +318,10 @@ template <typename T, int N> struct RowTile {
                                          uint32_t index, int lane)
     {
         const Row16 r(a, pc.q0, pc.lq, kv_head, index, lane);
-        last = !r.live ? -1 : a.causal ? r.row + pc.lk - pc.lq : pc.lk - 1;
+        last = last_of(a, pc, r);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int ch = j * 32 + (lane >> 4) * 8;
-            float v[8] = {};
-            if (r.live && ch < a.dim) {
-                struct alignas(16) {
-                    T e[8];
-                } x;
-                const char *p = row_ptr<T>(a.q, r.token, r.head) + ch * sizeof(T);
-                __builtin_memcpy(&x, __builtin_assume_aligned(p, 16), sizeof(x));
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = to_f32(x.e[e]);
-            }
-            q[j].set(v);
-        }
+        for (int j = 0; j < N; ++j)
+            q[j] = query_of<T>(a, r, j, lane);
     }
 };
 
@@ -355,6 +338,119 @@ struct Sight {
         any = low >= pc.lq ? -1 : a.causal ? min(high, pc.lq - 1) + pc.lk - pc.lq : pc.lk - 1;
     }
 };
+
+// 8 channels of an output from two tiles of sums and the sum of weights.
+template <typename T>
+__device__ __forceinline__ void put_block(const CacheArgs &a, const Row16 &at, int b, float4v even,
+                                          float4v odd, float sum, int lane)
+{
+    const int ch = b * 32 + (lane >> 4) * 8;
+    if (ch >= a.dim)
+        return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    struct alignas(16) {
+        T e[8];
+    } v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float o = i & 1 ? odd[i >> 1] : even[i >> 1];
+        v.e[i] = from_f32<T>(sum == 0.0f ? 0.0f : sizeof(T) == 4 ? o / sum : o * inv);
+    }
+    char *row = const_cast<char *>(row_ptr<T>(a.out, at.token, at.head));
+    __builtin_memcpy(__builtin_assume_aligned(row + ch * sizeof(T), 16), &v, sizeof(v));
+}
+
+// Sums of fp32 and bf16 values may pass the type's range where their mean does not: the
+// format goes to 6 * 2^125, the type to 1.3 times that, and weights to 2^8 each.  A power of two taken
+// off them would cost the smallest values their bits (2^-121, of 2^-149), so rows whose
+// sums of values are not finite, while those of weights are, are `lost`: the second kernel
+// computes them again, as means (put_mean).  (fp16: 2^16 * 2^15 a token at most.)
+//
+// Outputs of blocks b0 .. b0 + M / 2 - 1 of a finished row tile, and its lse; whether a row is lost.
+template <typename T, int M>
+__device__ __forceinline__ bool finish(const CacheArgs &a, const State<M> &s, const Row16 &at, int b0,
+                                       int lane, float &lse)
+{
+    const float sum = sum_groups(s.l);
+    lse = sum == 0.0f ? -INFINITY : row_lse<T>(s.m, sum, a.scale);
+    bool lost = false;
+    if (at.live) {
+        if constexpr (!__is_same(T, half_t)) {
+            float all = 0.0f;                    // NaN if a sum is not finite
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    all = fmaf(s.o[i][j], 0.0f, all);
+            lost = all != all && sum < INFINITY;
+        }
+#pragma unroll
+        for (int b = 0; b < M / 2; ++b)
+            put_block<T>(a, at, b0 + b, s.o[2 * b], s.o[2 * b + 1], sum, lane);
+        if (b0 == 0 && lane < 16)
+            a.lse[int64_t(at.head) * a.tokens + at.token] = lse;
+    }
+    return __ballot(lost) != 0;
+}
+
+// Block b of a row tile once more, from its lse: weights are at most a half, as are their
+// sums, so no sum exceeds the largest value, and small values lose nothing.  Few registers and no
+// LDS, one pair of strips at a time: for values that the format lets happen, not for speed.
+template <typename T, int N>
+__device__ __forceinline__ void put_mean(const CacheArgs &a, const Piece &pc, int sequence, int kv_head,
+                                         uint32_t tile, const Row16 &at, float lse, int b, int lane)
+{
+    constexpr Strip S{N};
+    const float c = a.scale * kLog2e, off = lse == -INFINITY ? 0.0f : fmaf(lse, kLog2e, 1.0f);
+    const int last = last_of(a, pc, at), any = Sight(a, pc, tile, 1).any;
+    const int strip_shift = a.page_shift - 4, held = (pc.lk + (1 << a.page_shift) - 1) >> a.page_shift;
+    const int32_t *const pages = a.table + sequence * a.table_stride;
+    const char *const heads = a.pool + int64_t(kv_head << strip_shift) * S.bytes();
+    float4v even = {}, odd = {};
+    float sum = 0.0f;
+    for (int t = 0; t * 32 <= any; ++t) {
+        asm volatile("" ::: "memory");           // queries are read again, not held
+        float w[8];
+        uint32_t ev[2][2], od[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int strip = 2 * t + i, tok = strip * 16 + (lane >> 4) * 4;
+            const int page = pages[min(strip >> strip_shift, held - 1)];
+            const bool gone = page < 0 || page >= a.pages;
+            const char *const p = heads + int64_t(gone ? 0 : page) * a.page_stride +
+                                  (strip & ((1 << strip_shift) - 1)) * S.bytes();
+            Raw<1> x;                            // one block of keys, then of values
+            float4v sc = {};
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) {
+                x.k.w[0] = *reinterpret_cast<const uint32_t *>(p + (lane * N + j) * 4);
+                x.ke = uint8_t(p[S.key_exps() + (lane & 15) * S.key_exp() + j]);
+                sc = product<T>(key_operand<T, 1>(x, 0), query_of<T>(a, at, j, lane), sc);
+            }
+            x.v.w[0] = *reinterpret_cast<const uint32_t *>(p + S.values() + (lane * N + b) * 4);
+            x.ve.w[0] = *reinterpret_cast<const uint32_t *>(p + S.value_exps() +
+                                                            ((lane >> 4) * N + b) * 4);
+            settle_values(x, gone ? 0 : pc.lk - tok);
+            value_halves<T, 1>(x, 0, ev[i], od[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[4 * i + e] =
+                    gone || tok + e > last ? 0.0f : __builtin_amdgcn_exp2f(fmaf(sc[e], c, -off));
+                sum += w[4 * i + e];
+            }
+        }
+        Parts<T> weights;
+        weights.set(w);
+        Vec<T> ve, vo;
+        __builtin_memcpy(&ve, ev, 16);
+        __builtin_memcpy(&vo, od, 16);
+        even = product<T>(ve, weights, even);
+        odd = product<T>(vo, weights, odd);
+    }
+    sum = sum_groups(sum);
+    if (at.live)
+        put_block<T>(a, at, b, even, odd, sum, lane);
+}
 
 // Fills rows of no sequence: the workgroups past `workers`.
 template <typename T> __device__ __forceinline__ void fill_rows(const CacheArgs &a)
@@ -394,12 +490,22 @@ struct Share {
     }
 };
 
-// What the second kernel is to join: the item that begins in a workgroup's range
-// and does not end there.
+// What the second kernel is to do: join the item that begins in a workgroup's range
+// and does not end there, and compute again those that begin and end in it, if rows are lost.
 struct Join {
-    int q0, lq, head, tile;
+    int q0, lq, lk, sequence, head, tile;
     int last;                                    // workgroup of its last part, -1: nothing
-    int pad[3];
+    int lost;
+
+    __device__ __forceinline__ void init() { last = -1, lost = 0; }
+
+    __device__ __forceinline__ void set(const Piece &p, int sequence_, int head_, int tile_, int last_)
+    {
+        q0 = p.q0, lq = p.lq, lk = p.lk;
+        sequence = sequence_, head = head_, tile = tile_, last = last_;
+    }
+
+    __device__ __forceinline__ Piece piece() const { return Piece{q0, lq, lk}; }
 };
 
 // A part in the workspace: registers as they are, [row tile][2 n + m and l][lane].

@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kern
     const Share share(units, a.workers);
     Join *join = reinterpret_cast<Join *>(a.joins) + blockIdx.x;
     if (threadIdx.x == 0)
-        join->last = -1;
+        join->init();
     if (int(blockIdx.x) >= share.n)
         return;
     __syncthreads();                             // another wave may write it below
@@ -322,11 +322,17 @@ __global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kern
                 }
                 if (alone || wave == 0) {
                     if (n0 == 0 && n1 == un.keys) {
+                        bool lost = false;
 #pragma unroll
-                        for (int r = 0; r < R; ++r)
-                            finish<T, 2 * N>(
+                        for (int r = 0; r < R; ++r) {
+                            float lse;
+                            lost |= finish<T, 2 * N>(
                                 a, st[r],
-                                Row16(a, pc.q0, pc.lq, kv_head, uint32_t(tile) * R + r, lane), 0, lane);
+                                Row16(a, pc.q0, pc.lq, kv_head, uint32_t(tile) * R + r, lane), 0, lane,
+                                lse);
+                        }
+                        if (lost && lane == 0)
+                            join->lost = 1;
                     } else {
                         float *slot = a.partial + (int64_t(blockIdx.x) * 2 + (n0 == 0 ? 1 : 0)) *
                                                       (R * part_floats<N>());
@@ -334,13 +340,38 @@ __global__ __launch_bounds__(256, (row_waves<T, N, R>())) void cache_attend_kern
                         for (int r = 0; r < R; ++r)
                             put_state(slot + r * part_floats<N>(), st[r], lane);
                         if (n0 == 0 && lane == 0)
-                            *join = Join{pc.q0, pc.lq, kv_head, tile,
-                                         share.owner(i_begin + un.keys - 1), {}};
+                            join->set(pc, b0 + i, kv_head, tile, share.owner(i_begin + un.keys - 1));
                     }
                 }
             }
         }
         base += __builtin_amdgcn_readlane(chunk.upto, 63);
+    }
+}
+
+// Block b of row tile r of the items that workgroup `worker` of the first kernel had to itself once
+// more, as means: its units are counted as there, one sequence after the other.
+template <typename T, int N, int ROWS>
+__device__ __forceinline__ void means_of(const CacheArgs &a, int worker, int r, int b, int wave, int lane)
+{
+    int units = 0;
+    for (int i = lane; i < a.batch; i += 64)
+        units += units_of<ROWS>(a, piece_of(a, i)).all;
+    const Share share(wave_sum(units), a.workers);
+    const int u_begin = share.begin(worker), u_end = share.begin(worker + 1);
+    int base = 0, turn = 0;
+    for (int sequence = 0; sequence < a.batch && base < u_end; ++sequence) {
+        const Piece pc = piece_of(a, sequence);
+        const Units un = units_of<ROWS>(a, pc);
+        for (int i = max(u_begin - base + un.keys - 1, 0) / un.keys;
+             i < un.tiles * a.k_heads && base + (i + 1) * un.keys <= u_end; ++i)
+            if ((turn++ & (kWaves - 1)) == wave) {
+                const uint32_t tile = uint32_t(i % un.tiles) * ROWS + r;
+                const Row16 at(a, pc.q0, pc.lq, i / un.tiles, tile, lane);
+                const float lse = at.live ? a.lse[int64_t(at.head) * a.tokens + at.token] : 0.0f;
+                put_mean<T, N>(a, pc, sequence, i / un.tiles, tile, at, lse, b, lane);
+            }
+        base += un.all;
     }
 }
 
@@ -351,11 +382,14 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
 {
     __shared__ __align__(16) float lds[2 * part_floats<1>()];
     const Join j = reinterpret_cast<const Join *>(a.joins)[blockIdx.x];
-    if (j.last < 0)
-        return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int r = int(blockIdx.y) / N, b = int(blockIdx.y) % N;
+    if constexpr (!__is_same(T, half_t))
+        if (j.lost)
+            means_of<T, N, ROWS>(a, int(blockIdx.x), r, b, wave, lane);
+    if (j.last < 0)
+        return;
     const float c = a.scale * kLog2e;
     const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
 
@@ -383,8 +417,13 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
             st[0].merge(x[n], c);
     }
     join_waves<1, 2>(st, lds, c, wave, lane);
-    if (wave == 0)
-        finish<T, 2>(a, st[0], Row16(a, j.q0, j.lq, j.head, uint32_t(j.tile) * ROWS + r, lane), b, lane);
+    if (wave == 0) {
+        const uint32_t tile = uint32_t(j.tile) * ROWS + r;
+        const Row16 at(a, j.q0, j.lq, j.head, tile, lane);
+        float lse;
+        if (finish<T, 2>(a, st[0], at, b, lane, lse))
+            put_mean<T, N>(a, j.piece(), j.sequence, j.head, tile, at, lse, b, lane);
+    }
 }
 
 // Row tiles of an item, by the rows of an average sequence: one (fp32: of up to 64 rows) or

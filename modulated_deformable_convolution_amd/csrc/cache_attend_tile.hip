@@ -133,7 +133,7 @@ template <typename T, int N, int R> __global__ __launch_bounds__(256, 2) void ca
     const Share share(units, a.workers);
     Join *join = reinterpret_cast<Join *>(a.joins) + blockIdx.x;
     if (threadIdx.x == 0)
-        join->last = -1;
+        join->init();
     if (int(blockIdx.x) >= share.n)
         return;
     const int u_begin = share.begin(int(blockIdx.x)), u_end = share.begin(int(blockIdx.x) + 1);
@@ -293,9 +293,15 @@ template <typename T, int N, int R> __global__ __launch_bounds__(256, 2) void ca
                 }
 
                 if (n0 == 0 && n1 == all) {
+                    bool lost = false;
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        finish<T, 2 * N>(a, st[r], Row16(a, pc.q0, pc.lq, kv_head, first + r, lane), 0, lane);
+                    for (int r = 0; r < R; ++r) {
+                        float lse;
+                        lost |= finish<T, 2 * N>(
+                            a, st[r], Row16(a, pc.q0, pc.lq, kv_head, first + r, lane), 0, lane, lse);
+                    }
+                    if (lost && lane == 0)
+                        join->lost = 1;
                 } else {
                     float *slot = a.partial + ((int64_t(blockIdx.x) * 2 + (n0 == 0 ? 1 : 0)) * kWaves +
                                                wave) * (R * part_floats<N>());
@@ -303,11 +309,43 @@ template <typename T, int N, int R> __global__ __launch_bounds__(256, 2) void ca
                     for (int r = 0; r < R; ++r)
                         put_state(slot + r * part_floats<N>(), st[r], lane);
                     if (n0 == 0 && threadIdx.x == 0)
-                        *join = Join{pc.q0, pc.lq, kv_head, tile, share.owner(i_begin + all - 1), {}};
+                        join->set(pc, b0 + i, kv_head, tile, share.owner(i_begin + all - 1));
                 }
             }
         }
         base += __builtin_amdgcn_readlane(chunk.upto, 63);
+    }
+}
+
+// Row tile r of the items that workgroup `worker` of the first kernel had to itself once more, as
+// means: its units are counted as there, one sequence after the other.
+template <typename T, int N, int ROWS>
+__device__ __forceinline__ void means_of(const CacheArgs &a, int worker, int r, int lane)
+{
+    using Steps = Ladder<ROWS / kWaves>;
+    int units = 0;
+    for (int i = lane; i < a.batch; i += 64) {
+        const Steps l(a, piece_of(a, i));
+        units += l.before(l.tiles) * a.k_heads;
+    }
+    const Share share(wave_sum(units), a.workers);
+    const int u_begin = share.begin(worker), u_end = share.begin(worker + 1);
+    int base = 0;
+    for (int sequence = 0; sequence < a.batch && base < u_end; ++sequence) {
+        const Piece pc = piece_of(a, sequence);
+        const Steps l(a, pc);
+        for (int head = 0; head < a.k_heads; ++head) {
+            for (int i = 0; i < l.tiles && base + l.before(i + 1) <= u_end; ++i) {
+                if (base + l.before(i) < u_begin)
+                    continue;
+                const uint32_t tile = uint32_t(i) * ROWS + r;
+                const Row16 at(a, pc.q0, pc.lq, head, tile, lane);
+                const float lse = at.live ? a.lse[int64_t(at.head) * a.tokens + at.token] : 0.0f;
+                for (int b = 0; b < N; ++b)
+                    put_mean<T, N>(a, pc, sequence, head, tile, at, lse, b, lane);
+            }
+            base += l.before(l.tiles);
+        }
     }
 }
 
@@ -317,10 +355,13 @@ template <typename T, int N, int ROWS>
 __global__ __launch_bounds__(256) void cache_tile_join_kernel(CacheArgs a)
 {
     const Join j = reinterpret_cast<const Join *>(a.joins)[blockIdx.x];
-    if (j.last < 0)
-        return;
     const int lane = threadIdx.x & 63;
     const int r = int(blockIdx.y) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    if constexpr (!__is_same(T, half_t))
+        if (j.lost)
+            means_of<T, N, ROWS>(a, int(blockIdx.x), r, lane);
+    if (j.last < 0)
+        return;
     const float c = a.scale * kLog2e;
     const int first = int(blockIdx.x), end = min(j.last, a.workers - 1);
     auto part = [&](int i) {
@@ -338,7 +379,12 @@ __global__ __launch_bounds__(256) void cache_tile_join_kernel(CacheArgs a)
         st.merge(x, c);
         x = y;
     }
-    finish<T, 2 * N>(a, st, Row16(a, j.q0, j.lq, j.head, uint32_t(j.tile) * ROWS + r, lane), 0, lane);
+    const uint32_t tile = uint32_t(j.tile) * ROWS + r;
+    const Row16 at(a, j.q0, j.lq, j.head, tile, lane);
+    float lse;
+    if (finish<T, 2 * N>(a, st, at, 0, lane, lse))
+        for (int b = 0; b < N; ++b)
+            put_mean<T, N>(a, j.piece(), j.sequence, j.head, tile, at, lse, b, lane);
 }
 
 template <typename T, int N> hipError_t launch(const CacheArgs &a, hipStream_t s)

@@ -59,3 +59,91 @@ def test_a_million_queries_before_a_short_cache(dt, heads):
     ref = R.attend(q, rk, rv, [0, n], [0, n], None, True, att.scale, dtype)
     within(out[-n:], ref["out"], "out")
     within(lse[:, -n:], ref["lse"], "lse")
+
+
+# what values are: all at the largest one, of both signs, large ones behind a low first score
+LARGE = ["equal", "signs", "late"]
+
+
+@pytest.mark.parametrize("lens,new,causal", [
+    ([2], 1, False), ([40, 3], 1, True), ([3000, 1], 2, True),                 # few rows, joined parts
+    ([33, 64], 20, False), ([70, 5], 5, True),                                 # two row tiles
+    ([200, 70], 70, True), ([1500], 300, True), ([700], 150, False),           # many rows
+], ids=str)
+@pytest.mark.parametrize("kind", LARGE)
+@pytest.mark.parametrize("dim", [32, 96, 128])
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_sums_of_values_near_the_largest(dt, dim, kind, lens, new, causal):
+    """The mean of values that the format holds is within the type's range, and so is out; a block
+    of small values beside them stays exact."""
+    dtype, gen, heads = DTYPES[dt], torch.Generator().manual_seed(30), 2
+    hi = C.LIMITS[dtype][1]
+    n = sum(lens)
+    k, v = (normal(gen, n, heads, dim) for _ in range(2))
+    q = normal(gen, new * len(lens), 4, dim, dtype=dtype)
+    if kind == "late":                               # from token 32 on 7 bits above those before
+        q = torch.ones_like(q)
+        k = torch.zeros_like(k)
+        at = torch.cat([torch.arange(x) for x in lens])
+        k[at >= 32] = 1.0
+        v = v.clamp(-1, 1) * 2.0 ** (hi - 2)
+    else:                                            # infinities are held as the largest value
+        k *= 2.0 ** -6
+        v = torch.full_like(v, math.inf)
+        if kind == "signs":
+            v[torch.rand(v.shape, generator=gen) < 0.5] = -math.inf
+    if dim > 32:                                     # one block of small values
+        v[..., 32:64] = normal(gen, n, heads, 32) * 2.0 ** (C.LIMITS[dtype][0] + 12)
+    k, v = k.to(dtype), v.to(dtype)
+    op, pool, table, rk, rv = rounded_cache(k, v, lens, 16, dtype, gen)
+    scale = 7 * math.log(2) / dim if kind == "late" else None
+    att = A.mdcn_attention_create(4, heads, dim, causal, scale)
+    ends = [new * i for i in range(len(lens) + 1)]
+    out, lse = K.attend(att, op, q.cuda(), pool, table, ints(lens), ints(ends))
+    ref = R.attend(q, rk, rv, ends, cu(lens), None, causal, att.scale, dtype)
+    within(out, ref["out"], "out")
+    within(lse, ref["lse"], "lse")
+    again = K.attend(att, op, q.cuda(), pool, table, ints(lens), ints(ends))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("new", [1, 12, 60])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_some_of_many_sequences_hold_values_near_the_largest(dt, new):
+    """Among ordinary ones, with a page missing, and where a graph replays the call."""
+    dtype, gen, heads, dim, page, n = DTYPES[dt], torch.Generator().manual_seed(33), 2, 64, 16, 130
+    lens = [new + (37 * i) % 60 for i in range(n)]
+    k, v = (normal(gen, sum(lens), heads, dim) for _ in range(2))
+    for b in range(0, n, 3):
+        v[sum(lens[:b]):sum(lens[:b + 1]), b % 2, 32 * (b % 2):] = math.inf
+    k, v = k.to(dtype), v.to(dtype)
+    op, pool, table, rk, rv = rounded_cache(k, v, lens, page, dtype, gen)
+    table[3, 0] = -1                                  # row 3 begins with token 16
+    keys, values, held = [], [], []
+    for b in range(n):
+        s = slice(sum(lens[:b]) + (16 if b == 3 else 0), sum(lens[:b + 1]))
+        keys.append(rk[s])
+        values.append(rv[s])
+        held.append(max(lens[b] - 16, 0) if b == 3 else lens[b])
+    att = A.mdcn_attention_create(2, heads, dim, True)
+    ends = [new * i for i in range(n + 1)]
+    q = normal(gen, new * n, 2, dim, dtype=dtype)
+    ref = R.attend(q, torch.cat(keys), torch.cat(values), ends, cu(held), None, True, att.scale, dtype)
+    args = (q.cuda(), pool, table, ints(lens), ints(ends))
+    out, lse = K.attend(att, op, *args)
+    within(out, ref["out"], "out")
+    within(lse, ref["lse"], "lse")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        K.attend(att, op, *args)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = K.attend(att, op, *args)
+    for _ in range(3):
+        got[0].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+        assert torch.equal(K.attend(att, op, *args)[0], out)
