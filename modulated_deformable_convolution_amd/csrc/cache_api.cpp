@@ -16,6 +16,7 @@ using namespace mdcn;
 
 constexpr int64_t kMaxRowTokens = int64_t(1) << 30;      // of a row of a table
 constexpr int64_t kMaxPageStride = int64_t(1) << 40;     // bytes
+constexpr int64_t kMaxPoolBytes = int64_t(1) << 60;      // from a pool's first page to its last
 constexpr int64_t kMaxCacheStride = (int64_t(1) << 32) - 16;
 constexpr int64_t kMaxEntries = (int64_t(1) << 31) - 1;  // of a table, and pages of a pool
 
@@ -143,8 +144,9 @@ mdcn_status pool_view(int64_t layers, int64_t pages, int64_t bytes, int64_t page
 {
     if (layers < 0 || layers > (1 << 20) || pages < 0 || pages > kMaxEntries || bytes < 0 ||
         bytes > (int64_t(1) << 30) || page_stride < 0 || page_stride > kMaxPageStride ||
-        layer_stride < 0 || layer_stride > (int64_t(1) << 60) / (layers + 1) || bytes % 16 ||
-        page_stride % 16 || layer_stride % 16)
+        page_stride > kMaxPoolBytes / (pages + 1) || layer_stride < 0 ||
+        layer_stride > kMaxPoolBytes / (layers + 1) || bytes % 16 || page_stride % 16 ||
+        layer_stride % 16)
         return MDCN_E_SHAPE;
     // rows of bytes that do not overlap, pages within layers or layers within pages
     if ((pages > 1 && page_stride < bytes) || (layers > 1 && layer_stride < bytes))

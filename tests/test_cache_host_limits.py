@@ -8,7 +8,7 @@ from helpers import ensure_built
 from modulated_deformable_convolution_amd import attention as A
 from modulated_deformable_convolution_amd import cache as K
 from modulated_deformable_convolution_amd import mdcn
-from test_cache_host import attended, dims
+from test_cache_host import STEP, at, attended, dims
 
 ensure_built()
 
@@ -35,3 +35,19 @@ def test_more_work_than_31_bits_count(dtype, heads, batch, tokens, width, taken)
     assert lib.mdcn_describe_cache_attend(att.handle, op.handle, dtype, d, buf, 256) == want
     if not taken:
         assert attended(att.handle, op.handle, d, dtype) == want
+
+
+@pytest.mark.parametrize("pages,stride,taken", [
+    (1 << 24, 1 << 40, False), ((1 << 24) + 1, 1 << 40, False), ((1 << 31) - 1, 1 << 33, False),
+    ((1 << 31) - 1, 1 << 29, True), ((1 << 20) - 1, 1 << 40, True),
+])
+def test_pools_whose_bytes_64_bits_do_not_count(pages, stride, taken):
+    """Their extent decides what may overlap what."""
+    lib, n = mdcn.library(), ctypes.c_size_t()
+    want = mdcn.MDCN_OK if taken else mdcn.MDCN_E_SHAPE
+    fork, compact = [1, pages, 16, stride, 0, 16, 4, 6, 5], [1, pages, 16, stride, 0, 4, 5]
+    assert lib.mdcn_pages_fork_workspace_bytes(dims(fork), ctypes.byref(n)) == want
+    assert lib.mdcn_pages_compact_workspace_bytes(dims(compact), ctypes.byref(n)) == want
+    copy = dims([1, 7, 16, pages, stride, 0, 30, 16, 0])
+    st = lib.mdcn_pages_copy(copy, at(0), at(0) - STEP, at(0) - 2 * STEP, at(0) - 3 * STEP, None)
+    assert st == (mdcn.MDCN_E_DEVICE if taken else want)
