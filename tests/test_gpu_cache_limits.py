@@ -147,3 +147,27 @@ def test_some_of_many_sequences_hold_values_near_the_largest(dt, new):
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], lse)
         assert torch.equal(K.attend(att, op, *args)[0], out)
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_values_near_the_largest_leave_the_other_rows_as_they_were(dt, new):
+    """Bit for bit, where their scores are very large too."""
+    dtype, gen, heads, dim, page, n = DTYPES[dt], torch.Generator().manual_seed(34), 2, 32, 16, 40
+    size = 2.0 ** (60 if dt == "f32" else 12)
+    lens = [new + (37 * i) % 60 for i in range(n)]
+    k, v = (normal(gen, sum(lens), heads, dim) for _ in range(2))
+    k[-lens[-1]:] *= size                             # of the last one
+    large = v.clone()
+    large[:lens[0]] = math.inf
+    q = normal(gen, new * n, 2, dim, dtype=dtype)
+    q[-new:] *= size
+    att, got = A.mdcn_attention_create(2, heads, dim, True), []
+    for x in (v, large):
+        op, pool, table, _, _ = rounded_cache(k.to(dtype), x.to(dtype), lens, page, dtype,
+                                              torch.Generator().manual_seed(1))
+        got.append(K.attend(att, op, q.cuda(), pool, table, ints(lens), ints([new * i for i in range(n + 1)])))
+    top = float(C.rounded(large[:1, :, :1].to(dtype), dtype).max())
+    assert torch.equal(got[0][0][new:], got[1][0][new:]) and torch.equal(got[0][1], got[1][1])
+    assert float((got[1][0][:new].double().cpu() / top - 1).abs().max()) <= 2 * R.unit(dtype) + 40 * R.E32 * lens[0]
+    assert bool(got[0][0].isfinite().all())
