@@ -490,7 +490,8 @@ mdcn_status mdcn_cache_load(const mdcn_cache *op, mdcn_dtype dtype, const int64_
  * tokens is never used.  fill, the row that sees no key, rows of no sequence and lse are as for
  * mdcn_attend_filled.  Keys and values are exact in the products; queries are too (fp32
  * ones as three bf16 parts: beyond 3.39e38 NaN), probabilities are rounded to the inputs' type
- * (fp32: to three bf16 parts, 2^-24).  The same bits in every call.
+ * (fp32: to three bf16 parts, 2^-24).  In 16-bit types scores times scale must stay below 10^9,
+ * past which rows may become NaN or zeros.  The same bits in every call.
  * Errors as for mdcn_attend; MDCN_E_SHAPE also for batches of more than about 1.5 * 10^8 items
  * of work (up to 16 to 128 rows of one sequence and key head each), which are counted in 31 bits. */
 mdcn_status mdcn_cache_attend_workspace_bytes(const mdcn_attention *att, const mdcn_cache *op,
@@ -524,6 +525,8 @@ mdcn_status mdcn_describe_cache_attend(const mdcn_attention *att, const mdcn_cac
  *   table: a new, empty sequence.  new_tokens: int32 or NULL (none); below 0 counts as 0.
  * Full pages are shared.  Of the rows with one parent the first one keeps a last page
  * that is full in part; each other gets a copy of it in a page of its own, in every layer.
+ * (A row whose used tokens are cut back into a page that other rows name too keeps it like any
+ * other, and what it stores there next is theirs as well: such a page is for the caller to copy.)
  * Pages for the new tokens follow.  Old rows that nobody goes on from, and entries beyond
  * their used tokens, give their pages up; those that nothing holds then are free, and the
  * lowest free pages are taken, in the order of rows and tokens; their count becomes 1.

@@ -269,7 +269,8 @@ def fork_pages(pool, table, used, owners, page: int, parents=None, new_tokens=No
     the table: empty) with room for new_tokens[i] more (None: none).  Full pages are shared, pages
     full in part copied for all children but the first, rows that nobody goes on from give theirs
     up.  Returns (table, used, owners, missing): missing int32 [1] is 0, or how many pages there
-    are too few, and then nothing was copied and the old table still holds."""
+    are too few, and then nothing was copied and the old table still holds.  Results that are not
+    given are parts of one allocation: clone one that is to be saved or kept by itself."""
     where = "fork_pages"
     lib = _m._lib or _m.library()
     key = (where, None if pool is None else _sig(pool), _sig(table), _sig(used), _sig(owners), page,
@@ -316,7 +317,8 @@ def fork_pages(pool, table, used, owners, page: int, parents=None, new_tokens=No
 def compact_pages(pool, table, owners, table_out=None, owners_out=None, moved=None, workspace=None,
                   stream=None):
     """Moves the n held pages to the numbers 0 .. n - 1.  Returns (table, owners, moved) with
-    the new numbers; moved int32 [pages]: the new number of each page, -1 if it is free."""
+    the new numbers, parts of one allocation as fork_pages' are; moved int32 [pages]: the new
+    number of each page, -1 if it is free."""
     where = "compact_pages"
     lib = _m._lib or _m.library()
     key = (where, _sig(pool), _sig(table), _sig(owners))

@@ -10,7 +10,7 @@
 //
 // One MI355X, 32 query and 8 key heads of 128, pages of 16: 48 caches of 1 to 16384 tokens in
 // bf16 82 to 85 us (384 MB; 430 past the L2s with the parts, 5.2 TB/s; strips alone read in this order
-// reach 5.9) and 5 to join.  Taking the conversions, the exponentials or both away leaves that time
+// reach 5.9) and 6 to join, 91 a call.  Taking the conversions, the exponentials or both away leaves that time
 // as it is, pages that stay in the L2s halve it: memory bounds it.  Older waves are served
 // first and end after half of the time; shares to match, priorities or smaller shares gained
 // nothing.  One cache of 4097 tokens in fp16: 8.4 us and 5, round trips to memory.
@@ -27,8 +27,8 @@ constexpr int kTile = 32;                        // tokens
 
 // Waves a SIMD that the registers leave room for: a row tile of 16-bit queries with its sums
 // takes 48 of 128 of them, a second one or the three parts of fp32 as much again.  More
-// workgroups than run together, of less work each, were slower (98 us for 1536 and 2048
-// against 92 for 1024 in the case below).
+// workgroups than run together, of less work each, are slower: calls on the 48 caches above take 97
+// and 95 us with 1536 and 2048, 91 with 1024; on 400 of 1 to 200 tokens 46 and 51, 38 with 1024.
 template <typename T, int N, int R> constexpr int row_waves()
 {
     return R > 1 ? 2 : sizeof(T) == 4 ? 3 : 4;
@@ -63,11 +63,13 @@ struct Units {
     int tiles, keys, all;
 };
 
-// Measured: 48 caches of 1 to 16384 tokens, 32/8 heads of 128 in bf16, with 0 / 10 / 20: 112, 99
-// and 103 us.
+// Calls with 0 / 5 / 10 / 20, 32/8 heads of 128 in bf16: 48 caches of 1 to 16384 tokens 101, 93, 91 and
+// 92 us, 48 of 512 23, 22, 23 and 24; where caches are alike 0 is as good or better: 16 of 4096
+// tokens 29, 30, 30 and 32, 400 of 1 to 200 36, 37, 38 and 38.
 constexpr int kItemCost = 10;
 // Tiles up to which one wave takes an item alone, without the others and their barriers.
-// With 0 / 3 / 8 these caches take 100, 99 and 103 us, 400 of 1 to 200 tokens 42, 39 and 33.
+// Calls with 0 / 3 / 8: the 48 caches 91, 91 and 93 us, 16 of 4096 tokens 30 each, 400 of 1 to 200
+// 40, 38 and 31: more suits short caches, and costs long ones their balance.
 constexpr int kAlone = 3;
 
 template <int R> __device__ __forceinline__ Units units_of(const CacheArgs &a, const Piece &p)
@@ -428,11 +430,11 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs a)
 
 // Row tiles of an item, by the rows of an average sequence: one (fp32: of up to 64 rows) or
 // two in the split kernel, which reads keys and values again for each item, kWaves or twice
-// as many in the tile kernel.  Measured in us, 16 sequences of 4096 tokens (fp32: 2048), 32 query
-// and 8 key heads of 128, with one row tile / two / the tile kernel:
+// as many in the tile kernel.  Calls in us, 16 sequences of 4096 tokens (fp32: 2048), 32 query
+// and 8 key heads of 128, with one row tile / two (fp32 has one only) / the tile kernel:
 //   rows   16          20          32          48          64          128
-//   bf16   32 36 64    42 38 64    41 38 64    53 49 69    61 50 70    99 70 76
-//   fp32   25 39 43    32 41 47    33 42 48    43 53 50    49 52 52    79 68 76
+//   bf16   31 34 64    39 35 64    39 35 64    50 47 69    59 47 69    93 65 74
+//   fp32   23    41    30    45    30    46    41    47    47    48    74    71
 int row_tiles(mdcn_dtype dtype, const CacheArgs &a)
 {
     const bool f32 = dtype == MDCN_F32;

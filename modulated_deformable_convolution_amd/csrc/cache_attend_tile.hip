@@ -8,11 +8,12 @@
 // an item see under the causal mask, is cut into equal contiguous ranges, one per
 // workgroup; an item that several share goes to the workspace in parts.
 //
-// One MI355X, 32 query and 8 key heads of 128 in bf16: six pieces of 2048 to 1 queries behind
-// 8192 to 1 tokens 290 us and 14 to join (a product of 8192^3 in that many operations 193); 45 us
-// of it go with the conversions, 34 with the exponentials.  LDS reads of operands are at 85 % of
+// One MI355X, 32 query and 8 key heads of 128 in bf16: a call on six pieces of 2048 to 1 queries behind
+// 8192 to 1 tokens 302 us, 14 of them to join (a product of 8192^3 in that many operations 193); 45 us
+// go with the conversions, 34 with the exponentials.  LDS reads of operands are at 85 % of
 // the vector units' time: 32 rows a wave, as 64 leave one wave a SIMD (1085 us when each wave
-// converted for itself).  768, 1024 and 2048 workgroups took 350, 320 and 344 us.
+// converted for itself).  With 768, 1024 and 2048 workgroups instead of 512 the
+// call takes 349, 310 and 335 us, one on 4096 queries of one prompt 239, 212 and 249 instead of 195.
 #include "cache_attend.h"
 
 namespace mdcn {
@@ -20,8 +21,9 @@ namespace mdcn {
 namespace {
 
 constexpr int kRound = 64;                       // tokens
-// Units that an item costs beside its tokens': with 0 / 3 / 8, six pieces of 2048 to 1 queries
-// behind 8192 to 1 tokens, 32/8 heads of 128 in bf16, took 356, 315 and 325 us.
+// Units that an item costs beside its tokens': with 0 / 3 / 8 the call above takes 357, 302 and 310 us,
+// 4096 queries of one prompt 250, 195 and 207, 8 pieces of 300 to 650 queries behind 400 to 750
+// tokens 106, 104 and 113.
 constexpr int kItemCost = 3;
 
 // Units of the items of one (sequence, key head), item i being rows 16 kWaves R i and on:

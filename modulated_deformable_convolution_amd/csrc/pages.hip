@@ -69,8 +69,10 @@ __host__ __device__ __forceinline__ int segments_of(int page_bytes)
 
 // Page src[i] to dst[i] in every layer, i < count (or *counter, if there is one); the
 // segments of a page are alike.  Past the caches, a turn a workgroup: 601 pages of 34 KB in 12
-// layers 92 us (5.5 TB/s read and written; a large copy 4.9), through the caches or with
-// 4096 workgroups of several turns 102, both 106.
+// layers 92 us (5.5 TB/s read and written, part of it from the last-level cache: 4 GiB of such pages
+// in any order 4.8), through the caches or with 4096 workgroups of several turns 102, both 106.
+// A page is a workgroup's turn however small: 1 GiB in pages of 4352 bytes at 4.9 TB/s, of 2176 at 3.7, of
+// 1088 at 2.3, of 544 at 1.3.
 __global__ __launch_bounds__(256) void copy_pages_kernel(PoolView from, PoolView to,
                                                          const int32_t *src, const int32_t *dst,
                                                          int count, const int32_t *counter)
@@ -312,8 +314,11 @@ __device__ void fork_take(const PagesArgs &a, const ForkState &f, const Team &t)
 }
 
 // Rows, pages and entries up to which one workgroup does all steps, with what they count in
-// LDS.  Forking 32 rows of 33 pages took 9 us that way and 21 as steps of their own kernels,
-// 512 rows of 20 pages 21 and 23; compacting 512 pages 8 and 13, 4096 11 and 16, 16000 30 and 20.
+// LDS.  Forking 32 rows of 33 pages takes 6 us that way and 17 as steps of their own kernels,
+// 512 rows of 20 14 and 19, 1024 of 16 18 and 20; compacting 512 pages 4 and 9, 4096 7 and 11, 8192
+// 11 and 12, 16000 23 and 12.  The entries' bound is generous: at 32768 the steps are the
+// faster ones, 24 and 20 us forking 1000 rows of 32 pages, 31 and 22 forking 2048 of 16, 16 and 11
+// compacting.
 constexpr int kSmallRows = 2048, kSmallPages = 8192, kSmallEntries = 32768;
 
 struct ForkLds {
