@@ -490,8 +490,8 @@ mdcn_status mdcn_cache_load(const mdcn_cache *op, mdcn_dtype dtype, const int64_
  * tokens is never used.  fill, the row that sees no key, rows of no sequence and lse are as for
  * mdcn_attend_filled.  Keys and values are exact in the products; queries are too (fp32
  * ones as three bf16 parts: beyond 3.39e38 NaN), probabilities are rounded to the inputs' type
- * (fp32: to three bf16 parts, 2^-24).  In 16-bit types scores times scale must stay below 10^9,
- * past which rows may become NaN or zeros.  The same bits in every call.
+ * (fp32: to three bf16 parts, 2^-24).  Scores times scale must stay below 10^7 in fp16 and 10^9
+ * in bf16, past which rows may become NaN or zeros.  The same bits in every call.
  * Errors as for mdcn_attend; MDCN_E_SHAPE also for batches of more than about 1.5 * 10^8 items
  * of work (up to 16 to 128 rows of one sequence and key head each), which are counted in 31 bits. */
 mdcn_status mdcn_cache_attend_workspace_bytes(const mdcn_attention *att, const mdcn_cache *op,

@@ -171,3 +171,24 @@ def test_values_near_the_largest_leave_the_other_rows_as_they_were(dt, new):
     assert torch.equal(got[0][0][new:], got[1][0][new:]) and torch.equal(got[0][1], got[1][1])
     assert float((got[1][0][:new].double().cpu() / top - 1).abs().max()) <= 2 * R.unit(dtype) + 40 * R.E32 * lens[0]
     assert bool(got[0][0].isfinite().all())
+
+
+@pytest.mark.parametrize("new", [1, 12, 60])
+@pytest.mark.parametrize("dt,size", [("f16", 9.9e6), ("bf16", 9.9e8), ("f32", 1e30)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores(dt, size, new, sign):
+    """Equal scores of the largest size that is allowed: rows are means of what they see.  Weights are
+    rounded once (u), and so is out; sums of n values are off by n 2^-24."""
+    dtype, gen, heads, dim, page, n = DTYPES[dt], torch.Generator().manual_seed(35), 2, 64, 16, 150
+    v = normal(gen, n, heads, dim, dtype=dtype)
+    q, k = torch.full((new, 4, dim), 4.0 * sign, dtype=dtype), torch.full((n, heads, dim), 4.0, dtype=dtype)
+    op, pool, table, _, rv = rounded_cache(k, v, [n], page, dtype, gen)
+    att = A.mdcn_attention_create(4, heads, dim, True, size / (16 * dim))
+    out, lse = K.attend(att, op, q.cuda(), pool, table, ints([n]), ints([0, new]))
+    rv = rv.repeat_interleave(2, 1)
+    for i in range(new):
+        see = rv[:n - new + i + 1]
+        bound = R.unit(dtype) * see.mean(0).abs() + (R.unit(dtype) + (n + 16) * R.E32) * see.abs().mean(0)
+        within(out[i], (see.mean(0), bound + R.tiny(dtype)), "out")
+    seen = torch.arange(n - new + 1, n + 1).double().log()
+    within(lse, ((sign * size + seen).expand(4, new), torch.tensor(8 * R.E32 * size)), "lse")
