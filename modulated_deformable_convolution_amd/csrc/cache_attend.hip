@@ -507,7 +507,7 @@ bool cache_attend_countable(mdcn_dtype dtype, const CacheArgs &a)
     const CacheShape c = cache_attend_shape(dtype, a);
     const int tiles = c.rows / 16;
     const int shift = __builtin_ctz(unsigned(c.unit / (tiles > 2 ? 64 : kTile)));
-    return most_units(a, tiles, shift, std::min(a.batch, a.tokens)) <= 2e9;
+    return a.batch == 0 || most_units(a, tiles, shift, std::min(a.batch, a.tokens)) <= 2e9;
 }
 
 size_t cache_attend_bytes(mdcn_dtype dtype, const CacheArgs &a)

@@ -25,6 +25,7 @@ ensure_built()
     (65536, 1, 1 << 20, 1, False),                   # many rows of one sequence
     (64, 1, 1 << 29, 1, False),
     (64, 1, 1 << 24, 1, True),
+    (64, 0, 1 << 29, 1, True),                       # tokens of no sequence
 ])
 def test_more_work_than_31_bits_count(dtype, heads, batch, tokens, width, taken):
     att, op = A.mdcn_attention_create(heads, heads, 8, True), K.mdcn_cache_create(heads, 8, 16)
